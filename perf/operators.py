@@ -196,8 +196,8 @@ def _cache(case, layers, held, spare, g):
         for at in range(0, n_pages, 16384):
             x = torch.randn(min(16384, n_pages - at), PAGE, d, device="cuda", generator=g)
             e = _exponent(x.abs().amax((1, 2)))
-            codes[i, at:at + 16384] = torch.ldexp(x, -e[:, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
-            scales[i, at:at + 16384] = torch.ldexp(torch.ones_like(e, dtype=torch.float32), e)
+            codes[i, at:at + 16384] = (x * _power(-e)[:, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+            scales[i, at:at + 16384] = _power(e)
     order = torch.randperm(n_pages, device="cuda", generator=g).to(torch.int32)
     table = torch.zeros(case["bs"], width, dtype=torch.int32, device="cuda")
     at = torch.arange(width, device="cuda")[None]
@@ -300,6 +300,11 @@ def _exponent(amax):
     return torch.where(amax > 0, e, -EMAX).clamp(-EMAX, EMAX)
 
 
+def _power(e):
+    """2^e in 32 bits, from its exponent field."""
+    return ((e + 127) << 23).to(torch.int32).view(torch.float32)
+
+
 def _plan(state):
     length, want, table, ring = state["length"].long(), state["want"].long(), state["table"], state["ring"]
     n_pages, width, room, spans = ring.shape[0], table.shape[1], state["room"], state["spans"]
@@ -362,12 +367,12 @@ def _append(state):
         _, e_old = torch.frexp(scales[:, pages])
         e = torch.maximum(_exponent(amax), torch.where(old > 0, e_old - 1, -EMAX))
         held = codes[:, pages].view(torch.float8_e4m3fn).float()
-        kept = torch.ldexp(held, (e_old - 1 - e)[:, :, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+        kept = (held * _power(e_old - 1 - e)[:, :, None, None]).to(torch.float8_e4m3fn).view(torch.uint8)
         keep = (torch.arange(PAGE, device=x.device) < old[:, None])[None, :, :, None]
         codes[:, pages] = torch.where(keep, kept, codes[:, pages])
-        fresh = torch.ldexp(x, -e[:, span][:, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
+        fresh = (x * _power(-e)[:, span][:, :, None]).to(torch.float8_e4m3fn).view(torch.uint8)
         codes.view(layers, -1, d)[:, slots] = fresh
-        scales[:, pages] = torch.ldexp(torch.ones_like(amax), e)
+        scales[:, pages] = _power(e)
     return {"codes": codes.view(torch.float8_e4m3fn), "scales": scales}
 
 
@@ -419,10 +424,11 @@ def exact(case, seed):
         held = torch.stack([value[c.int()] for c in state["codes"]])
         scales, entries = state["scales"].double().cpu(), state["entries"].double()
         slots, rows = state["slots"].tolist(), state["seg_row"].tolist()
+        steps = torch.tensor([2.0 ** (k - 9) for k in range(15)], dtype=torch.float64, device="cuda")
 
         def rounded(x):
             """To the nearest E4M3 value, halves to the even one."""
-            step = torch.ldexp(torch.ones_like(x), (torch.frexp(x)[1] - 1).clamp(min=-6) - 3)
+            step = steps[(torch.frexp(x)[1] - 1).clamp(min=-6, max=8) + 6]
             return torch.round(x / step) * step
         for layer in range(held.shape[0]):
             tops = entries[layer].abs().amax(1).tolist()
