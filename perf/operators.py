@@ -271,8 +271,7 @@ def _own_cache(state):
     if case["op"] == "plan":
         return M.QCache(512, 64, codes=(), scales=(), page_table=state["table"], n_pages=state["ring"].shape[0])
     return M.QCache(case["kv_lora"], case["d_rope"], codes=list(state["codes"]), scales=list(state["scales"]),
-                    page_table=state["table"], n_heads=case.get("heads", 0),
-                    max_queries=state["q"].shape[0] if "q" in state else 0, max_bs=case["bs"])
+                    page_table=state["table"], n_heads=case.get("heads", 0))
 
 
 def _run_own(state):
