@@ -31,7 +31,7 @@
  *    workspace must be zero-filled again. Bytes 72..79 of the workspace hold
  *    an optional limit, in nanoseconds (uint64), on the waits of the rollout's
  *    and verification's CTAs for one another; 0 (the zero fill) means 2 s.
- *  - Batch size bs is 1..32 for every call.
+ *  - Batch size bs is 1..32 for every call but those of the 8-bit latent cache.
  */
 #ifndef DSPARK_H
 #define DSPARK_H
@@ -272,6 +272,118 @@ dspark_status dspark_kv_append(dspark_handle_t *h, const float *x_new, int n_max
  * dspark_check(h, NULL, stream) reads and clears it. Allocates nothing.
  * aux bf16 [bs, block, n_aux, hidden]; x fp32 [bs, block, hidden] (overwritten). */
 dspark_status dspark_fuse_ctx_noalloc(dspark_handle_t *h, const void *aux, float *x, int bs, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit latent cache: page plan, quantising append, attention.
+ *
+ * A paged latent cache like dspark_kv_t's, with E4M3 codes and one scale per
+ * page (64 tokens; every head shares the one latent, so a page has one scale):
+ * element = code * scale. Scales are powers of two, 2^-60 .. 2^60, so that
+ * raising a page's scale moves its codes by whole binades. The calls need no
+ * handle; the sizes are in the struct. They use the error word at the start of
+ * the workspace (zero-filled once, as above); read it with
+ * dspark_qcache_check(). Batch size bs is 1..1024 for these calls.
+ */
+typedef struct {
+    int kv_lora, d_rope;              /* one of (512, 64), (256, 32), (128, 32), (64, 16) */
+    int page_size;                    /* 64 */
+    int n_layers;                     /* 0..DSPARK_MAX_LAYERS (0: a struct for dspark_qcache_plan only) */
+    void *codes[DSPARK_MAX_LAYERS];   /* device, E4M3 [n_pages, 64, kv_lora + d_rope] */
+    float *scales[DSPARK_MAX_LAYERS]; /* device, fp32 [n_pages] */
+    int n_pages;                      /* < 2^25 */
+    int32_t *page_table;              /* device int32 [bs, max_pages] */
+    int max_pages;                    /* < 2^25 */
+} dspark_qcache_t;
+
+/* Arguments of dspark_qcache_plan (device pointers). */
+typedef struct {
+    const int32_t *length;      /* [bs] tokens that each request holds */
+    const int32_t *want;        /* [bs] tokens that it is to hold: more, fewer or as many */
+    int32_t *ring;              /* [n_pages] ring of free pages */
+    const int32_t *ring_state;  /* [2] position of the ring's first free page, number of free pages */
+    int32_t *length_out;        /* [bs] tokens that each request holds afterwards */
+    int32_t *ring_state_out;    /* [2] */
+    int32_t *cu_new;            /* [bs + 1] running sum of the new tokens */
+    int32_t *slots;             /* [max_new] page * 64 + offset of every new token, then -1 */
+    int32_t *positions;         /* [max_new] position of every new token in its request, then -1 */
+    int32_t *seg_row;           /* [max_seg + 1] first new token of every page that new tokens touch, then their number */
+} dspark_qplan_t;
+
+/* (7) Page plan: page tables and slot maps from the requests' lengths, on the
+ * device. In request order: a request that grows takes pages from the front of
+ * the ring for the pages it lacks, its page-table entries are written, and its
+ * new tokens are listed; a request that shrinks (0: it ends) gives its last
+ * pages back to the end of the ring. A request that grows is served only if it
+ * and all growing requests before it fit into the free pages, max_new and
+ * max_seg; one that is not keeps its length (length_out) and is no error.
+ * Pages given back in a call serve later calls. Inputs stay as they are but
+ * for the page table (entries of new pages) and the ring (pages given back):
+ * the same call again gives the same results; pass length_out and
+ * ring_state_out to the next call. The outputs may not alias the inputs.
+ * max_new 0..2^30 (then slots and positions may be null), max_seg likewise >= 0.
+ * Device errors (DSPARK_ERR_OOB): a length or want outside [0, 64 max_pages]
+ * (that request stays as it is), ring_state outside the ring (no page is
+ * taken), more pages than the ring holds given back (the rest is dropped), a
+ * page number outside [0, n_pages) in the ring (its tokens get slot -1). */
+dspark_status dspark_qcache_plan(const dspark_qcache_t *c, const dspark_qplan_t *p, int bs, int max_new, int max_seg,
+                                 void *ws, size_t ws_bytes, void *stream);
+
+enum { DSPARK_ENTRY_BF16 = 0, DSPARK_ENTRY_FP32 = 1 };
+
+/* (8) Quantising append, every layer at once: row i of a layer's entries
+ * [rows, kv_lora + d_rope] goes to slots[i]; rows seg_row[s] .. seg_row[s+1]-1
+ * lie in one page, in order (dspark_qcache_plan's slots and seg_row). The
+ * page's scale becomes the least power of two 2^e, -60 <= e <= 60, with
+ * amax <= 448 * 2^e over its new rows, or its present scale if that is larger
+ * and the page holds tokens before the first new one; the codes of those are
+ * then moved to the new scale. Rounding is to nearest even, saturating.
+ * Rows with slot -1 are skipped. row_stride and layer_stride count elements
+ * (multiples of 8 for bf16, 4 for fp32; layer_stride is unused for one layer).
+ * Device errors: DSPARK_ERR_OOB for a slot or row outside its range
+ * (that page's rows are not written), DSPARK_ERR_BAD_INPUT for an element that
+ * is not finite or above 448 * 2^60 (NaN is stored as 0, the others as +-448)
+ * or a held page's scale that is no power of two in range. */
+dspark_status dspark_qcache_append(const dspark_qcache_t *c, const void *entries, int entry_type, int64_t row_stride,
+                                   int64_t layer_stride, const int32_t *slots, int rows, const int32_t *seg_row,
+                                   int n_seg, void *ws, size_t ws_bytes, void *stream);
+
+/* Arguments of dspark_qcache_attend. */
+typedef struct {
+    const void *q;          /* bf16 [total_q, n_heads, kv_lora + d_rope], absorbed and roped; heads contiguous */
+    int64_t q_stride;       /* elements from one query token to the next (a multiple of 8) */
+    const int32_t *cu_q;    /* device int32 [bs + 1]: request b's queries are cu_q[b] .. cu_q[b+1]-1 */
+    const int32_t *length;  /* device int32 [bs]: cached tokens, the queries' own included where causal */
+    int n_heads;            /* 1..1024 */
+    int total_q;            /* rows of q: host bound on cu_q[bs] */
+    int causal;             /* 0: every query sees tokens 0..length-1; 1: query i of n sees 0..length-n+i */
+    float scale;            /* softmax scale, > 0 */
+    void *o;                /* bf16 [total_q, n_heads, kv_lora] */
+    int64_t o_stride;       /* elements from one token to the next (a multiple of 8) */
+    float *lse;             /* fp32 [total_q, n_heads] natural log of the sum of exp(scores), or null */
+} dspark_qattn_t;
+
+/* (9) Attention over one layer of the 8-bit cache, from one token per request
+ * (decode) over a drafted block to a chunk of a prompt:
+ *   o = softmax(scale * q k^T) v,  k = the cached entry, v = its first kv_lora elements.
+ * A query that sees no token gives o = 0 and lse = -inf. Scores, maxima and
+ * sums are fp32; q enters to the full bf16 (elements below 2^-17 of their
+ * row's largest lose low bits), the softmax weights with at least 8
+ * significant bits. Cached elements must be finite (the append writes no
+ * other); entries past a request's length are never used. The workspace holds
+ * split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of
+ * range (those requests' queries are skipped) or a page number out of range
+ * (read as page 0), DSPARK_ERR_BAD_INPUT for a non-finite query (its row's
+ * outputs are NaN) or a scale that is no power of two in range,
+ * DSPARK_ERR_TIMEOUT. */
+dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const dspark_qattn_t *a, int bs, void *ws,
+                                   size_t ws_bytes, void *stream);
+
+/* Workspace bytes of the three calls; max_heads 0: of plan and append alone.
+ * 0 if an argument is out of range. */
+size_t dspark_qcache_workspace_bytes(const dspark_qcache_t *c, int max_heads);
+
+/* Synchronise the stream, return and clear the error word. */
+dspark_status dspark_qcache_check(void *ws, void *stream);
 
 /* Synchronise the stream, return and clear the device error word
  * (DSPARK_OK if no kernel recorded an error since the last check). With

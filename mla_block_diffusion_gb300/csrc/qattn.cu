@@ -1,0 +1,381 @@
+// Attention over the 8-bit latent cache (include/dspark.h, call 9): the kernel
+// for every latent width, and the combine of split items.
+#include <math.h>
+
+#include "e4m3.cuh"
+#include "qattn.cuh"
+
+namespace ds {
+
+DS_DEVINL void ldsm4(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+DS_DEVINL void ldsm4t(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(smem_u32(p)));
+}
+DS_DEVINL void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+DS_DEVINL float qa_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------------------
+// Every width, mma.sync m16n8k16 in f16.
+//
+// A CTA of 8 warps holds 64 query rows: warp (w & 3) 16 of them, w >> 2 one half
+// of the output columns (both halves compute the scores of their rows). E4M3
+// codes are exact in f16; a query row is scaled by a power of two so that its
+// largest magnitude lies in [2^7, 2^8), where a bf16 significand is exact in
+// f16 down to 2^-22 of it. Online softmax in the log2 domain: the weight that
+// meets a code is w = 2^(s + e - m) with e the page scale's exponent and m the
+// row's running maximum of s + e, so that codes are used as they are; the row
+// sum adds w * 2^-e. Weights are rounded to f16 (2^-12), sums are fp32.
+// ---------------------------------------------------------------------------
+template <int D, int DV>
+struct QgCfg {
+    static constexpr int kThreads = 256;
+    static constexpr int kRow = D * 2 + 16;                 // bytes per shared row: an odd number of 16-byte pieces
+    static constexpr int kSmem = (64 + kQcPage) * kRow + 64 * 8 + 1024;
+    static constexpr int kPieces = kQcPage * D / 16;        // 16-byte pieces of a page
+    static constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
+    static_assert((kRow / 16) % 2 == 1, "conflict-free row stride");
+    static_assert(kSmem >= QaWork<64, 64>::kScratch, "scratch of the work division");
+};
+
+template <int D, int DV>
+__global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const QaParams p) {
+    using C = QgCfg<D, DV>;
+    using W = QaWork<kQaTile, kQcPage>;
+    extern __shared__ __align__(16) uint8_t qg_smem[];
+    uint8_t *sQ = qg_smem, *sK = sQ + 64 * C::kRow;
+    float *s_c = (float *)(sK + kQcPage * C::kRow);  // score factor of every row (NaN: a non-finite query)
+    int *s_lim = (int *)(s_c + 64);                  // tokens every row sees
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = warp & 3, half = warp >> 2;
+    const int cta = blockIdx.x, grid = gridDim.x;
+    constexpr int NV = DV / 2 / 8;                   // output column tiles of a warp
+
+    pdl_trigger();
+    pdl_wait();
+    W wk;
+    wk.find(p, cta, grid, qg_smem);
+    long long left = wk.end - wk.begin, unit = wk.begin;
+    QaSplit sp;
+    sp.b = sp.t = sp.lo_slot = 0;
+    sp.c_hi = -1;
+    int slot = 2 * cta;
+    for (; left > 0; slot = 2 * cta + 1) {
+        const QaItem it = wk.item;
+        const int take = (int)min((long long)(it.chunks - wk.off), left);
+        const bool first = wk.off == 0, whole = first && take == it.chunks;
+        if (first && !whole) {
+            sp.b = it.b;
+            sp.t = it.t;
+            sp.lo_slot = slot;
+            sp.c_hi = wk.owner(unit + it.chunks - 1);
+        }
+        const int r0 = it.t * kQaTile, R = it.nq * p.H;
+        __syncthreads();
+        // query rows as f16
+        for (int r = warp; r < 64; r += 8) {
+            const bool in = r0 + r < R;
+            const int tok = in ? (r0 + r) / p.H : 0, hd = in ? (r0 + r) % p.H : 0;
+            const __nv_bfloat16 *src = p.q + (size_t)(it.q0 + tok) * p.q_stride + (size_t)hd * D;
+            uint32_t mx = 0;
+            uint4 v[(D / 8 + 31) / 32];
+#pragma unroll
+            for (int j = 0; j < (D / 8 + 31) / 32; ++j) {
+                const int k = lane + 32 * j;
+                v[j] = in && k < D / 8 ? __ldg((const uint4 *)src + k) : make_uint4(0, 0, 0, 0);
+                const uint32_t *u = (const uint32_t *)&v[j];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mx = max(mx, max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+            }
+            mx = __reduce_max_sync(~0u, mx);
+            const bool bad = mx >= 0x7f800000u;
+            // 2^a times the largest magnitude lies in [2^7, 2^8)
+            int a = mx < 0x00800000u ? 0 : 7 - ((int)(mx >> 23) - 127);
+            a = min(a, 100);
+            const float f = qc_pow2(a);
+#pragma unroll
+            for (int j = 0; j < (D / 8 + 31) / 32; ++j) {
+                const int k = lane + 32 * j;
+                if (k < D / 8) {
+                    const uint32_t *u = (const uint32_t *)&v[j];
+                    uint32_t h[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        h[i] = bad ? 0u : f32x2_to_f16x2(__uint_as_float(u[i] << 16) * f, __uint_as_float(u[i] & 0xffff0000u) * f);
+                    *(uint4 *)(sQ + r * C::kRow + k * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+            }
+            if (lane == 0) {
+                s_c[r] = bad ? __uint_as_float(0x7fffffffu) : qc_pow2(-a) * p.scale_log2;
+                s_lim[r] = in ? W::sees(p, it.nq, it.len, tok) : 0;
+                if (bad && first) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+            }
+        }
+        float oacc[NV][4];
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) oacc[i][j] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        // pages: raw codes into registers one page ahead, decoded into shared memory
+        uint4 raw[C::kPer];
+        int e_next = 0;
+        auto load = [&](int c) {
+            const int n = it.len;
+            if (c * kQcPage >= n) return;  // nothing cached: the unit only writes its outputs
+            int pg = p.page_table[(size_t)it.b * p.max_pages + c];
+            if (pg < 0 || pg >= p.n_pages) {
+                if (tid == 0) set_error(p.err, DSPARK_ERR_OOB);
+                pg = 0;
+            }
+            if (!qc_scale_exponent(p.scales[pg], &e_next) && tid == 0) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+            const uint4 *src = (const uint4 *)(p.codes + (size_t)pg * kQcPage * D);
+            const int used = min(kQcPage, n - c * kQcPage) * (D / 16);  // pieces of cached tokens
+#pragma unroll
+            for (int j = 0; j < C::kPer; ++j) {
+                const int i = tid + j * C::kThreads;
+                raw[j] = i < used ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+            }
+        };
+        load(wk.off);
+        for (int c = wk.off; c < wk.off + take; ++c) {
+            const int base = c * kQcPage;
+            const int e = e_next;
+            __syncthreads();  // the page before has been read
+            if (base < it.len) {
+#pragma unroll
+                for (int j = 0; j < C::kPer; ++j) {
+                    const int i = tid + j * C::kThreads;
+                    if (i < C::kPieces) {
+                        const uint32_t *u = (const uint32_t *)&raw[j];
+                        uint8_t *dst = sK + (i / (D / 16)) * C::kRow + (i % (D / 16)) * 32;
+                        uint32_t h[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            h[2 * k] = e4m3x2_to_f16x2_(u[k] & 0xffffu);
+                            h[2 * k + 1] = e4m3x2_to_f16x2_(u[k] >> 16);
+                        }
+                        *(uint4 *)dst = make_uint4(h[0], h[1], h[2], h[3]);
+                        *(uint4 *)(dst + 16) = make_uint4(h[4], h[5], h[6], h[7]);
+                    }
+                }
+            }
+            __syncthreads();
+            if (c + 1 < wk.off + take) load(c + 1);
+            if (base >= it.len) continue;
+            // scores of 16 rows x 64 tokens
+            float s[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t a[4];
+                ldsm4(a, sQ + (16 * rg + (lane & 15)) * C::kRow + k * 32 + (lane >> 4) * 16);
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    uint32_t b[4];
+                    ldsm4(b, sK + (16 * n + (lane & 7) + ((lane >> 4) << 3)) * C::kRow + k * 32 + ((lane >> 3) & 1) * 16);
+                    mma_f16_16816(s[2 * n], a, b[0], b[1]);
+                    mma_f16_16816(s[2 * n + 1], a, b[2], b[3]);
+                }
+            }
+            const float fe = (float)e, scale = qc_pow2(e), unscale = qc_pow2(-e);
+            uint32_t pr[8][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // rows lane / 4 and lane / 4 + 8
+                const int row = 16 * rg + (lane >> 2) + 8 * h;
+                const float cf = s_c[row] * scale;
+                const int lim = s_lim[row] - base;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int col = 8 * n + 2 * (lane & 3) + j;
+                        float &x = s[n][2 * h + j];
+                        x = col < lim ? x * cf + fe : -INFINITY;
+                        mx = fmaxf(mx, x);
+                    }
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, 2));
+                const float mn = fmaxf(m[h], mx), mb = mn == -INFINITY ? 0.f : mn;
+                const float corr = qa_ex2(m[h] - mb);
+                m[h] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    const float w0 = qa_ex2(s[n][2 * h] - mb), w1 = qa_ex2(s[n][2 * h + 1] - mb);
+                    sum += w0 + w1;
+                    pr[n][h] = f32x2_to_f16x2(w0, w1);
+                }
+                l[h] = l[h] * corr + sum * unscale;
+                if (__any_sync(~0u, corr != 1.f)) {
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        oacc[i][2 * h] *= corr;
+                        oacc[i][2 * h + 1] *= corr;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a[4] = {pr[2 * k][0], pr[2 * k][1], pr[2 * k + 1][0], pr[2 * k + 1][1]};
+#pragma unroll
+                for (int n = 0; n < NV / 2; ++n) {
+                    uint32_t b[4];
+                    ldsm4t(b, sK + (16 * k + (lane & 15)) * C::kRow + (half * (DV / 2) + 16 * n) * 2 + (lane >> 4) * 16);
+                    mma_f16_16816(oacc[2 * n], a, b[0], b[1]);
+                    mma_f16_16816(oacc[2 * n + 1], a, b[2], b[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(~0u, l[h], 1);
+            l[h] += __shfl_xor_sync(~0u, l[h], 2);
+            const int row = 16 * rg + (lane >> 2) + 8 * h, r = r0 + row;
+            if (whole) {
+                if (r < R) {
+                    const bool bad = isnan(s_c[row]);
+                    const float inv = bad ? __uint_as_float(0x7fffffffu) : l[h] > 0.f ? 1.f / l[h] : 0.f;
+                    const int tok = it.q0 + r / p.H, hd = r % p.H;
+                    __nv_bfloat16 *dst = p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + half * (DV / 2) + 2 * (lane & 3);
+#pragma unroll
+                    for (int n = 0; n < NV; ++n)
+                        *(__nv_bfloat162 *)(dst + 8 * n) = __floats2bfloat162_rn(oacc[n][2 * h] * inv, oacc[n][2 * h + 1] * inv);
+                    if (p.lse && half == 0 && (lane & 3) == 0)
+                        p.lse[(size_t)tok * p.H + hd] = bad ? __uint_as_float(0x7fffffffu)
+                                                      : l[h] > 0.f ? (m[h] + log2f(l[h])) * 0.6931471805599453f : -INFINITY;
+                }
+            } else {
+                const bool bad = isnan(s_c[row]);
+                float *dst = p.part_o + ((size_t)slot * kQaTile + row) * DV + half * (DV / 2) + 2 * (lane & 3);
+#pragma unroll
+                for (int n = 0; n < NV; ++n) *(float2 *)(dst + 8 * n) = make_float2(oacc[n][2 * h], oacc[n][2 * h + 1]);
+                if (half == 0 && (lane & 3) == 0)
+                    p.part_ml[slot * kQaTile + row] = make_float2(bad ? 0.f : m[h], bad ? __uint_as_float(0x7fffffffu) : l[h]);
+            }
+        }
+        left -= take;
+        unit += it.chunks - wk.off;
+        if (left > 0) wk.next(p);
+    }
+    if (tid == 0) p.split[cta] = sp;
+}
+
+// ---------------------------------------------------------------------------
+// Combine: block (c, g) adds the partials of the item that starts in CTA c and
+// goes on in later ones, rows 8g .. 8g + 7, in CTA order. Bound: latency (the
+// partials are in L2).
+// ---------------------------------------------------------------------------
+template <int DV>
+__global__ void __launch_bounds__(128) qattn_combine_kernel(const QaParams p) {
+    __shared__ float s_w[8][kQaMaxGrid];
+    __shared__ float s_l[8], s_m[8];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int c = blockIdx.x, g = blockIdx.y;
+    pdl_trigger();
+    pdl_wait();
+    const QaSplit sp = p.split[c];
+    if (sp.c_hi < 0) return;
+    const int q0 = p.cu_q[sp.b], R = (p.cu_q[sp.b + 1] - q0) * p.H, r0 = sp.t * kQaTile + 8 * g;
+    if (r0 >= R) return;
+    const int n = sp.c_hi - c + 1;
+    for (int i = warp; i < 8; i += 4) {
+        float m = -INFINITY, l = 0.f;
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + 8 * g + i];
+            m = fmaxf(m, ml.x);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+        const float mb = m == -INFINITY ? 0.f : m;
+        for (int k = lane; k < n; k += 32) {
+            const float2 ml = p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + 8 * g + i];
+            const float w = qa_ex2(ml.x - mb);
+            s_w[i][k] = w;
+            l += w * ml.y;
+        }
+        l = warp_sum(l);
+        if (lane == 0) {
+            s_l[i] = l;
+            s_m[i] = m;
+        }
+    }
+    __syncthreads();
+    constexpr int kRowsAtOnce = 512 / DV;  // 128 threads x 4 columns
+    const int col = 4 * tid % DV, sub = 4 * tid / DV;
+    for (int i = sub; i < 8; i += kRowsAtOnce) {
+        const int r = r0 + i;
+        if (r >= R) break;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+            const int slot = k == 0 ? sp.lo_slot : 2 * (c + k);
+            const float4 v = __ldcg((const float4 *)(p.part_o + ((size_t)slot * kQaTile + 8 * g + i) * DV + col));
+            const float w = s_w[i][k];
+            o.x += w * v.x;
+            o.y += w * v.y;
+            o.z += w * v.z;
+            o.w += w * v.w;
+        }
+        const float l = s_l[i];
+        const float inv = isnan(l) ? l : l > 0.f ? 1.f / l : 0.f;
+        const int tok = q0 + r / p.H, hd = r % p.H;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+        uint2 u;
+        u.x = *(const uint32_t *)&lo;
+        u.y = *(const uint32_t *)&hi;
+        *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + col) = u;
+        if (p.lse && col == 0)
+            p.lse[(size_t)tok * p.H + hd] = isnan(l) ? l : l > 0.f ? (s_m[i] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    }
+}
+
+template <int DV>
+static cudaError_t combine(const QaParams &p, int grid, cudaStream_t st) {
+    return launch_pdl(qattn_combine_kernel<DV>, dim3(grid, kQaTile / 8), dim3(128), 0, st, p);
+}
+
+template <int D, int DV>
+static cudaError_t any_width(const QaParams &p, int num_sms, cudaStream_t st) {
+    using C = QgCfg<D, DV>;
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(qattn_any_kernel<D, DV>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    const int grid = min(num_sms, kQaMaxGrid);
+    const cudaError_t e = launch_pdl(qattn_any_kernel<D, DV>, dim3(grid), dim3(C::kThreads), (size_t)C::kSmem, st, p);
+    return e != cudaSuccess ? e : combine<DV>(p, grid, st);
+}
+
+cudaError_t launch_qattn(const QaParams &p, int kv_lora, int, int num_sms, cudaStream_t st) {
+    switch (kv_lora) {
+        case 512: return any_width<576, 512>(p, num_sms, st);
+        case 256: return any_width<288, 256>(p, num_sms, st);
+        case 128: return any_width<160, 128>(p, num_sms, st);
+        case 64: return any_width<80, 64>(p, num_sms, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace ds

@@ -23,7 +23,8 @@ STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_ALIGN", 3: "ERR_SHAPE", 4: "ERR_UNSUPP
           6: "ERR_WORKSPACE", 16: "ERR_TIMEOUT", 17: "ERR_BAD_INPUT", 18: "ERR_OOB"}
 EXPORTS = ("dspark_create", "dspark_destroy", "dspark_workspace_bytes", "dspark_fuse_ctx", "dspark_draft_block",
            "dspark_markov_rollout", "dspark_confidence", "dspark_verify", "dspark_check", "dspark_status_str",
-           "dspark_fuse_ctx_noalloc", "dspark_kv_append")
+           "dspark_fuse_ctx_noalloc", "dspark_kv_append", "dspark_qcache_plan", "dspark_qcache_append",
+           "dspark_qcache_attend", "dspark_qcache_workspace_bytes", "dspark_qcache_check")
 
 
 class Geom(C.Structure):
@@ -59,6 +60,23 @@ class Sample(C.Structure):
                 ("top_p", C.c_float), ("seed", C.c_uint64), ("step", C.c_uint32)]
 
 
+class QCacheStruct(C.Structure):
+    _fields_ = [("kv_lora", C.c_int), ("d_rope", C.c_int), ("page_size", C.c_int), ("n_layers", C.c_int),
+                ("codes", C.c_void_p * MAX_LAYERS), ("scales", C.c_void_p * MAX_LAYERS), ("n_pages", C.c_int),
+                ("page_table", C.c_void_p), ("max_pages", C.c_int)]
+
+
+class QPlanArgs(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("length", "want", "ring", "ring_state", "length_out", "ring_state_out",
+                                          "cu_new", "slots", "positions", "seg_row")]
+
+
+class QAttnArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_stride", C.c_int64), ("cu_q", C.c_void_p), ("length", C.c_void_p),
+                ("n_heads", C.c_int), ("total_q", C.c_int), ("causal", C.c_int), ("scale", C.c_float),
+                ("o", C.c_void_p), ("o_stride", C.c_int64), ("lse", C.c_void_p)]
+
+
 class DSparkError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn}: {STATUS.get(status, status)} ({status})")
@@ -89,10 +107,16 @@ def lib():
         L.dspark_check.argtypes = [vp, vp, vp]
         L.dspark_fuse_ctx_noalloc.argtypes = [vp, vp, vp, i, vp]
         L.dspark_kv_append.argtypes = [vp, vp, i, vp, C.POINTER(KV), i, vp, sz, vp]
+        L.dspark_qcache_plan.argtypes = [C.POINTER(QCacheStruct), C.POINTER(QPlanArgs), i, i, i, vp, sz, vp]
+        L.dspark_qcache_append.argtypes = [C.POINTER(QCacheStruct), vp, i, C.c_int64, C.c_int64, vp, i, vp, i, vp, sz, vp]
+        L.dspark_qcache_attend.argtypes = [C.POINTER(QCacheStruct), i, C.POINTER(QAttnArgs), i, vp, sz, vp]
+        L.dspark_qcache_workspace_bytes.argtypes = [C.POINTER(QCacheStruct), i]
+        L.dspark_qcache_workspace_bytes.restype = sz
+        L.dspark_qcache_check.argtypes = [vp, vp]
         L.dspark_status_str.argtypes = [i]
         L.dspark_status_str.restype = C.c_char_p
         for f in EXPORTS:
-            if f not in ("dspark_destroy", "dspark_workspace_bytes", "dspark_status_str"):
+            if f not in ("dspark_destroy", "dspark_workspace_bytes", "dspark_status_str", "dspark_qcache_workspace_bytes"):
                 getattr(L, f).restype = i
         _lib = L
     return _lib
@@ -241,3 +265,128 @@ class DSpark:
     def check_noalloc(self) -> int:
         """Synchronise and return (and clear) the error word of the allocation-free fusion's fixed scratch."""
         return lib().dspark_check(self.h, None, _stream())
+
+
+def _int32(name: str, t: torch.Tensor, n: int):
+    """t holds at least n contiguous int32 values on the GPU."""
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
+
+
+class QCache:
+    """A paged latent cache in E4M3 with one power-of-two scale per page of 64 tokens.
+
+    ``codes``: per layer uint8 (or float8_e4m3fn) [n_pages, 64, kv_lora + d_rope]; ``scales``: per layer fp32
+    [n_pages]; ``page_table`` int32 [bs, max_pages]. All belong to the caller and are written in place. The three
+    calls are the page plan, the quantising append (every layer) and the attention over one layer; they run on the
+    current stream and do not wait. ``check()`` reads the error word that their kernels set. Without ``n_heads`` the
+    workspace serves the plan and the append alone; a zero-filled ``workspace`` (uint8) may be given instead, and
+    caches that run on one stream may share it.
+    """
+
+    def __init__(self, kv_lora: int, d_rope: int, codes: Sequence[torch.Tensor], scales: Sequence[torch.Tensor],
+                 page_table: torch.Tensor, n_heads: int = 0, n_pages: Optional[int] = None,
+                 workspace: Optional[torch.Tensor] = None):
+        if len(codes) != len(scales) or len(codes) > MAX_LAYERS:
+            raise ValueError("one code pool and one scale vector per layer, at most %d layers" % MAX_LAYERS)
+        self.D, self.n_heads = kv_lora + d_rope, n_heads
+        if n_pages is None:
+            if not len(codes):
+                raise ValueError("n_pages is needed without code pools")
+            n_pages = int(codes[0].shape[0])
+        for t, u in zip(codes, scales):
+            if (t.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(t.shape) != (n_pages, 64, self.D)
+                    or not t.is_contiguous() or not t.is_cuda):
+                raise ValueError(f"codes: contiguous uint8 or float8_e4m3fn CUDA tensors [{n_pages}, 64, {self.D}]")
+            if u.dtype != torch.float32 or u.numel() != n_pages or not u.is_contiguous() or not u.is_cuda:
+                raise ValueError(f"scales: contiguous fp32 CUDA tensors [{n_pages}]")
+        if page_table.dim() != 2:
+            raise ValueError("page_table: int32 [bs, max_pages]")
+        _int32("page_table", page_table, 1)
+        c = QCacheStruct(kv_lora=kv_lora, d_rope=d_rope, page_size=64, n_layers=len(codes), n_pages=n_pages,
+                         page_table=page_table.data_ptr(), max_pages=int(page_table.shape[1]))
+        for l, (t, u) in enumerate(zip(codes, scales)):
+            c.codes[l], c.scales[l] = t.data_ptr(), u.data_ptr()
+        # the struct holds raw device pointers: keep the tensors alive as long as it lives
+        self._keep = (list(codes), list(scales), page_table)
+        self.c, self.page_table, self.n_pages = c, page_table, n_pages
+        need = lib().dspark_qcache_workspace_bytes(C.byref(c), n_heads)
+        if need == 0:
+            raise DSparkError("dspark_qcache_workspace_bytes", 3)
+        if workspace is None:
+            workspace = torch.zeros(need, dtype=torch.uint8, device=page_table.device)
+        self.ws, self.ws_bytes = workspace, workspace.numel()
+
+    def plan(self, length: torch.Tensor, want: torch.Tensor, ring: torch.Tensor, ring_state: torch.Tensor,
+             length_out: torch.Tensor, ring_state_out: torch.Tensor, cu_new: torch.Tensor,
+             slots: Optional[torch.Tensor], positions: Optional[torch.Tensor], seg_row: torch.Tensor):
+        """Pages, slots and positions for requests that go from ``length`` to ``want`` tokens (int32 [bs]).
+
+        Free pages come from ``ring`` [n_pages] at ``ring_state`` [2] (first free, number). Outputs: ``length_out``
+        [bs], ``ring_state_out`` [2], ``cu_new`` [bs + 1], ``slots`` and ``positions`` (one per new token, then -1;
+        their size is the most new tokens served), ``seg_row`` (first new token of every touched page, then their
+        number; its size less one is the most pages served)."""
+        bs = length.numel()
+        max_new = 0 if slots is None else slots.numel()
+        if bs > self.page_table.shape[0]:
+            raise ValueError("more requests than rows of the page table")
+        for name, t, n in (("length", length, bs), ("want", want, bs), ("ring", ring, self.n_pages),
+                           ("ring_state", ring_state, 2), ("length_out", length_out, bs),
+                           ("ring_state_out", ring_state_out, 2), ("cu_new", cu_new, bs + 1), ("seg_row", seg_row, 1)):
+            _int32(name, t, n)
+        if slots is not None:
+            _int32("slots", slots, 0)
+        if max_new:
+            _int32("positions", positions, max_new)
+        a = QPlanArgs(length.data_ptr(), want.data_ptr(), ring.data_ptr(), ring_state.data_ptr(), length_out.data_ptr(),
+                      ring_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr() if max_new else None,
+                      positions.data_ptr() if max_new else None, seg_row.data_ptr())
+        _chk("dspark_qcache_plan", lib().dspark_qcache_plan(C.byref(self.c), C.byref(a), bs, max_new,
+                                                            seg_row.numel() - 1, _p(self.ws), self.ws_bytes, _stream()))
+
+    def append(self, entries: torch.Tensor, slots: torch.Tensor, seg_row: torch.Tensor):
+        """Quantise entries [n_layers, rows, kv_lora + d_rope] (bf16 or fp32, any row and layer stride) into the slots
+        of dspark_qcache_plan, raising the scales of pages that need it."""
+        if entries.dim() != 3 or entries.shape[0] != self.c.n_layers or entries.shape[2] != self.D or not entries.is_cuda:
+            raise ValueError(f"entries: CUDA tensor [{self.c.n_layers}, rows, {self.D}]")
+        if entries.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("entries: bf16 or fp32")
+        if entries.stride(2) != 1:
+            raise ValueError("entries: the elements of a row are contiguous")
+        rows = min(entries.shape[1], slots.numel())
+        _int32("slots", slots, 0)
+        _int32("seg_row", seg_row, 1)
+        row_stride = entries.stride(1) if entries.shape[1] > 1 else self.D  # torch leaves the stride of one row open
+        _chk("dspark_qcache_append", lib().dspark_qcache_append(
+            C.byref(self.c), _p(entries), 0 if entries.dtype == torch.bfloat16 else 1, row_stride,
+            entries.stride(0), _p(slots), rows, _p(seg_row), seg_row.numel() - 1, _p(self.ws), self.ws_bytes, _stream()))
+
+    def attend(self, layer: int, q: torch.Tensor, cu_q: torch.Tensor, length: torch.Tensor, o: torch.Tensor,
+               lse: Optional[torch.Tensor] = None, causal: bool = True, scale: float = 1.0):
+        """o = softmax(scale q k^T) v over one layer: q bf16 [total_q, n_heads, kv_lora + d_rope] (any token stride),
+        request b's queries at cu_q[b] .. cu_q[b+1]-1, ``length`` cached tokens each; o bf16 [total_q, n_heads,
+        kv_lora], lse fp32 [total_q, n_heads]."""
+        kv = self.c.kv_lora
+        if q.dim() != 3 or q.shape[2] != self.D or q.dtype != torch.bfloat16 or not q.is_cuda:
+            raise ValueError(f"q: bf16 CUDA tensor [total_q, n_heads, {self.D}]")
+        n, h = q.shape[0], q.shape[1]
+        if tuple(o.shape) != (n, h, kv) or o.dtype != torch.bfloat16 or not o.is_cuda:
+            raise ValueError(f"o: bf16 CUDA tensor [{n}, {h}, {kv}]")
+        if n and (q.stride(2) != 1 or (h > 1 and q.stride(1) != self.D) or o.stride(2) != 1 or (h > 1 and o.stride(1) != kv)):
+            raise ValueError("q and o: the heads of a token are contiguous")
+        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * h or not lse.is_contiguous() or not lse.is_cuda):
+            raise ValueError(f"lse: contiguous fp32 CUDA tensor [{n}, {h}]")
+        bs = length.numel()
+        if bs > self.page_table.shape[0]:
+            raise ValueError("more requests than rows of the page table")
+        _int32("length", length, 1)
+        _int32("cu_q", cu_q, bs + 1)
+        a = QAttnArgs(q.data_ptr() or None, q.stride(0) if n > 1 else h * self.D, cu_q.data_ptr(), length.data_ptr(), h, n,
+                      int(bool(causal)), float(scale), o.data_ptr() or None, o.stride(0) if n > 1 else h * kv,
+                      None if lse is None else lse.data_ptr())
+        _chk("dspark_qcache_attend", lib().dspark_qcache_attend(C.byref(self.c), layer, C.byref(a), bs, _p(self.ws),
+                                                                self.ws_bytes, _stream()))
+
+    def check(self) -> int:
+        """Synchronise and return (and clear) the device error word."""
+        return lib().dspark_qcache_check(_p(self.ws), _stream())
