@@ -289,7 +289,7 @@ typedef struct {
     int page_size;                    /* 64 */
     int n_layers;                     /* 0..DSPARK_MAX_LAYERS (0: a struct for dspark_qcache_plan only) */
     void *codes[DSPARK_MAX_LAYERS];   /* device, E4M3 [n_pages, 64, kv_lora + d_rope] */
-    float *scales[DSPARK_MAX_LAYERS]; /* device, fp32 [n_pages] */
+    float *scales[DSPARK_MAX_LAYERS]; /* device, fp32 [n_pages] (4-byte aligned: rows of a [n_layers, n_pages] matrix) */
     int n_pages;                      /* < 2^25 */
     int32_t *page_table;              /* device int32 [bs, max_pages] */
     int max_pages;                    /* < 2^25 */
@@ -366,8 +366,8 @@ typedef struct {
  * (decode) over a drafted block to a chunk of a prompt:
  *   o = softmax(scale * q k^T) v,  k = the cached entry, v = its first kv_lora elements.
  * A query that sees no token gives o = 0 and lse = -inf. Scores, maxima and
- * sums are fp32; q enters to the full bf16 (elements below 2^-17 of their
- * row's largest lose low bits), the softmax weights with at least 8
+ * sums are fp32; q enters to the full bf16 (elements below 2^-13 of their
+ * row's largest keep an absolute error of 2^-22 of it), the softmax weights with at least 8
  * significant bits. Cached elements must be finite (the append writes no
  * other); entries past a request's length are never used. The workspace holds
  * split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of

@@ -534,6 +534,19 @@ namespace ds {
 const dspark_geom_t *handle_geom(const dspark_handle_t *h) { return &h->g; }
 int handle_num_sms(const dspark_handle_t *h) { return h->num_sms; }
 const CUtensorMap *handle_fc_map(const dspark_handle_t *h) { return &h->fc; }
+bool encode_u16_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes,
+                    uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || !base) return false;
+    cuuint64_t dims[2] = {row_bytes / 2, rows};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_bytes / 2, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_bf16_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     return make_map(m, base, rows, cols, box_rows);
 }

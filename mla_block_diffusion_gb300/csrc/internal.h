@@ -144,6 +144,10 @@ const dspark_geom_t *handle_geom(const dspark_handle_t *h);
 int handle_num_sms(const dspark_handle_t *h);
 const CUtensorMap *handle_fc_map(const dspark_handle_t *h);
 bool encode_bf16_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Rows of bytes as 16-bit elements: boxes of box_bytes (128 or 64, swizzled in
+// the same width) x box_rows.
+bool encode_u16_map(CUtensorMap *m, const void *base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes,
+                    uint32_t box_rows);
 
 // Error word of the allocation-free fusion's fixed scratch on the current
 // device (synchronises the stream; reads and clears the word).

@@ -1,5 +1,5 @@
 // Attention over the 8-bit latent cache (include/dspark.h, call 9): the kernel
-// for every latent width, and the combine of split items.
+// for the smaller latent widths, and the combine of split items.
 #include <math.h>
 
 #include "e4m3.cuh"
@@ -31,7 +31,7 @@ DS_DEVINL float qa_ex2(float x) {
 }
 
 // ---------------------------------------------------------------------------
-// Every width, mma.sync m16n8k16 in f16.
+// The smaller widths (256 + 32, 128 + 32, 64 + 16), mma.sync m16n8k16 in f16.
 //
 // A CTA of 8 warps holds 64 query rows: warp (w & 3) 16 of them, w >> 2 one half
 // of the output columns (both halves compute the scores of their rows). E4M3
@@ -281,77 +281,109 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
 }
 
 // ---------------------------------------------------------------------------
-// Combine: block (c, g) adds the partials of the item that starts in CTA c and
-// goes on in later ones, rows 8g .. 8g + 7, in CTA order. Bound: latency (the
-// partials are in L2).
+// Combine: the rows of items that were split, one warp per row and 128 columns
+// (a row's columns at the narrower widths), partials in CTA order. The warp's
+// lanes hold the partials' weights; eight partials are in flight at a time.
+// Bound: latency and L2 (the partials were just written).
 // ---------------------------------------------------------------------------
+constexpr int kQaCombineThreads = 256;
+
 template <int DV>
-__global__ void __launch_bounds__(128) qattn_combine_kernel(const QaParams p) {
-    __shared__ float s_w[8][kQaMaxGrid];
-    __shared__ float s_l[8], s_m[8];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int c = blockIdx.x, g = blockIdx.y;
+__global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const QaParams p, int ctas) {
+    __shared__ QaSplit s_list[kQaMaxGrid];
+    __shared__ int s_first[kQaMaxGrid];
+    __shared__ unsigned s_mask[kQaMaxGrid / 32];
+    constexpr int kCols = DV < 128 ? DV : 128, kSub = DV / kCols;
+    const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
     pdl_wait();
-    const QaSplit sp = p.split[c];
-    if (sp.c_hi < 0) return;
-    const int q0 = p.cu_q[sp.b], R = (p.cu_q[sp.b + 1] - q0) * p.H, r0 = sp.t * kQaTile + 8 * g;
-    if (r0 >= R) return;
-    const int n = sp.c_hi - c + 1;
-    for (int i = warp; i < 8; i += 4) {
-        float m = -INFINITY, l = 0.f;
-        for (int k = lane; k < n; k += 32) {
-            const float2 ml = p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + 8 * g + i];
-            m = fmaxf(m, ml.x);
+    // the split items in CTA order (every block lists them alike)
+    QaSplit sp_own[kQaMaxGrid / kQaCombineThreads];
+#pragma unroll
+    for (int i = 0; i < kQaMaxGrid / kQaCombineThreads; ++i) {
+        const int c = tid + i * kQaCombineThreads;
+        sp_own[i].c_hi = -1;
+        if (c < ctas) sp_own[i] = p.split[c];
+        const unsigned mask = __ballot_sync(~0u, sp_own[i].c_hi >= 0);
+        if (lane == 0) s_mask[c / 32] = mask;
+    }
+    __syncthreads();
+    int n_split = 0;
+    for (int w = 0; w < kQaMaxGrid / 32; ++w) {
+        const unsigned mask = s_mask[w];
+#pragma unroll
+        for (int i = 0; i < kQaMaxGrid / kQaCombineThreads; ++i) {
+            const int c = tid + i * kQaCombineThreads;
+            if (c / 32 == w && sp_own[i].c_hi >= 0) {
+                const int at = n_split + __popc(mask & ((1u << lane) - 1u));
+                s_list[at] = sp_own[i];
+                s_first[at] = c;
+            }
         }
+        n_split += __popc(mask);
+    }
+    __syncthreads();
+    const int tasks = n_split * kQaTile * kSub, warps = gridDim.x * (kQaCombineThreads / 32);
+    for (int task = blockIdx.x * (kQaCombineThreads / 32) + (tid >> 5); task < tasks; task += warps) {
+        const int sub = task % kSub, row = task / kSub % kQaTile, li = task / kSub / kQaTile;
+        const QaSplit sp = s_list[li];
+        const int c = s_first[li], n = sp.c_hi - c + 1;
+        const int q0 = p.cu_q[sp.b], r = sp.t * kQaTile + row;
+        if (r >= (p.cu_q[sp.b + 1] - q0) * p.H) continue;
+        // weights of up to 32 partials at a time; all of them fit into one round but for very long splits
+        float m = -INFINITY;
+        for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(&p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + row]).x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
         const float mb = m == -INFINITY ? 0.f : m;
-        for (int k = lane; k < n; k += 32) {
-            const float2 ml = p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + 8 * g + i];
-            const float w = qa_ex2(ml.x - mb);
-            s_w[i][k] = w;
-            l += w * ml.y;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float l = 0.f;
+        const float *src = p.part_o + (size_t)row * DV + sub * kCols + 4 * lane;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float w = 0.f;
+            if (k0 + lane < n) {
+                const float2 ml = __ldcg(&p.part_ml[(k0 + lane == 0 ? sp.lo_slot : 2 * (c + k0 + lane)) * kQaTile + row]);
+                w = qa_ex2(ml.x - mb);
+                l += w * ml.y;
+            }
+            const int kn = min(32, n - k0);
+            for (int k = 0; k < kn; k += 8) {
+                float4 v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int kk = k0 + k + j;
+                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (kk < n && 4 * lane < kCols)
+                        v[j] = __ldcg((const float4 *)(src + (size_t)(kk == 0 ? sp.lo_slot : 2 * (c + kk)) * (kQaTile * DV)));
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float wk = __shfl_sync(~0u, w, (k + j) & 31);
+                    o.x += wk * v[j].x;
+                    o.y += wk * v[j].y;
+                    o.z += wk * v[j].z;
+                    o.w += wk * v[j].w;
+                }
+            }
         }
         l = warp_sum(l);
-        if (lane == 0) {
-            s_l[i] = l;
-            s_m[i] = m;
-        }
-    }
-    __syncthreads();
-    constexpr int kRowsAtOnce = 512 / DV;  // 128 threads x 4 columns
-    const int col = 4 * tid % DV, sub = 4 * tid / DV;
-    for (int i = sub; i < 8; i += kRowsAtOnce) {
-        const int r = r0 + i;
-        if (r >= R) break;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const int slot = k == 0 ? sp.lo_slot : 2 * (c + k);
-            const float4 v = __ldcg((const float4 *)(p.part_o + ((size_t)slot * kQaTile + 8 * g + i) * DV + col));
-            const float w = s_w[i][k];
-            o.x += w * v.x;
-            o.y += w * v.y;
-            o.z += w * v.z;
-            o.w += w * v.w;
-        }
-        const float l = s_l[i];
         const float inv = isnan(l) ? l : l > 0.f ? 1.f / l : 0.f;
         const int tok = q0 + r / p.H, hd = r % p.H;
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-        uint2 u;
-        u.x = *(const uint32_t *)&lo;
-        u.y = *(const uint32_t *)&hi;
-        *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + col) = u;
-        if (p.lse && col == 0)
-            p.lse[(size_t)tok * p.H + hd] = isnan(l) ? l : l > 0.f ? (s_m[i] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (4 * lane < kCols) {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+            uint2 u;
+            u.x = *(const uint32_t *)&lo;
+            u.y = *(const uint32_t *)&hi;
+            *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + sub * kCols + 4 * lane) = u;
+        }
+        if (p.lse && sub == 0 && lane == 0)
+            p.lse[(size_t)tok * p.H + hd] = isnan(l) ? l : l > 0.f ? (mb + log2f(l)) * 0.6931471805599453f : -INFINITY;
     }
 }
 
 template <int DV>
-static cudaError_t combine(const QaParams &p, int grid, cudaStream_t st) {
-    return launch_pdl(qattn_combine_kernel<DV>, dim3(grid, kQaTile / 8), dim3(128), 0, st, p);
+static cudaError_t combine(const QaParams &p, int grid, int num_sms, cudaStream_t st) {
+    return launch_pdl(qattn_combine_kernel<DV>, dim3(2 * num_sms), dim3(kQaCombineThreads), 0, st, p, grid);
 }
 
 template <int D, int DV>
@@ -365,12 +397,16 @@ static cudaError_t any_width(const QaParams &p, int num_sms, cudaStream_t st) {
     }
     const int grid = min(num_sms, kQaMaxGrid);
     const cudaError_t e = launch_pdl(qattn_any_kernel<D, DV>, dim3(grid), dim3(C::kThreads), (size_t)C::kSmem, st, p);
-    return e != cudaSuccess ? e : combine<DV>(p, grid, st);
+    return e != cudaSuccess ? e : combine<DV>(p, grid, num_sms, st);
 }
 
 cudaError_t launch_qattn(const QaParams &p, int kv_lora, int, int num_sms, cudaStream_t st) {
     switch (kv_lora) {
-        case 512: return any_width<576, 512>(p, num_sms, st);
+        case 512: {
+            const int grid = min(num_sms, kQaMaxGrid);
+            const cudaError_t e = launch_qattn_tc(p, grid, st);
+            return e != cudaSuccess ? e : combine<512>(p, grid, num_sms, st);
+        }
         case 256: return any_width<288, 256>(p, num_sms, st);
         case 128: return any_width<160, 128>(p, num_sms, st);
         case 64: return any_width<80, 64>(p, num_sms, st);

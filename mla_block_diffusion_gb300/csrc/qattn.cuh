@@ -29,23 +29,26 @@ struct QaItem {
 
 template <int TILE, int CH>
 struct QaWork {
+    static_assert((TILE & (TILE - 1)) == 0 && (CH & (CH - 1)) == 0, "powers of two");
     // Request b's queries and length; out of range: no queries (reported by `report`).
     static DS_DEVINL void request(const QaParams &p, int b, int *q0, int *nq, int *len, bool report = false) {
         const int a = p.cu_q[b], z = p.cu_q[b + 1], n = p.length[b];
-        const bool ok = a >= 0 && z >= a && z <= p.total_q && n >= 0 && n <= (long long)p.max_pages * kQcPage;
+        const bool ok = a >= 0 && z >= a && z <= p.total_q && n >= 0 && (unsigned)n <= (unsigned)p.max_pages * kQcPage;
         if (!ok && report) set_error(p.err, DSPARK_ERR_OOB);
         *q0 = ok ? a : 0;
         *nq = ok ? z - a : 0;
         *len = ok ? n : 0;
     }
-    static DS_DEVINL int tiles(const QaParams &p, int nq) { return (int)(((long long)nq * p.H + TILE - 1) / TILE); }
+    // total_q * H < 2^31 - TILE * 1024
+    static DS_DEVINL int tiles(const QaParams &p, int nq) { return (int)(((unsigned)nq * (unsigned)p.H + TILE - 1) / TILE); }
     // Tokens that query i of nq sees.
     static DS_DEVINL int sees(const QaParams &p, int nq, int len, int i) {
         return p.causal ? max(0, len - nq + i + 1) : len;
     }
     static DS_DEVINL int chunks(const QaParams &p, int nq, int len, int t) {
-        const int last = min(nq - 1, (int)((((long long)t + 1) * TILE - 1) / p.H));
-        return max(1, (int)(((long long)sees(p, nq, len, last) + CH - 1) / CH));
+        unsigned seen = (unsigned)len;
+        if (p.causal) seen = (unsigned)sees(p, nq, len, min(nq - 1, (int)((((unsigned)t + 1u) * TILE - 1u) / (unsigned)p.H)));
+        return max(1, (int)((seen + CH - 1) / CH));
     }
 
     long long begin, end;  // this CTA's units
@@ -55,93 +58,100 @@ struct QaWork {
     int off;               // units of it before `begin`
 
     // Block-wide exclusive sum; *sum gets the total. scratch: one word per warp.
-    static DS_DEVINL long long scan(long long v, long long *scratch, long long *sum) {
+    template <typename T>
+    static DS_DEVINL T scan(T v, T *scratch, T *sum) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-        long long inc = v;
+        T inc = v;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(~0u, inc, d);
+            const T o = __shfl_up_sync(~0u, inc, d);
             if (lane >= d) inc += o;
         }
-        __syncthreads();
         if (lane == 31) scratch[warp] = inc;
         __syncthreads();
-        long long base = 0, all = 0;
+        T base = 0, all = 0;
         for (int w = 0; w < nw; ++w) {
-            if (w < warp) base += scratch[w];
-            all += scratch[w];
+            const T x = scratch[w];
+            if (w < warp) base += x;
+            all += x;
         }
         *sum = all;
         return base + inc - v;
     }
 
-    static constexpr int kScratch = (32 + 4) * 8 + (kQcMaxBs + 2) * 4;  // bytes of shared memory that find() uses
+    struct Scratch {  // shared memory that find() uses
+        long long units[32];
+        int tiles[32];
+        int at[4];                          // request, tile, units before `begin`
+        int first[kQcMaxBs + 1];            // first tile of every request
+        int q0[kQcMaxBs], nq[kQcMaxBs], len[kQcMaxBs];
+    };
+    static constexpr int kScratch = sizeof(Scratch);
 
-    // All threads of the block. cta of grid.
+    // All threads of the block: this CTA's range of the grid's.
     DS_DEVINL void find(const QaParams &p, int cta, int grid, void *smem) {
-        long long *s_scan = (long long *)smem;
-        int *s_item = (int *)(s_scan + 32);  // b, t, off
-        int *s_tiles = (int *)(s_scan + 36);
+        Scratch &s = *(Scratch *)smem;
         const int nt = blockDim.x, tid = threadIdx.x;
-        // first tile of every request
-        const int per = (p.bs + nt - 1) / nt;
-        long long mine = 0, all_tiles;
-        for (int j = 0; j < per; ++j) {
-            const int b = tid * per + j;
-            if (b >= p.bs) break;
+        // requests: their tiles, and the first tile of each
+        const int per = (p.bs + nt - 1) / nt, b0 = tid * per, b1 = min(p.bs, b0 + per);
+        int mine = 0, all_tiles;
+        for (int b = b0; b < b1; ++b) {
             int q0, nq, len;
             request(p, b, &q0, &nq, &len, cta == 0);
+            s.q0[b] = q0;
+            s.nq[b] = nq;
+            s.len[b] = len;
             mine += tiles(p, nq);
         }
-        long long at = scan(mine, s_scan, &all_tiles);
-        for (int j = 0; j < per; ++j) {
-            const int b = tid * per + j;
-            if (b >= p.bs) break;
-            int q0, nq, len;
-            request(p, b, &q0, &nq, &len);
-            s_tiles[b] = (int)at;
-            at += tiles(p, nq);
+        int at = scan(mine, s.tiles, &all_tiles);
+        for (int b = b0; b < b1; ++b) {
+            s.first[b] = at;
+            at += tiles(p, s.nq[b]);
         }
-        if (tid == 0) s_tiles[p.bs] = (int)all_tiles;
+        if (tid == 0) s.first[p.bs] = all_tiles;
         __syncthreads();
         // units of this thread's run of tiles
-        const int i0 = (int)((long long)tid * all_tiles / nt), i1 = (int)((long long)(tid + 1) * all_tiles / nt);
+        const int run = (all_tiles + nt - 1) / nt, i0 = min(all_tiles, tid * run), i1 = min(all_tiles, i0 + run);
         auto walk = [&](long long from, bool seek) -> long long {
             if (i0 >= i1) return from;
             int lo = 0, hi = p.bs;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (s_tiles[mid] <= i0) lo = mid;
+                if (s.first[mid] <= i0) lo = mid;
                 else hi = mid;
             }
-            int b = lo, q0, nq, len;
-            request(p, b, &q0, &nq, &len);
+            int b = lo;
             for (int i = i0; i < i1; ++i) {
-                while (i >= s_tiles[b + 1]) {
-                    ++b;
-                    request(p, b, &q0, &nq, &len);
-                }
-                const int n = chunks(p, nq, len, i - s_tiles[b]);
+                while (i >= s.first[b + 1]) ++b;
+                const int n = chunks(p, s.nq[b], s.len[b], i - s.first[b]);
                 if (seek && from <= begin && begin < from + n) {
-                    s_item[0] = b;
-                    s_item[1] = i - s_tiles[b];
-                    s_item[2] = (int)(begin - from);
+                    s.at[0] = b;
+                    s.at[1] = i - s.first[b];
+                    s.at[2] = (int)(begin - from);
                 }
                 from += n;
             }
             return from;
         };
-        const long long start = scan(walk(0, false), s_scan, &total);
+        const long long start = scan(walk(0, false), s.units, &total);
         parts = (int)(total < grid ? total : grid);
-        begin = cta < parts ? (long long)cta * total / parts : total;
-        end = cta < parts ? (long long)(cta + 1) * total / parts : total;
+        if (total < (1ll << 22)) {  // grid <= 512: 32-bit divisions
+            const unsigned T = (unsigned)total, P = max(1u, (unsigned)parts);
+            begin = cta < parts ? (unsigned)cta * T / P : T;
+            end = cta < parts ? (unsigned)(cta + 1) * T / P : T;
+        } else {
+            begin = cta < parts ? (long long)cta * total / parts : total;
+            end = cta < parts ? (long long)(cta + 1) * total / parts : total;
+        }
         walk(start, true);
         __syncthreads();
         if (begin < end) {
-            item.b = s_item[0];
-            item.t = s_item[1];
-            off = s_item[2];
-            request(p, item.b, &item.q0, &item.nq, &item.len);
+            item.b = s.at[0];
+            item.t = s.at[1];
+            off = s.at[2];
+            item.q0 = s.q0[item.b];
+            item.nq = s.nq[item.b];
+            item.len = s.len[item.b];
             item.chunks = chunks(p, item.nq, item.len, item.t);
         }
         __syncthreads();

@@ -1,0 +1,661 @@
+// Attention over the 8-bit latent cache at the full latent width (512 + 64) on
+// the 5th-generation tensor core; codes go to it as they are stored.
+//
+// A CTA holds 64 query rows (token, head) and walks chunks of 128 cached tokens
+// (two pages). Both products are formed transposed, with tokens or value
+// dimensions as the 128 rows of the accumulator and the query rows as its
+// columns, so that 64 rows (one token of 64 heads) fill the tensor core:
+//
+//   S^T [128 tokens, 64 hi | 64 lo] = K [128, 576] (Qhi | Qlo)^T    kind::f8f6f4
+//     A query row times 2^a, its largest magnitude in [2^7, 2^8), is the sum of
+//     two E4M3 numbers, hi and lo / 16: exact for bf16 down to 2^-13 of the
+//     largest, below that to 2^-22 of it. s = hi + lo / 16.
+//   O^T [4 x 128 dims, 64] += V^T (Phi + Plo)^T                     kind::mxf8f6f4
+//     V is K's first 512 columns, read from the same bytes. For every row and 32
+//     tokens, b = round(max t) (t = s + e in the log2 domain, e the page scale's
+//     exponent), the weights 2^(t - b + 8) < 363 are the sum of two E4M3 numbers
+//     hi and lo / 16 (8 significant bits, absolute error 2^-14), and the block's
+//     E8M0 scale is 2^(b - 8 - M) with M the row's reference: E4M3 alone spans 17
+//     binades, too few beside a token that outweighs thousands of others; the
+//     scale of every 32 tokens follows their own size. M is the first chunk's
+//     maximum and moves only when a block exceeds it by 2^60 (O and the sum are
+//     then rescaled), since E8M0 and the fp32 accumulator have the range: the
+//     usual rescaling of O whenever a maximum grows does not exist here.
+//     Row sums add the unrounded weights times 2^(b - 8 - M - e) in fp32.
+//
+// Tensor memory: O^T 4 x 64 columns, S^T 128, scale words. Shared memory: the
+// query tile 72 KB, two chunk stages of 72 KB (four boxes of 128 dims in the
+// 128-byte swizzle, K-major for S^T and MN-major for O^T; the rope box in the
+// 64-byte swizzle), Plo 8 KB; Phi takes the place of the chunk's rope box, which
+// only S^T reads. A box goes back to the producer as soon as the products of its
+// dimensions are done.
+//
+// Bound: the tensor core (128 products of 64 rows a chunk against 73 KB of
+// codes). Measured issue rates: 64.7 clocks a score step (N = 128, full rate), 51
+// an output step (N = 64, bound by the 6 KB of operands it reads from shared
+// memory), so a chunk is 1165 + 1629 clocks against 2177 at the full rate.
+//
+// Roles (10 warps): warp 0 TMA producer; warp 1 MMA issuer and tensor-memory
+// owner; warps 2-9 queries, softmax and output (a thread holds one token of 32
+// rows). All waits are bounded; a timeout raises DSPARK_ERR_TIMEOUT.
+#include <math.h>
+
+#include <type_traits>
+
+#include "e4m3.cuh"
+#include "internal.h"
+#include "qattn.cuh"
+
+namespace ds {
+
+constexpr int kQtKeys = 128;                       // tokens per chunk
+constexpr int kQtThreads = 320;
+constexpr int kQtD = 576, kQtDV = 512;
+constexpr int kQtBox = kQtKeys * 128;              // bytes: 128 tokens x 128 dims
+constexpr int kQtRope = kQtKeys * 64;              // 128 tokens x 64 dims
+constexpr int kQtStage = 4 * kQtBox + kQtRope;
+constexpr int kQtQ = 4 * kQtBox + kQtRope;         // (64 hi + 64 lo) rows x 576
+constexpr int kQtPlo = kQtKeys * 64;
+constexpr int kQtOutPitch = kQtDV * 2 + 16;           // staged output row, bytes
+constexpr int kQtColO = 0, kQtColS = 256, kQtColSfa = 384, kQtColSfb = 392;
+constexpr int kQtMoveLog2 = 60;
+
+struct QtMisc {
+    uint64_t full[2][5], free_[2][5];  // per stage: boxes 0..3, rope
+    uint64_t s_full, s_free, p_ready, pv_done, q_ready, item_done, mma_done, grp[2];
+    uint32_t tmem;
+    volatile int abort;
+    uint8_t issued[2][8];              // loads in flight: 1 | parity << 1, per box
+    int8_t e[2][2];                    // page scale exponents of a stage's pages
+    alignas(16) float c[kQaTile];      // score factor per row; -0 marks a non-finite query
+    alignas(16) int lim[kQaTile];      // tokens that a row sees
+    alignas(16) int16_t b[2][2][4][32];  // block exponents by group, chunk parity, lane quarter, row; at an item's
+                                         // end the output factors of the group's warps
+    alignas(16) float w[8][32];        // per warp, one value per row
+};
+constexpr int kQtSmem = kQtQ + 2 * kQtStage + kQtPlo + (int)sizeof(QtMisc);
+static_assert(kQtSmem <= 232448, "shared memory");
+static_assert(kQaTile * kQtOutPitch <= kQtQ, "the staged output takes the place of the queries");
+static_assert(sizeof(QtMisc::b) == 8 * 32 * sizeof(float), "output factors");
+static_assert(QaWork<kQaTile, kQtKeys>::kScratch <= kQtStage, "scratch of the work division");
+
+DS_DEVINL float redux_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+DS_DEVINL float qt_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+DS_DEVINL void tmem_st1(uint32_t addr, uint32_t v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(addr), "r"(v) : "memory");
+}
+DS_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+DS_DEVINL bool qt_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+}
+
+__global__ void __launch_bounds__(kQtThreads, 1)
+    qattn_tc_kernel(const __grid_constant__ CUtensorMap tm_dims, const __grid_constant__ CUtensorMap tm_rope,
+                    const QaParams p) {
+    using W = QaWork<kQaTile, kQtKeys>;
+    extern __shared__ __align__(1024) uint8_t qt_smem[];
+    uint8_t *sQ = qt_smem, *sK = sQ + kQtQ, *sP = sK + 2 * kQtStage;
+    QtMisc &ms = *(QtMisc *)(sP + kQtPlo);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, grid = gridDim.x;
+
+    pdl_trigger();
+    if (tid == 0) {
+        for (int s = 0; s < 2; ++s)
+            for (int d = 0; d < 5; ++d) {
+                mbar_init(&ms.full[s][d], 1);
+                mbar_init(&ms.free_[s][d], 1);
+                ms.issued[s][d] = 0;
+            }
+        mbar_init(&ms.s_full, 1);
+        mbar_init(&ms.s_free, 8);
+        mbar_init(&ms.p_ready, 8);
+        mbar_init(&ms.pv_done, 1);
+        mbar_init(&ms.q_ready, 8);
+        mbar_init(&ms.item_done, 8);
+        mbar_init(&ms.mma_done, 1);
+        mbar_init(&ms.grp[0], 4);
+        mbar_init(&ms.grp[1], 4);
+        ms.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_dims);
+        tma_prefetch_desc(&tm_rope);
+    }
+    if (warp == 1) tmem_alloc(&ms.tmem, 512);
+    pdl_wait();
+    W wk;
+    wk.find(p, cta, grid, sK);
+    fence_async_smem();  // the scratch was written through the generic proxy
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ms.tmem;
+    long long left = wk.end - wk.begin;
+    volatile int *abort = &ms.abort;
+    uint32_t ci = 0;  // chunks of this CTA so far
+
+    if (warp == 0) {
+        // ---- producer: page numbers and scales 32 pages at a time, one block ahead
+        bool ok = true;
+        while (left > 0 && ok) {
+            const QaItem it = wk.item;
+            const int take = (int)min((long long)(it.chunks - wk.off), left);
+            const int npages = (it.len + kQcPage - 1) / kQcPage, first = 2 * wk.off;
+            const int32_t *row = p.page_table + (size_t)it.b * p.max_pages;
+            auto page = [&](int i) {  // page number i of the request (0 past its end)
+                int pg = i < npages && i < first + 2 * take ? row[i] : 0;
+                if (pg < 0 || pg >= p.n_pages) {
+                    set_error(p.err, DSPARK_ERR_OOB);
+                    pg = 0;
+                }
+                return pg;
+            };
+            auto exponent = [&](int i, int pg) {
+                int e = 0;
+                if (i < npages && i < first + 2 * take && !qc_scale_exponent(p.scales[pg], &e)) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+                return e;
+            };
+            int pg = page(first + lane), ex = exponent(first + lane, pg), pg_n = 0, ex_n = 0;
+            for (int i = 0; i < take && ok; ++i, ++ci) {
+                const int j = i & 15;
+                if (j == 0) {
+                    if (i > 0) {
+                        pg = pg_n;
+                        ex = ex_n;
+                    }
+                    pg_n = page(first + 2 * (i + 16) + lane);
+                }
+                if (j == 8) ex_n = exponent(first + 2 * (i + 8) + lane, pg_n);
+                const int pa = __shfl_sync(~0u, pg, 2 * j), pb = __shfl_sync(~0u, pg, 2 * j + 1);
+                const int ea = __shfl_sync(~0u, ex, 2 * j), eb = __shfl_sync(~0u, ex, 2 * j + 1);
+                if (lane == 0) {
+                    const int st = ci & 1, n = max(0, min(2, npages - (first + 2 * i)));
+                    const uint32_t par = ((ci >> 1) - 1) & 1;
+                    uint8_t *dst = sK + st * kQtStage;
+                    for (int d = 0; d < 5; ++d) {
+                        if (ci >= 2 && !mbar_wait_bounded(&ms.free_[st][d], par, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        if (d == 0) {
+                            ms.e[st][0] = (int8_t)ea;
+                            ms.e[st][1] = (int8_t)eb;
+                        }
+                        uint64_t *bar = &ms.full[st][d];
+                        const int bytes = d < 4 ? kQtBox / 2 : kQtRope / 2;
+                        if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * bytes));
+                        else mbar_arrive(bar);
+                        for (int k = 0; k < n; ++k) {
+                            uint8_t *to = dst + d * kQtBox + k * bytes;
+                            const int y = (k ? pb : pa) * kQcPage;
+                            // 16-bit elements: 64 (32) of them a box row
+                            if (d < 4) tma_load_2d(to, &tm_dims, d * 64, y, bar);
+                            else tma_load_2d(to, &tm_rope, 256, y, bar);
+                        }
+                        ms.issued[st][d] = (uint8_t)(1 | ((ci >> 1) & 1) << 1);
+                    }
+                }
+                ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+            }
+            left -= take;
+            if (left > 0) wk.next(p);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // Everything about an operand but its stage is a constant added to one word: the
+            // issuing thread shares its scheduler with softmax warps and has about 50
+            // clocks for each MMA.
+            const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sK)), p_lo = sdesc_lo(smem_u32(sP));
+            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4);
+            auto scores = [&](auto stage, uint32_t x) -> bool {
+                constexpr int st = decltype(stage)::value;
+                constexpr uint32_t id = idesc_e4m3_f32(128, 128);
+                const uint32_t par = (x >> 1) & 1;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    if (!mbar_wait_bounded(&ms.full[st][d], par, abort)) return false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_e4m3_w(tmem + kQtColS, k_lo + ((st * kQtStage + d * kQtBox + 32 * k) >> 4), kHi128,
+                                   q_lo + ((d * kQtBox + 32 * k) >> 4), kHi128, id, d > 0 || k > 0);
+                }
+                if (!mbar_wait_bounded(&ms.full[st][4], par, abort)) return false;
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    mma_e4m3_w(tmem + kQtColS, k_lo + ((st * kQtStage + 4 * kQtBox + 32 * k) >> 4), kHi64,
+                               q_lo + ((4 * kQtBox + 32 * k) >> 4), kHi64, id, 1);
+                mma_commit(&ms.s_full);
+                return true;
+            };
+            auto output = [&](auto stage, uint32_t first) {
+                constexpr int st = decltype(stage)::value;
+                constexpr uint32_t phi = (st * kQtStage + 4 * kQtBox) >> 4;
+                const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 8 * st;
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t id = idesc_mx_e4m3_mn(128, 64, k);
+                        const uint32_t a = k_lo + ((st * kQtStage + d * kQtBox + 4096 * k) >> 4);
+                        mma_mx_e4m3_w(tmem + kQtColO + 64 * d, a, kHi128, k_lo + phi + 128 * k, kHi64, id, sfa, sfb,
+                                      k > 0 ? 1u : first);
+                        mma_mx_e4m3_w(tmem + kQtColO + 64 * d, a, kHi128, p_lo + 128 * k, kHi64, id, sfa, sfb + 4, 1);
+                    }
+                    mma_commit(&ms.free_[st][d]);
+                }
+                mma_commit(&ms.free_[st][4]);
+                mma_commit(&ms.pv_done);
+            };
+            using S0 = std::integral_constant<int, 0>;
+            using S1 = std::integral_constant<int, 1>;
+            bool ok = true;
+            for (uint32_t items = 0; left > 0 && ok; ++items) {
+                const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
+                ok = mbar_wait_bounded(&ms.q_ready, items & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                ok = (ci & 1) ? scores(S1(), ci) : scores(S0(), ci);
+                for (int i = 0; i < take && ok; ++i, ++ci) {
+                    // the next chunk's scores overlap this chunk's softmax
+                    if (i + 1 < take) {
+                        ok = mbar_wait_bounded(&ms.s_free, ci & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        ok = (ci & 1) ? scores(S0(), ci + 1) : scores(S1(), ci + 1);
+                        if (!ok) break;
+                    }
+                    ok = mbar_wait_bounded(&ms.p_ready, ci & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (ci & 1) output(S1(), i > 0);
+                    else output(S0(), i > 0);
+                }
+                left -= take;
+                if (left > 0) wk.next(p);
+            }
+            mma_commit(&ms.mma_done);
+            mbar_drain(&ms.mma_done, 0);
+        }
+        __syncwarp();
+    } else {
+        // ---- queries, softmax, output: thread = token 32 q4 + lane of the chunk, rows 32 g ..
+        const int g = (warp - 2) >> 2, q4 = warp & 3, tok = 32 * q4 + lane;
+        const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
+        uint32_t gph = 0;
+        auto group_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.grp[g]);
+            return qt_warp_wait(&ms.grp[g], gph++ & 1, abort);
+        };
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_st1(tl + kQtColSfa + k, 0x7f7f7f7fu);  // V is not scaled
+        long long unit = wk.begin;
+        QaSplit sp;
+        sp.b = sp.t = sp.lo_slot = 0;
+        sp.c_hi = -1;
+        int slot = 2 * cta;
+        bool ok = true;
+        for (uint32_t items = 0; left > 0 && ok; ++items, slot = 2 * cta + 1) {
+            const QaItem it = wk.item;
+            const int take = (int)min((long long)(it.chunks - wk.off), left);
+            const bool first = wk.off == 0, whole = first && take == it.chunks;
+            if (first && !whole) {
+                sp.b = it.b;
+                sp.t = it.t;
+                sp.lo_slot = slot;
+                sp.c_hi = wk.owner(unit + it.chunks - 1);
+            }
+            const int r0 = it.t * kQaTile, R = it.nq * p.H;
+            // query rows as E4M3 pairs: 8 rows a warp, four lanes a row
+            {
+                constexpr int kPer = kQtD / 8 / 4;  // 16-byte pieces of a row per lane
+                const int r = 8 * (warp - 2) + (lane >> 2);
+                const bool in = r0 + r < R;
+                const int tq = in ? (r0 + r) / p.H : 0, hd = in ? (r0 + r) - tq * p.H : 0;
+                const uint4 *src = (const uint4 *)(p.q + (size_t)(it.q0 + tq) * p.q_stride + (size_t)hd * kQtD) + (lane & 3);
+                uint4 v[kPer];
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) v[j] = in ? __ldg(src + 4 * j) : make_uint4(0, 0, 0, 0);
+                uint32_t mx = 0;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const uint32_t *u = (const uint32_t *)&v[j];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = max(mx, max((u[i] << 16) & 0x7fffffffu, u[i] & 0x7fff0000u));
+                }
+                mx = max(mx, __shfl_xor_sync(~0u, mx, 1));
+                mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
+                const bool bad = mx >= 0x7f800000u;
+                const int a = min(mx < 0x00800000u ? 0 : 7 - ((int)(mx >> 23) - 127), 100);
+                const float f = bad ? 0.f : qc_pow2(a);
+                // the item before: its staged output has been read
+                if (items > 0 && !qt_warp_wait(&ms.item_done, (items - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int pc = (lane & 3) + 4 * j;  // 8 elements each
+                    const uint32_t *u = (const uint32_t *)&v[j];
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t w[2], x[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint32_t two = bad ? 0u : u[2 * i + k];
+                            const uint32_t h16 = f32x2_to_f16x2(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xffff0000u) * f);
+                            w[k] = f16x2_to_e4m3x2(h16);
+                            x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));
+                        }
+                        hi[i] = w[0] | w[1] << 16;
+                        lo[i] = x[0] | x[1] << 16;
+                    }
+                    // 16-byte pieces: c ^ (row & 7) in 128-byte rows, c ^ (row / 2 & 3) in the rope's 64-byte
+                    // rows; the same for row r + 64
+                    const int d = pc >> 4, c = (pc & 15) >> 1;
+                    const int rs = d < 4 ? 128 : 64, ch = d < 4 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                    uint8_t *at = sQ + d * kQtBox + r * rs + ch * 16 + (pc & 1) * 8;
+                    *(uint2 *)at = make_uint2(hi[0], hi[1]);
+                    *(uint2 *)(at + 64 * rs) = make_uint2(lo[0], lo[1]);
+                }
+                if ((lane & 3) == 0) {
+                    ms.c[r] = bad ? -0.f : qc_pow2(-a) * p.scale_log2;
+                    ms.lim[r] = in ? W::sees(p, it.nq, it.len, tq) : 0;
+                    if (bad && first) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+                }
+            }
+            fence_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.q_ready);
+            ok = group_sync();  // c and lim of the rows of this group come from its own four warps
+            if (!ok) break;
+
+            const float c_own = ms.c[32 * g + lane];
+            float l[32], mref = 0.f;  // mref: the reference of row 32 g + lane
+#pragma unroll
+            for (int j = 0; j < 32; ++j) l[j] = 0.f;
+            // every row of the tile sees at least what its first row sees
+            const int all_see = W::sees(p, it.nq, it.len, r0 / p.H);
+            for (int i = 0; i < take; ++i, ++ci) {
+                const int base = (wk.off + i) * kQtKeys, st = ci & 1;
+                ok = qt_warp_wait(&ms.s_full, ci & 1, abort) && qt_warp_wait(&ms.full[st][0], (ci >> 1) & 1, abort);
+                if (!ok) break;
+                tc_fence_after();
+                float t[32];
+                {
+                    uint32_t a[2][16], b[2][16];
+                    tmem_ld16_issue(tl + kQtColS + 32 * g, a[0]);
+                    tmem_ld16_issue(tl + kQtColS + 64 + 32 * g, b[0]);
+                    tmem_ld16_issue(tl + kQtColS + 32 * g + 16, a[1]);
+                    tmem_ld16_issue(tl + kQtColS + 64 + 32 * g + 16, b[1]);
+                    tmem_ld_wait_tied(a[0]);
+                    tmem_ld_wait_tied(a[1]);
+                    tmem_ld_wait_tied(b[0]);
+                    tmem_ld_wait_tied(b[1]);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        t[j] = __fmaf_rn(__uint_as_float(b[j >> 4][j & 15]), 0.0625f, __uint_as_float(a[j >> 4][j & 15]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.s_free);
+                const bool masked = base + kQtKeys > all_see;
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const int4 m = *(const int4 *)&ms.lim[32 * g + j];
+                        if (base + tok >= m.x) t[j] = -INFINITY;
+                        if (base + tok >= m.y) t[j + 1] = -INFINITY;
+                        if (base + tok >= m.z) t[j + 2] = -INFINITY;
+                        if (base + tok >= m.w) t[j + 3] = -INFINITY;
+                    }
+                    const int nvalid = max(0, it.len - base);
+                    if (nvalid < kQtKeys) {
+                        // no tokens here: zero value rows, so that weights of 0 meet finite codes
+                        uint8_t *kb = sK + st * kQtStage + nvalid * 128;
+                        const int pieces = (kQtKeys - nvalid) * 8;  // per box
+                        for (int x = tid - 64; x < pieces; x += 256)
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) *(uint4 *)(kb + d * kQtBox + x * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                // block maxima (the lanes' 32 tokens are one scale block of one page; the
+                // factor is positive, so the maximum of the raw scores is the one), then
+                // lane j prepares row j: b, and the exponent's addend e + 8 - b
+                float *wrow = ms.w[warp - 2];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 m = make_float4(redux_max(t[j]), redux_max(t[j + 1]), redux_max(t[j + 2]), redux_max(t[j + 3]));
+                    if (lane == 0) *(float4 *)(wrow + j) = m;
+                }
+                const int e = ms.e[st][q4 >> 1];
+                const float fe = (float)e, ks = qc_pow2(e);
+                __syncwarp();
+                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c_own * ks, fe), -16384.f), 16383.f));
+                ms.b[g][ci & 1][q4][lane] = (int16_t)(int)bf;
+                __syncwarp();
+                wrow[lane] = (fe + 8.f) - bf;
+                __syncwarp();
+                // weights
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 c = *(const float4 *)&ms.c[32 * g + j], x = *(const float4 *)(wrow + j);
+                    t[j] = qt_ex2(__fmaf_rn(t[j], c.x * ks, x.x));
+                    t[j + 1] = qt_ex2(__fmaf_rn(t[j + 1], c.y * ks, x.y));
+                    t[j + 2] = qt_ex2(__fmaf_rn(t[j + 2], c.z * ks, x.z));
+                    t[j + 3] = qt_ex2(__fmaf_rn(t[j + 3], c.w * ks, x.w));
+                }
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const int4 m = *(const int4 *)&ms.lim[32 * g + j];
+                        if (base + tok >= m.x) t[j] = 0.f;
+                        if (base + tok >= m.y) t[j + 1] = 0.f;
+                        if (base + tok >= m.z) t[j + 2] = 0.f;
+                        if (base + tok >= m.w) t[j + 3] = 0.f;
+                    }
+                }
+                // their two E4M3 terms
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint32_t w[2], x[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t h16 = f32x2_to_f16x2(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
+                        w[k] = f16x2_to_e4m3x2(h16);
+                        x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));
+                    }
+                    hi[j] = w[0] | w[1] << 16;
+                    lo[j] = x[0] | x[1] << 16;
+                }
+                // Phi over the chunk's rope box (its scores are done)
+                const int sw = (tok >> 1) & 3;
+                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
+                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                ok = group_sync();
+                if (!ok) break;
+                int bq[4], bm = -32768;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bq[k] = ms.b[g][ci & 1][k][lane];
+                    bm = max(bm, bq[k]);
+                }
+                const bool move = i == 0 || (float)bm - mref > (float)kQtMoveLog2;
+                if (__any_sync(~0u, move)) {  // the same in the group's four warps
+                    const float mnew = move ? (float)bm : mref;
+                    const float f = i == 0 ? 0.f : qt_ex2(mref - mnew);
+                    mref = mnew;
+                    if (i > 0) {
+                        ok = qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) l[j] *= __shfl_sync(~0u, f, j);
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k) {
+                            float v[16];
+                            uint32_t u[16];
+                            const uint32_t at = tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1);
+                            tmem_ld16(at, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * __shfl_sync(~0u, f, 16 * (k & 1) + j));
+                            tmem_st16(at, u);
+                        }
+                    }
+                }
+                const int m_int = (int)mref;
+                // scale words of row 32 g + lane: 2^(b - 8 - M) for hi, 2^-4 of it for lo, one byte per 32 tokens
+                {
+                    uint32_t wh = 0;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) wh |= (uint32_t)min(max(bq[k] - m_int + (127 - 8), 4), 250) << (8 * k);
+                    tmem_st1(tl + kQtColSfb + 8 * st + g, wh);
+                    tmem_st1(tl + kQtColSfb + 8 * st + 4 + g, wh - 0x04040404u);
+                }
+                // Plo once the chunk before has been read
+                if (ci > 0 && !qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *pl = sP + tok * 64;
+                *(uint4 *)(pl + ((2 * g) ^ sw) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *(uint4 *)(pl + ((2 * g + 1) ^ sw) * 16) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                fence_async_smem();
+                tmem_st_wait();
+                tc_fence_before();
+                // lane j: what a weight of row j adds to the sum, 2^(b - 8 - M - e)
+                wrow[lane] = __int_as_float(max((int)bf - m_int - e + (127 - 8), 0) << 23);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.p_ready);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 x = *(const float4 *)(wrow + j);
+                    l[j] = __fmaf_rn(t[j], x.x, l[j]);
+                    l[j + 1] = __fmaf_rn(t[j + 1], x.y, l[j + 1]);
+                    l[j + 2] = __fmaf_rn(t[j + 2], x.z, l[j + 2]);
+                    l[j + 3] = __fmaf_rn(t[j + 3], x.w, l[j + 3]);
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            // row sums: lane j ends with the sum of row 32 g + j over the warp's tokens, then over the four warps
+#pragma unroll
+            for (int w = 16; w > 0; w >>= 1) {
+#pragma unroll
+                for (int k = 0; k < w; ++k) {
+                    const bool up = (lane & w) != 0;
+                    const float send = up ? l[k] : l[k + w], keep = up ? l[k + w] : l[k];
+                    l[k] = keep + __shfl_xor_sync(~0u, send, w);
+                }
+            }
+            ms.w[warp - 2][lane] = l[0];
+            ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const float lsum = (ms.w[4 * g][lane] + ms.w[4 * g + 1][lane]) + (ms.w[4 * g + 2][lane] + ms.w[4 * g + 3][lane]);
+            const bool bad = __float_as_uint(c_own) == 0x80000000u;
+            const float nan = __uint_as_float(0x7fffffffu);
+            const int row = 32 * g + lane, r = r0 + row;
+            if (q4 == 0) {
+                if (!whole) {
+                    p.part_ml[slot * kQaTile + row] = make_float2(mref, bad ? nan : lsum);
+                } else if (r < R && p.lse) {
+                    const int tq = it.q0 + r / p.H, hd = r % p.H;
+                    p.lse[(size_t)tq * p.H + hd] = bad ? nan : lsum > 0.f ? (mref + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+                }
+            }
+            if (!whole) {
+                float *dst = p.part_o + ((size_t)slot * kQaTile + 32 * g) * kQtDV + 32 * q4 + lane;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float v[16];
+                    tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) dst[(16 * (k & 1) + j) * kQtDV + 128 * (k >> 1)] = v[j];
+                }
+            } else {
+                // staged over the queries (every score is done), then whole rows
+                float *inv = (float *)ms.b + 32 * (warp - 2);  // no block exponent is read any more
+                inv[lane] = bad ? nan : lsum > 0.f ? 1.f / lsum : 0.f;
+                __syncwarp();
+                uint8_t *out = sQ + 32 * g * kQtOutPitch + (32 * q4 + lane) * 2;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    float v[16];
+                    tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 x = *(const float4 *)(inv + 16 * (k & 1) + j);
+                        const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            *(__nv_bfloat16 *)(out + (16 * (k & 1) + j + y) * kQtOutPitch + 256 * (k >> 1)) = __float2bfloat16_rn(v[j + y] * f[y]);
+                    }
+                }
+                ok = group_sync();
+                if (!ok) break;
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    const int rw = 32 * g + 8 * q4 + k;
+                    if (r0 + rw >= R) break;
+                    const int tq = (r0 + rw) / p.H, hd = r0 + rw - tq * p.H;
+                    uint4 *dst = (uint4 *)(p.o + (size_t)(it.q0 + tq) * p.o_stride + (size_t)hd * kQtDV);
+                    const uint4 *from = (const uint4 *)(sQ + rw * kQtOutPitch);
+                    dst[lane] = from[lane];
+                    dst[lane + 32] = from[lane + 32];
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.item_done);
+            left -= take;
+            unit += it.chunks - wk.off;
+            if (left > 0) wk.next(p);
+        }
+        if (tid == 64) p.split[cta] = sp;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (ms.abort) {
+        if (tid == 0) {
+            set_error(p.err, DSPARK_ERR_TIMEOUT);
+            for (int s = 0; s < 2; ++s)
+                for (int d = 0; d < 5; ++d)
+                    if (ms.issued[s][d]) mbar_drain(&ms.full[s][d], ms.issued[s][d] >> 1);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+cudaError_t launch_qattn_tc(const QaParams &p, int grid, cudaStream_t st) {
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(qattn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQtSmem);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    // the pool as 16-bit elements: boxes of 128 (64) bytes of 64 tokens
+    CUtensorMap dims, rope;
+    if (!encode_u16_map(&dims, p.codes, (uint64_t)p.n_pages * kQcPage, kQtD, 128, kQcPage) ||
+        !encode_u16_map(&rope, p.codes, (uint64_t)p.n_pages * kQcPage, kQtD, 64, kQcPage))
+        return cudaErrorInvalidValue;
+    return launch_pdl(qattn_tc_kernel, dim3(grid), dim3(kQtThreads), (size_t)kQtSmem, st, dims, rope, p);
+}
+
+}  // namespace ds

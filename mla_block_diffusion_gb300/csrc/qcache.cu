@@ -404,7 +404,7 @@ dspark_status check_cache(const dspark_qcache_t *c, bool plan) {
     if (c->n_layers < 1) return DSPARK_ERR_SHAPE;
     for (int l = 0; l < c->n_layers; ++l) {
         if (!c->codes[l] || !c->scales[l]) return DSPARK_ERR_NULL;
-        if (!ok16(c->codes[l]) || !ok16(c->scales[l])) return DSPARK_ERR_ALIGN;
+        if (!ok16(c->codes[l]) || ((uintptr_t)c->scales[l] & 3u)) return DSPARK_ERR_ALIGN;
     }
     return DSPARK_OK;
 }

@@ -47,6 +47,8 @@ struct QaParams {
     int *err;
 };
 
+// The full latent width (512 + 64) on the 5th-generation tensor core.
+cudaError_t launch_qattn_tc(const QaParams &p, int grid, cudaStream_t st);
 cudaError_t launch_qattn(const QaParams &p, int kv_lora, int d_rope, int num_sms, cudaStream_t st);
 
 }  // namespace ds

@@ -123,7 +123,10 @@ def test_append_layers(L):
     c = cache()
     c.codes[1] = None
     assert L.dspark_qcache_append(C.byref(c), *ok) == NULL
-    c.codes[1] = P(2) + 1
+    c.codes[1] = P(2) + 8
+    assert L.dspark_qcache_append(C.byref(c), *ok) == ALIGN
+    c = cache()
+    c.scales[1] = P(4) + 2
     assert L.dspark_qcache_append(C.byref(c), *ok) == ALIGN
     # nothing to do is no error
     assert L.dspark_qcache_append(C.byref(cache()), None, 0, 576, 0, None, 0, None, 0, P(50), 1024, None) == 0
