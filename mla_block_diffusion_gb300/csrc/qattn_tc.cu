@@ -35,12 +35,12 @@
 // an output step (N = 64, bound by the 6 KB of operands it reads from shared
 // memory), so a chunk is 1165 + 1629 clocks against 2177 at the full rate.
 //
-// Roles (10 warps): warp 0 TMA producer; warp 1 MMA issuer and tensor-memory
-// owner; warps 2-9 queries, softmax and output (a thread holds one token of 32
-// rows). All waits are bounded; a timeout raises DSPARK_ERR_TIMEOUT.
+// Roles (12 warps): warp 0 TMA producer; warp 1 issues the scores (and owns tensor
+// memory), warp 2 the outputs, so that whichever of the two is ready keeps the
+// tensor core busy; warps 4-11 queries, softmax and output (a thread holds one
+// token of 32 rows) with the registers that the first four give up. All waits are
+// bounded; a timeout raises DSPARK_ERR_TIMEOUT.
 #include <math.h>
-
-#include <type_traits>
 
 #include "e4m3.cuh"
 #include "internal.h"
@@ -49,7 +49,9 @@
 namespace ds {
 
 constexpr int kQtKeys = 128;                       // tokens per chunk
-constexpr int kQtThreads = 320;
+constexpr int kQtThreads = 384;
+constexpr int kQtSoft0 = 4;                        // first softmax warp; registers: 168 x 384 = 88 x 128 + 208 x 256
+constexpr int kQtRegsIssue = 88, kQtRegsSoft = 208;
 constexpr int kQtD = 576, kQtDV = 512;
 constexpr int kQtBox = kQtKeys * 128;              // bytes: 128 tokens x 128 dims
 constexpr int kQtRope = kQtKeys * 64;              // 128 tokens x 64 dims
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.q_ready, 8);
         mbar_init(&ms.item_done, 8);
-        mbar_init(&ms.mma_done, 1);
+        mbar_init(&ms.mma_done, 2);
         mbar_init(&ms.grp[0], 4);
         mbar_init(&ms.grp[1], 4);
         ms.abort = 0;
@@ -142,6 +144,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     volatile int *abort = &ms.abort;
     uint32_t ci = 0;  // chunks of this CTA so far
 
+    if (warp < kQtSoft0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQtRegsIssue));
     if (warp == 0) {
         // ---- producer: page numbers and scales 32 pages at a time, one block ahead
         bool ok = true;
@@ -209,74 +213,69 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (left > 0) wk.next(p);
         }
     } else if (warp == 1) {
+        // ---- scores: chunk ci + 1 while the softmax works on chunk ci
         if (lane == 0) {
-            // Everything about an operand but its stage is a constant added to one word: the
-            // issuing thread shares its scheduler with softmax warps and has about 50
-            // clocks for each MMA.
-            const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sK)), p_lo = sdesc_lo(smem_u32(sP));
-            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4);
-            auto scores = [&](auto stage, uint32_t x) -> bool {
-                constexpr int st = decltype(stage)::value;
-                constexpr uint32_t id = idesc_e4m3_f32(128, 128);
-                const uint32_t par = (x >> 1) & 1;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                    if (!mbar_wait_bounded(&ms.full[st][d], par, abort)) return false;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_e4m3_w(tmem + kQtColS, k_lo + ((st * kQtStage + d * kQtBox + 32 * k) >> 4), kHi128,
-                                   q_lo + ((d * kQtBox + 32 * k) >> 4), kHi128, id, d > 0 || k > 0);
-                }
-                if (!mbar_wait_bounded(&ms.full[st][4], par, abort)) return false;
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    mma_e4m3_w(tmem + kQtColS, k_lo + ((st * kQtStage + 4 * kQtBox + 32 * k) >> 4), kHi64,
-                               q_lo + ((4 * kQtBox + 32 * k) >> 4), kHi64, id, 1);
-                mma_commit(&ms.s_full);
-                return true;
-            };
-            auto output = [&](auto stage, uint32_t first) {
-                constexpr int st = decltype(stage)::value;
-                constexpr uint32_t phi = (st * kQtStage + 4 * kQtBox) >> 4;
-                const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 8 * st;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t id = idesc_mx_e4m3_mn(128, 64, k);
-                        const uint32_t a = k_lo + ((st * kQtStage + d * kQtBox + 4096 * k) >> 4);
-                        mma_mx_e4m3_w(tmem + kQtColO + 64 * d, a, kHi128, k_lo + phi + 128 * k, kHi64, id, sfa, sfb,
-                                      k > 0 ? 1u : first);
-                        mma_mx_e4m3_w(tmem + kQtColO + 64 * d, a, kHi128, p_lo + 128 * k, kHi64, id, sfa, sfb + 4, 1);
-                    }
-                    mma_commit(&ms.free_[st][d]);
-                }
-                mma_commit(&ms.free_[st][4]);
-                mma_commit(&ms.pv_done);
-            };
-            using S0 = std::integral_constant<int, 0>;
-            using S1 = std::integral_constant<int, 1>;
+            // everything about an operand but its stage is a constant added to one word: the
+            // issuing thread shares its scheduler with softmax warps
+            const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sK));
+            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4), id = idesc_e4m3_f32(128, 128);
             bool ok = true;
             for (uint32_t items = 0; left > 0 && ok; ++items) {
                 const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
                 ok = mbar_wait_bounded(&ms.q_ready, items & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                ok = (ci & 1) ? scores(S1(), ci) : scores(S0(), ci);
                 for (int i = 0; i < take && ok; ++i, ++ci) {
-                    // the next chunk's scores overlap this chunk's softmax
-                    if (i + 1 < take) {
-                        ok = mbar_wait_bounded(&ms.s_free, ci & 1, abort);
+                    ok = i == 0 || mbar_wait_bounded(&ms.s_free, (ci - 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t st = ci & 1, par = (ci >> 1) & 1;
+                    uint32_t a = k_lo + st * (kQtStage >> 4), b = q_lo;
+#pragma unroll 1
+                    for (int d = 0; d < 4; ++d, a += kQtBox >> 4, b += kQtBox >> 4) {
+                        ok = mbar_wait_bounded(&ms.full[st][d], par, abort);
                         if (!ok) break;
-                        tc_fence_after();
-                        ok = (ci & 1) ? scores(S0(), ci + 1) : scores(S1(), ci + 1);
-                        if (!ok) break;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, k > 0 ? 1u : (uint32_t)(d > 0));
                     }
+                    ok = ok && mbar_wait_bounded(&ms.full[st][4], par, abort);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) mma_e4m3_w(tmem + kQtColS, a + 2 * k, kHi64, b + 2 * k, kHi64, id, 1);
+                    mma_commit(&ms.s_full);
+                }
+                left -= take;
+                if (left > 0) wk.next(p);
+            }
+            mma_commit(&ms.mma_done);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---- outputs
+        if (lane == 0) {
+            const uint32_t k_lo = sdesc_lo(smem_u32(sK)), p_lo = sdesc_lo(smem_u32(sP));
+            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4);
+            bool ok = true;
+            while (left > 0 && ok) {
+                const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
+                for (int i = 0; i < take; ++i, ++ci) {
                     ok = mbar_wait_bounded(&ms.p_ready, ci & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    if (ci & 1) output(S1(), i > 0);
-                    else output(S0(), i > 0);
+                    const uint32_t st = ci & 1, phi = k_lo + st * (kQtStage >> 4) + (4 * kQtBox >> 4);
+                    const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 8 * st, first = i > 0;
+                    uint32_t a = k_lo + st * (kQtStage >> 4), d_col = tmem + kQtColO;
+#pragma unroll 1
+                    for (int d = 0; d < 4; ++d, a += kQtBox >> 4, d_col += 64) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t id = idesc_mx_e4m3_mn(128, 64, k);
+                            mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, phi + 128 * k, kHi64, id, sfa, sfb, k > 0 ? 1u : first);
+                            mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, p_lo + 128 * k, kHi64, id, sfa, sfb + 4, 1);
+                        }
+                        mma_commit(&ms.free_[st][d]);
+                    }
+                    mma_commit(&ms.free_[st][4]);
+                    mma_commit(&ms.pv_done);
                 }
                 left -= take;
                 if (left > 0) wk.next(p);
@@ -285,9 +284,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             mbar_drain(&ms.mma_done, 0);
         }
         __syncwarp();
+    }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQtRegsSoft));
         // ---- queries, softmax, output: thread = token 32 q4 + lane of the chunk, rows 32 g ..
-        const int g = (warp - 2) >> 2, q4 = warp & 3, tok = 32 * q4 + lane;
+        const int g = (warp - kQtSoft0) >> 2, q4 = warp & 3, tok = 32 * q4 + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
         uint32_t gph = 0;
         auto group_sync = [&]() {
@@ -317,7 +318,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             // query rows as E4M3 pairs: 8 rows a warp, four lanes a row
             {
                 constexpr int kPer = kQtD / 8 / 4;  // 16-byte pieces of a row per lane
-                const int r = 8 * (warp - 2) + (lane >> 2);
+                const int r = 8 * (warp - kQtSoft0) + (lane >> 2);
                 const bool in = r0 + r < R;
                 const int tq = in ? (r0 + r) / p.H : 0, hd = in ? (r0 + r) - tq * p.H : 0;
                 const uint4 *src = (const uint4 *)(p.q + (size_t)(it.q0 + tq) * p.q_stride + (size_t)hd * kQtD) + (lane & 3);
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         // no tokens here: zero value rows, so that weights of 0 meet finite codes
                         uint8_t *kb = sK + st * kQtStage + nvalid * 128;
                         const int pieces = (kQtKeys - nvalid) * 8;  // per box
-                        for (int x = tid - 64; x < pieces; x += 256)
+                        for (int x = tid - 32 * kQtSoft0; x < pieces; x += 256)
 #pragma unroll
                             for (int d = 0; d < 4; ++d) *(uint4 *)(kb + d * kQtBox + x * 16) = make_uint4(0, 0, 0, 0);
                     }
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 // block maxima (the lanes' 32 tokens are one scale block of one page; the
                 // factor is positive, so the maximum of the raw scores is the one), then
                 // lane j prepares row j: b, and the exponent's addend e + 8 - b
-                float *wrow = ms.w[warp - 2];
+                float *wrow = ms.w[warp - kQtSoft0];
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 m = make_float4(redux_max(t[j]), redux_max(t[j + 1]), redux_max(t[j + 2]), redux_max(t[j + 3]));
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     l[k] = keep + __shfl_xor_sync(~0u, send, w);
                 }
             }
-            ms.w[warp - 2][lane] = l[0];
+            ms.w[warp - kQtSoft0][lane] = l[0];
             ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
@@ -587,7 +588,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
             } else {
                 // staged over the queries (every score is done), then whole rows
-                float *inv = (float *)ms.b + 32 * (warp - 2);  // no block exponent is read any more
+                float *inv = (float *)ms.b + 32 * (warp - kQtSoft0);  // no block exponent is read any more
                 inv[lane] = bad ? nan : lsum > 0.f ? 1.f / lsum : 0.f;
                 __syncwarp();
                 uint8_t *out = sQ + 32 * g * kQtOutPitch + (32 * q4 + lane) * 2;
@@ -624,7 +625,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             unit += it.chunks - wk.off;
             if (left > 0) wk.next(p);
         }
-        if (tid == 64) p.split[cta] = sp;
+        if (tid == 32 * kQtSoft0) p.split[cta] = sp;
     }
     tc_fence_before();
     __syncthreads();
