@@ -299,10 +299,14 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         const int g = (warp - kQtSoft0) >> 2, q4 = warp & 3, tok = 32 * q4 + lane;
         const uint32_t tl = tmem + ((uint32_t)(32 * q4) << 16);
         uint32_t gph = 0;
-        auto group_sync = [&]() {
+        auto group_arrive = [&]() {
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.grp[g]);
-            return qt_warp_wait(&ms.grp[g], gph++ & 1, abort);
+        };
+        auto group_wait = [&]() { return qt_warp_wait(&ms.grp[g], gph++ & 1, abort); };
+        auto group_sync = [&]() {
+            group_arrive();
+            return group_wait();
         };
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_st1(tl + kQtColSfa + k, 0x7f7f7f7fu);  // V is not scaled
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 ms.b[g][ci & 1][q4][lane] = (int16_t)(int)bf;
                 __syncwarp();
                 wrow[lane] = (fe + 8.f) - bf;
-                __syncwarp();
+                group_arrive();  // the wait comes after the weights
                 // weights
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
@@ -488,12 +492,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     hi[j] = w[0] | w[1] << 16;
                     lo[j] = x[0] | x[1] << 16;
                 }
-                // Phi over the chunk's rope box (its scores are done)
-                const int sw = (tok >> 1) & 3;
-                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
-                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                ok = group_sync();
+                ok = group_wait();
                 if (!ok) break;
                 int bq[4], bm = -32768;
 #pragma unroll
@@ -533,6 +532,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     tmem_st1(tl + kQtColSfb + 8 * st + g, wh);
                     tmem_st1(tl + kQtColSfb + 8 * st + 4 + g, wh - 0x04040404u);
                 }
+                // Phi over the chunk's rope box (its scores are done)
+                const int sw = (tok >> 1) & 3;
+                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
+                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 // Plo once the chunk before has been read
                 if (ci > 0 && !qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort)) {
                     ok = false;
