@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
             sp.b = it.b;
             sp.t = it.t;
             sp.lo_slot = slot;
-            sp.c_hi = wk.owner(unit + it.chunks - 1);
+            sp.c_hi = wk.last_cta(unit);
         }
         const int r0 = it.t * kQaTile, R = it.nq * p.H;
         __syncthreads();

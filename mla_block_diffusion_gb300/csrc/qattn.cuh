@@ -3,13 +3,23 @@
 //
 // An item is one tile of TILE query rows (token-major, heads inside) of one
 // request; its units are the chunks of CH cached tokens that its last query
-// sees (one unit if none: the item still writes its outputs). The units of all
-// items, in order, are cut into one equal range per CTA whatever the requests'
-// lengths, so ragged batches leave no CTA idle. An item that lies in one
-// range is finished there; one that is cut leaves a partial per CTA (fp32
-// output, reference and sum per row) for the combine kernel, which adds them in
-// CTA order: the result does not depend on timing. A CTA cuts at most the items
-// at its two ends: slot 2c holds its first piece, slot 2c + 1 a later one.
+// sees (one unit if none: the item still writes its outputs). Two ways to divide
+// them, whatever the requests' lengths:
+//   - pieces: an item of n units is cut into ceil(n / per) equal pieces, one per
+//     CTA, with the least `per` that the grid holds by either of two estimates;
+//   - ranges: the units of all items, in order, are cut into one equal range per
+//     CTA, which leaves no CTA idle but gives many of them two or more items.
+// A further item costs a CTA about QaWork::kItemCost units (its queries in, its
+// output out, the pipeline drained and refilled), so the division with the
+// smaller maximum of units, items counted so, is taken: pieces when items are
+// fewer than CTAs and of like size, ranges otherwise. (One block of 7 tokens and
+// 64 heads over 4096 tokens: 7 items of 32 chunks in 16 pieces each, against
+// ranges of 1.5 chunks that give six CTAs a second item.)
+// An item that one CTA holds whole is finished there; one that is cut leaves a
+// partial per CTA (fp32 output, reference and sum per row) for the combine
+// kernel, which adds them in CTA order: the result does not depend on timing. A
+// range cuts at most the items at its two ends: slot 2c holds CTA c's first
+// piece, slot 2c + 1 a later one.
 //
 // Lengths live on the device, so every CTA finds its own range: a scan of the
 // requests' tile counts, then of the units of all tiles dealt out to the
@@ -51,9 +61,11 @@ struct QaWork {
         return max(1, (int)((seen + CH - 1) / CH));
     }
 
+    static constexpr int kItemCost = 4;
     long long begin, end;  // this CTA's units
     long long total;
     int parts;             // CTAs with units: never more than there are units, so that no range is empty
+    int piece_hi;          // pieces: the item's last CTA; ranges: -1
     QaItem item;           // the item that holds `begin`
     int off;               // units of it before `begin`
 
@@ -82,13 +94,29 @@ struct QaWork {
     struct Scratch {  // shared memory that find() uses
         long long units[32];
         int tiles[32];
-        int at[4];                          // request, tile, units before `begin`
+        int at[4];                          // request, tile, units before `begin`, last CTA
+        int longest;                        // most units of an item
         int first[kQcMaxBs + 1];            // first tile of every request
         int q0[kQcMaxBs], nq[kQcMaxBs], len[kQcMaxBs];
     };
     static constexpr int kScratch = sizeof(Scratch);
 
-    // All threads of the block: this CTA's range of the grid's.
+    // The request of tile i of all, and its units.
+    static DS_DEVINL int request_of(const QaParams &p, const Scratch &s, int i) {
+        int lo = 0, hi = p.bs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s.first[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    }
+    static DS_DEVINL int units_of(const QaParams &p, const Scratch &s, int i) {
+        const int b = request_of(p, s, i);
+        return chunks(p, s.nq[b], s.len[b], i - s.first[b]);
+    }
+
+    // All threads of the block: this CTA's part of the work.
     DS_DEVINL void find(const QaParams &p, int cta, int grid, void *smem) {
         Scratch &s = *(Scratch *)smem;
         const int nt = blockDim.x, tid = threadIdx.x;
@@ -114,13 +142,7 @@ struct QaWork {
         const int run = (all_tiles + nt - 1) / nt, i0 = min(all_tiles, tid * run), i1 = min(all_tiles, i0 + run);
         auto walk = [&](long long from, bool seek) -> long long {
             if (i0 >= i1) return from;
-            int lo = 0, hi = p.bs;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s.first[mid] <= i0) lo = mid;
-                else hi = mid;
-            }
-            int b = lo;
+            int b = request_of(p, s, i0);
             for (int i = i0; i < i1; ++i) {
                 while (i >= s.first[b + 1]) ++b;
                 const int n = chunks(p, s.nq[b], s.len[b], i - s.first[b]);
@@ -133,18 +155,64 @@ struct QaWork {
             }
             return from;
         };
+        if (tid == 0) s.longest = 0;
+        // tight: the `per` that would do if items wasted half a piece each; loose: one that always does
         const long long start = scan(walk(0, false), s.units, &total);
         parts = (int)(total < grid ? total : grid);
-        if (total < (1ll << 22)) {  // grid <= 512: 32-bit divisions
-            const unsigned T = (unsigned)total, P = max(1u, (unsigned)parts);
-            begin = cta < parts ? (unsigned)cta * T / P : T;
-            end = cta < parts ? (unsigned)(cta + 1) * T / P : T;
-        } else {
-            begin = cta < parts ? (long long)cta * total / parts : total;
-            end = cta < parts ? (long long)(cta + 1) * total / parts : total;
+        piece_hi = -1;
+        bool pieces = all_tiles < grid && total < (1ll << 22);
+        int cut = 0;
+        if (pieces) {  // the same in all threads
+            const int T = (int)total;
+            const int loose = (T + grid - all_tiles - 1) / (grid - all_tiles);
+            const int tight = (2 * T + 2 * grid - all_tiles - 1) / (2 * grid - all_tiles);
+            // an item a thread: all_tiles < grid <= 512 needs up to two rounds
+            int n_tight = 0;
+            for (int i = tid; i < all_tiles; i += nt) {
+                const int n = units_of(p, s, i);
+                n_tight += (n + tight - 1) / tight;
+                atomicMax(&s.longest, n);
+            }
+            int sum;
+            scan(n_tight, s.tiles, &sum);
+            cut = sum <= grid ? tight : loose;
+            pieces = min(cut, s.longest) <= (T + grid - 1) / grid + kItemCost;
         }
-        walk(start, true);
-        __syncthreads();
+        if (pieces) {
+            // running count of pieces; the thread whose item holds piece `cta` finds it
+            const int rounds = (all_tiles + nt - 1) / nt, j0 = min(all_tiles, tid * rounds), j1 = min(all_tiles, j0 + rounds);
+            int mine_p = 0, all_p;
+            for (int i = j0; i < j1; ++i) mine_p += (units_of(p, s, i) + cut - 1) / cut;
+            __syncthreads();  // scan's words are free again
+            int at_p = scan(mine_p, s.tiles, &all_p);
+            for (int i = j0; i < j1; ++i) {
+                const int n = units_of(p, s, i), w = (n + cut - 1) / cut, k = cta - at_p;
+                if (k >= 0 && k < w) {
+                    const int b = request_of(p, s, i);
+                    s.at[0] = b;
+                    s.at[1] = i - s.first[b];
+                    s.at[2] = (int)((unsigned)k * (unsigned)n / (unsigned)w);
+                    s.at[3] = at_p + w - 1;
+                    s.longest = (int)((unsigned)(k + 1) * (unsigned)n / (unsigned)w);  // where the piece ends
+                }
+                at_p += w;
+            }
+            __syncthreads();
+            begin = cta < all_p ? s.at[2] : 0;
+            end = cta < all_p ? s.longest : 0;
+            piece_hi = s.at[3];
+        } else {
+            if (total < (1ll << 22)) {  // grid <= 512: 32-bit divisions
+                const unsigned T = (unsigned)total, P = max(1u, (unsigned)parts);
+                begin = cta < parts ? (unsigned)cta * T / P : T;
+                end = cta < parts ? (unsigned)(cta + 1) * T / P : T;
+            } else {
+                begin = cta < parts ? (long long)cta * total / parts : total;
+                end = cta < parts ? (long long)(cta + 1) * total / parts : total;
+            }
+            walk(start, true);
+            __syncthreads();
+        }
         if (begin < end) {
             item.b = s.at[0];
             item.t = s.at[1];
@@ -168,8 +236,10 @@ struct QaWork {
         }
         item.chunks = chunks(p, item.nq, item.len, item.t);
     }
-    // The CTA whose range holds unit u.
-    DS_DEVINL int owner(long long u) const { return (int)(((u + 1) * parts - 1) / total); }
+    // The last CTA that holds units of the item that starts at unit u (of this CTA's counting).
+    DS_DEVINL int last_cta(long long u) const {
+        return piece_hi >= 0 ? piece_hi : (int)(((u + item.chunks) * parts - 1) / total);
+    }
 };
 
 }  // namespace ds

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 sp.b = it.b;
                 sp.t = it.t;
                 sp.lo_slot = slot;
-                sp.c_hi = wk.owner(unit + it.chunks - 1);
+                sp.c_hi = wk.last_cta(unit);
             }
             const int r0 = it.t * kQaTile, R = it.nq * p.H;
             // query rows as E4M3 pairs: 8 rows a warp, four lanes a row

@@ -143,7 +143,8 @@ def _mat(v) -> "Mat":
 
 
 def _stream():
-    return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the raw handle: torch.cuda.current_stream() builds a Stream object first (3 us against 0.2 us a call)
+    return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
 
 
 def _chk(fn: str, st: int):
@@ -267,9 +268,12 @@ class DSpark:
         return lib().dspark_check(self.h, None, _stream())
 
 
+_I32 = torch.int32
+
+
 def _int32(name: str, t: torch.Tensor, n: int):
     """t holds at least n contiguous int32 values on the GPU."""
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
 
 
@@ -289,7 +293,7 @@ class QCache:
                  workspace: Optional[torch.Tensor] = None):
         if len(codes) != len(scales) or len(codes) > MAX_LAYERS:
             raise ValueError("one code pool and one scale vector per layer, at most %d layers" % MAX_LAYERS)
-        self.D, self.n_heads = kv_lora + d_rope, n_heads
+        self.D, self.kv, self.layers = kv_lora + d_rope, kv_lora, len(codes)
         if n_pages is None:
             if not len(codes):
                 raise ValueError("n_pages is needed without code pools")
@@ -309,13 +313,15 @@ class QCache:
             c.codes[l], c.scales[l] = t.data_ptr(), u.data_ptr()
         # the struct holds raw device pointers: keep the tensors alive as long as it lives
         self._keep = (list(codes), list(scales), page_table)
-        self.c, self.page_table, self.n_pages = c, page_table, n_pages
+        self.c, self.ref, self.rows, self.n_pages = c, C.byref(c), int(page_table.shape[0]), n_pages
         need = lib().dspark_qcache_workspace_bytes(C.byref(c), n_heads)
         if need == 0:
             raise DSparkError("dspark_qcache_workspace_bytes", 3)
         if workspace is None:
             workspace = torch.zeros(need, dtype=torch.uint8, device=page_table.device)
-        self.ws, self.ws_bytes = workspace, workspace.numel()
+        if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous uint8 CUDA tensor, zero-filled before its first use")
+        self.ws, self.ws_ptr, self.ws_bytes = workspace, C.c_void_p(workspace.data_ptr()), workspace.numel()
 
     def plan(self, length: torch.Tensor, want: torch.Tensor, ring: torch.Tensor, ring_state: torch.Tensor,
              length_out: torch.Tensor, ring_state_out: torch.Tensor, cu_new: torch.Tensor,
@@ -326,66 +332,83 @@ class QCache:
         [bs], ``ring_state_out`` [2], ``cu_new`` [bs + 1], ``slots`` and ``positions`` (one per new token, then -1;
         their size is the most new tokens served), ``seg_row`` (first new token of every touched page, then their
         number; its size less one is the most pages served)."""
-        bs = length.numel()
+        bs, n, seg = length.numel(), self.n_pages, seg_row.numel()
         max_new = 0 if slots is None else slots.numel()
-        if bs > self.page_table.shape[0]:
+        if bs > self.rows:
             raise ValueError("more requests than rows of the page table")
-        for name, t, n in (("length", length, bs), ("want", want, bs), ("ring", ring, self.n_pages),
-                           ("ring_state", ring_state, 2), ("length_out", length_out, bs),
-                           ("ring_state_out", ring_state_out, 2), ("cu_new", cu_new, bs + 1), ("seg_row", seg_row, 1)):
-            _int32(name, t, n)
-        if slots is not None:
-            _int32("slots", slots, 0)
+        _int32("length", length, bs)
+        _int32("want", want, bs)
+        _int32("ring", ring, n)
+        _int32("ring_state", ring_state, 2)
+        _int32("length_out", length_out, bs)
+        _int32("ring_state_out", ring_state_out, 2)
+        _int32("cu_new", cu_new, bs + 1)
+        _int32("seg_row", seg_row, 1)
+        ps = pp = None
         if max_new:
+            _int32("slots", slots, 0)
             _int32("positions", positions, max_new)
+            ps, pp = slots.data_ptr(), positions.data_ptr()
         a = QPlanArgs(length.data_ptr(), want.data_ptr(), ring.data_ptr(), ring_state.data_ptr(), length_out.data_ptr(),
-                      ring_state_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr() if max_new else None,
-                      positions.data_ptr() if max_new else None, seg_row.data_ptr())
-        _chk("dspark_qcache_plan", lib().dspark_qcache_plan(C.byref(self.c), C.byref(a), bs, max_new,
-                                                            seg_row.numel() - 1, _p(self.ws), self.ws_bytes, _stream()))
+                      ring_state_out.data_ptr(), cu_new.data_ptr(), ps, pp, seg_row.data_ptr())
+        st = lib().dspark_qcache_plan(self.ref, C.byref(a), bs, max_new, seg - 1, self.ws_ptr, self.ws_bytes, _stream())
+        if st:
+            raise DSparkError("dspark_qcache_plan", st)
 
     def append(self, entries: torch.Tensor, slots: torch.Tensor, seg_row: torch.Tensor):
         """Quantise entries [n_layers, rows, kv_lora + d_rope] (bf16 or fp32, any row and layer stride) into the slots
         of dspark_qcache_plan, raising the scales of pages that need it."""
-        if entries.dim() != 3 or entries.shape[0] != self.c.n_layers or entries.shape[2] != self.D or not entries.is_cuda:
-            raise ValueError(f"entries: CUDA tensor [{self.c.n_layers}, rows, {self.D}]")
-        if entries.dtype not in (torch.bfloat16, torch.float32):
+        shape = entries.shape
+        if len(shape) != 3 or shape[0] != self.layers or shape[2] != self.D or not entries.is_cuda:
+            raise ValueError(f"entries: CUDA tensor [{self.layers}, rows, {self.D}]")
+        kind = 0 if entries.dtype is torch.bfloat16 else 1
+        if kind and entries.dtype is not torch.float32:
             raise ValueError("entries: bf16 or fp32")
-        if entries.stride(2) != 1:
+        layer_stride, row_stride, one = entries.stride()
+        if one != 1:
             raise ValueError("entries: the elements of a row are contiguous")
-        rows = min(entries.shape[1], slots.numel())
         _int32("slots", slots, 0)
         _int32("seg_row", seg_row, 1)
-        row_stride = entries.stride(1) if entries.shape[1] > 1 else self.D  # torch leaves the stride of one row open
-        _chk("dspark_qcache_append", lib().dspark_qcache_append(
-            C.byref(self.c), _p(entries), 0 if entries.dtype == torch.bfloat16 else 1, row_stride,
-            entries.stride(0), _p(slots), rows, _p(seg_row), seg_row.numel() - 1, _p(self.ws), self.ws_bytes, _stream()))
+        rows = min(shape[1], slots.numel())
+        if shape[1] <= 1:
+            row_stride = self.D  # torch leaves the stride of one row open
+        st = lib().dspark_qcache_append(self.ref, entries.data_ptr(), kind, row_stride, layer_stride, slots.data_ptr(), rows,
+                                        seg_row.data_ptr(), seg_row.numel() - 1, self.ws_ptr, self.ws_bytes, _stream())
+        if st:
+            raise DSparkError("dspark_qcache_append", st)
 
     def attend(self, layer: int, q: torch.Tensor, cu_q: torch.Tensor, length: torch.Tensor, o: torch.Tensor,
                lse: Optional[torch.Tensor] = None, causal: bool = True, scale: float = 1.0):
         """o = softmax(scale q k^T) v over one layer: q bf16 [total_q, n_heads, kv_lora + d_rope] (any token stride),
         request b's queries at cu_q[b] .. cu_q[b+1]-1, ``length`` cached tokens each; o bf16 [total_q, n_heads,
         kv_lora], lse fp32 [total_q, n_heads]."""
-        kv = self.c.kv_lora
-        if q.dim() != 3 or q.shape[2] != self.D or q.dtype != torch.bfloat16 or not q.is_cuda:
-            raise ValueError(f"q: bf16 CUDA tensor [total_q, n_heads, {self.D}]")
-        n, h = q.shape[0], q.shape[1]
-        if tuple(o.shape) != (n, h, kv) or o.dtype != torch.bfloat16 or not o.is_cuda:
+        D, kv, shape = self.D, self.kv, q.shape
+        if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_cuda:
+            raise ValueError(f"q: bf16 CUDA tensor [total_q, n_heads, {D}]")
+        n, h, _ = shape
+        if o.shape != (n, h, kv) or o.dtype is not torch.bfloat16 or not o.is_cuda:
             raise ValueError(f"o: bf16 CUDA tensor [{n}, {h}, {kv}]")
-        if n and (q.stride(2) != 1 or (h > 1 and q.stride(1) != self.D) or o.stride(2) != 1 or (h > 1 and o.stride(1) != kv)):
+        qs, qh, q1 = q.stride()
+        os, oh, o1 = o.stride()
+        if n and (q1 != 1 or o1 != 1 or h > 1 and (qh != D or oh != kv)):
             raise ValueError("q and o: the heads of a token are contiguous")
-        if lse is not None and (lse.dtype != torch.float32 or lse.numel() != n * h or not lse.is_contiguous() or not lse.is_cuda):
-            raise ValueError(f"lse: contiguous fp32 CUDA tensor [{n}, {h}]")
+        if n <= 1:  # torch leaves the stride of one token open
+            qs, os = h * D, h * kv
+        pl = None
+        if lse is not None:
+            if lse.dtype is not torch.float32 or lse.numel() != n * h or not lse.is_contiguous() or not lse.is_cuda:
+                raise ValueError(f"lse: contiguous fp32 CUDA tensor [{n}, {h}]")
+            pl = lse.data_ptr() or None
         bs = length.numel()
-        if bs > self.page_table.shape[0]:
+        if bs > self.rows:
             raise ValueError("more requests than rows of the page table")
         _int32("length", length, 1)
         _int32("cu_q", cu_q, bs + 1)
-        a = QAttnArgs(q.data_ptr() or None, q.stride(0) if n > 1 else h * self.D, cu_q.data_ptr(), length.data_ptr(), h, n,
-                      int(bool(causal)), float(scale), o.data_ptr() or None, o.stride(0) if n > 1 else h * kv,
-                      None if lse is None else lse.data_ptr())
-        _chk("dspark_qcache_attend", lib().dspark_qcache_attend(C.byref(self.c), layer, C.byref(a), bs, _p(self.ws),
-                                                                self.ws_bytes, _stream()))
+        a = QAttnArgs(q.data_ptr() or None, qs, cu_q.data_ptr(), length.data_ptr(), h, n, 1 if causal else 0, scale,
+                      o.data_ptr() or None, os, pl)
+        st = lib().dspark_qcache_attend(self.ref, layer, C.byref(a), bs, self.ws_ptr, self.ws_bytes, _stream())
+        if st:
+            raise DSparkError("dspark_qcache_attend", st)
 
     def check(self) -> int:
         """Synchronise and return (and clear) the device error word."""
