@@ -281,10 +281,11 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
 }
 
 // ---------------------------------------------------------------------------
-// Combine: the rows of items that were split, one warp per row and 128 columns
-// (a row's columns at the narrower widths), partials in CTA order. The warp's
-// lanes hold the partials' weights; eight partials are in flight at a time.
-// Bound: latency and L2 (the partials were just written).
+// Combine: the rows of items that were split, one warp per two rows and 128
+// columns (all columns at the narrower widths), partials in CTA order. The warp's
+// lanes hold the partials' weights; eight partials of each row are in flight, the
+// first of them requested together with the weights. Bound: latency and L2 (the
+// partials were just written).
 // ---------------------------------------------------------------------------
 constexpr int kQaCombineThreads = 256;
 
@@ -292,6 +293,7 @@ template <int DV>
 __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const QaParams p, int ctas) {
     __shared__ QaSplit s_list[kQaMaxGrid];
     __shared__ int s_first[kQaMaxGrid];
+    __shared__ int s_q0[kQaMaxGrid], s_rows[kQaMaxGrid];  // the item's first query token, rows from its start to the request's end
     __shared__ unsigned s_mask[kQaMaxGrid / 32];
     constexpr int kCols = DV < 128 ? DV : 128, kSub = DV / kCols;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -323,61 +325,92 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
         n_split += __popc(mask);
     }
     __syncthreads();
-    const int tasks = n_split * kQaTile * kSub, warps = gridDim.x * (kQaCombineThreads / 32);
+    for (int i = tid; i < n_split; i += kQaCombineThreads) {
+        const int q0 = p.cu_q[s_list[i].b];
+        s_q0[i] = q0;
+        s_rows[i] = (p.cu_q[s_list[i].b + 1] - q0) * p.H - s_list[i].t * kQaTile;
+    }
+    __syncthreads();
+    constexpr int kRows = 2, kDeep = 8;  // rows a warp takes at once, partials of each in flight
+    const int tasks = n_split * (kQaTile / kRows) * kSub, warps = gridDim.x * (kQaCombineThreads / 32);
+    const bool on = 4 * lane < kCols;
     for (int task = blockIdx.x * (kQaCombineThreads / 32) + (tid >> 5); task < tasks; task += warps) {
-        const int sub = task % kSub, row = task / kSub % kQaTile, li = task / kSub / kQaTile;
+        const int sub = task % kSub, row0 = task / kSub % (kQaTile / kRows) * kRows, li = task / kSub / (kQaTile / kRows);
+        const int left = s_rows[li] - row0;
+        if (left <= 0) continue;
         const QaSplit sp = s_list[li];
         const int c = s_first[li], n = sp.c_hi - c + 1;
-        const int q0 = p.cu_q[sp.b], r = sp.t * kQaTile + row;
-        if (r >= (p.cu_q[sp.b + 1] - q0) * p.H) continue;
-        // weights of up to 32 partials at a time; all of them fit into one round but for very long splits
-        float m = -INFINITY;
-        for (int k = lane; k < n; k += 32) m = fmaxf(m, __ldcg(&p.part_ml[(k == 0 ? sp.lo_slot : 2 * (c + k)) * kQaTile + row]).x);
+        auto slot = [&](int k) { return (size_t)(k == 0 ? sp.lo_slot : 2 * (c + k)); };
+        const float *src = p.part_o + (size_t)row0 * DV + sub * kCols + 4 * lane;
+        float4 v[kRows][kDeep];
+        auto fetch = [&](int k0) {
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        const float mb = m == -INFINITY ? 0.f : m;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float l = 0.f;
-        const float *src = p.part_o + (size_t)row * DV + sub * kCols + 4 * lane;
-        for (int k0 = 0; k0 < n; k0 += 32) {
-            float w = 0.f;
-            if (k0 + lane < n) {
-                const float2 ml = __ldcg(&p.part_ml[(k0 + lane == 0 ? sp.lo_slot : 2 * (c + k0 + lane)) * kQaTile + row]);
-                w = qa_ex2(ml.x - mb);
-                l += w * ml.y;
-            }
-            const int kn = min(32, n - k0);
-            for (int k = 0; k < kn; k += 8) {
-                float4 v[8];
+            for (int i = 0; i < kRows; ++i)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int kk = k0 + k + j;
-                    v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (kk < n && 4 * lane < kCols)
-                        v[j] = __ldcg((const float4 *)(src + (size_t)(kk == 0 ? sp.lo_slot : 2 * (c + kk)) * (kQaTile * DV)));
-                }
+                for (int j = 0; j < kDeep; ++j)
+                    v[i][j] = on && k0 + j < n ? __ldcg((const float4 *)(src + slot(k0 + j) * (kQaTile * DV) + i * DV))
+                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        // references and sums, lane = partial; the first partials are requested with them
+        float2 ml[kRows];
+        float m[kRows], l[kRows], w[kRows];
+        auto stats = [&](int k0, int i) {
+            return k0 + lane < n ? __ldcg(&p.part_ml[slot(k0 + lane) * kQaTile + row0 + i]) : make_float2(-INFINITY, 0.f);
+        };
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float wk = __shfl_sync(~0u, w, (k + j) & 31);
-                    o.x += wk * v[j].x;
-                    o.y += wk * v[j].y;
-                    o.z += wk * v[j].z;
-                    o.w += wk * v[j].w;
-                }
-            }
+        for (int i = 0; i < kRows; ++i) ml[i] = stats(0, i);
+        fetch(0);
+        float4 o[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            m[i] = ml[i].x;
+            for (int k0 = 32; k0 < n; k0 += 32) m[i] = fmaxf(m[i], stats(k0, i).x);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(~0u, m[i], d));
+            if (m[i] == -INFINITY) m[i] = 0.f;
+            w[i] = qa_ex2(ml[i].x - m[i]);
+            l[i] = w[i] * ml[i].y;
+            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        l = warp_sum(l);
-        const float inv = isnan(l) ? l : l > 0.f ? 1.f / l : 0.f;
-        const int tok = q0 + r / p.H, hd = r % p.H;
-        if (4 * lane < kCols) {
-            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-            uint2 u;
-            u.x = *(const uint32_t *)&lo;
-            u.y = *(const uint32_t *)&hi;
-            *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + sub * kCols + 4 * lane) = u;
+        for (int k = 0; k < n; k += kDeep) {
+            if (k > 0) {
+                fetch(k);
+                if ((k & 31) == 0) {
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i) {
+                        ml[i] = stats(k, i);
+                        w[i] = qa_ex2(ml[i].x - m[i]);
+                        l[i] += w[i] * ml[i].y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j) {
+                    const float wk = __shfl_sync(~0u, w[i], (k + j) & 31);
+                    o[i].x += wk * v[i][j].x;
+                    o[i].y += wk * v[i][j].y;
+                    o[i].z += wk * v[i][j].z;
+                    o[i].w += wk * v[i][j].w;
+                }
         }
-        if (p.lse && sub == 0 && lane == 0)
-            p.lse[(size_t)tok * p.H + hd] = isnan(l) ? l : l > 0.f ? (mb + log2f(l)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (i >= left) break;
+            const float sum = warp_sum(l[i]);
+            const float inv = isnan(sum) ? sum : sum > 0.f ? 1.f / sum : 0.f;
+            const int r = sp.t * kQaTile + row0 + i, tq = r / p.H, hd = r - tq * p.H, tok = s_q0[li] + tq;
+            if (on) {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv), hi = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
+                uint2 u;
+                u.x = *(const uint32_t *)&lo;
+                u.y = *(const uint32_t *)&hi;
+                *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + sub * kCols + 4 * lane) = u;
+            }
+            if (p.lse && sub == 0 && lane == 0)
+                p.lse[(size_t)tok * p.H + hd] = isnan(sum) ? sum : sum > 0.f ? (m[i] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        }
     }
 }
 
