@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
         // query rows as f16
         for (int r = warp; r < 64; r += 8) {
             const bool in = r0 + r < R;
-            const int tok = in ? (r0 + r) / p.H : 0, hd = in ? (r0 + r) % p.H : 0;
+            const int tok = in ? (int)W::token(p, r0 + r) : 0, hd = in ? r0 + r - tok * p.H : 0;
             const __nv_bfloat16 *src = p.q + (size_t)(it.q0 + tok) * p.q_stride + (size_t)hd * D;
             uint32_t mx = 0;
             uint4 v[(D / 8 + 31) / 32];
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
                 if (r < R) {
                     const bool bad = isnan(s_c[row]);
                     const float inv = bad ? __uint_as_float(0x7fffffffu) : l[h] > 0.f ? 1.f / l[h] : 0.f;
-                    const int tok = it.q0 + r / p.H, hd = r % p.H;
+                    const int tk = (int)W::token(p, r), tok = it.q0 + tk, hd = r - tk * p.H;
                     __nv_bfloat16 *dst = p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + half * (DV / 2) + 2 * (lane & 3);
 #pragma unroll
                     for (int n = 0; n < NV; ++n)
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
             if (i >= left) break;
             const float sum = warp_sum(l[i]);
             const float inv = isnan(sum) ? sum : sum > 0.f ? 1.f / sum : 0.f;
-            const int r = sp.t * kQaTile + row0 + i, tq = r / p.H, hd = r - tq * p.H, tok = s_q0[li] + tq;
+            const int r = sp.t * kQaTile + row0 + i, tq = (int)QaWork<kQaTile, kQcPage>::token(p, r), hd = r - tq * p.H, tok = s_q0[li] + tq;
             if (on) {
                 const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv), hi = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
                 uint2 u;

@@ -49,6 +49,10 @@ struct QaWork {
         *nq = ok ? z - a : 0;
         *len = ok ? n : 0;
     }
+    // Query token of row r of a request: r / H by the reciprocal (exact below 2^31).
+    static DS_DEVINL unsigned token(const QaParams &p, unsigned r) {
+        return (unsigned)(((unsigned long long)r * p.h_mul) >> p.h_shift);
+    }
     // total_q * H < 2^31 - TILE * 1024
     static DS_DEVINL int tiles(const QaParams &p, int nq) { return (int)(((unsigned)nq * (unsigned)p.H + TILE - 1) / TILE); }
     // Tokens that query i of nq sees.
@@ -57,7 +61,7 @@ struct QaWork {
     }
     static DS_DEVINL int chunks(const QaParams &p, int nq, int len, int t) {
         unsigned seen = (unsigned)len;
-        if (p.causal) seen = (unsigned)sees(p, nq, len, min(nq - 1, (int)((((unsigned)t + 1u) * TILE - 1u) / (unsigned)p.H)));
+        if (p.causal) seen = (unsigned)sees(p, nq, len, min(nq - 1, (int)token(p, ((unsigned)t + 1u) * TILE - 1u)));
         return max(1, (int)((seen + CH - 1) / CH));
     }
 
@@ -95,7 +99,6 @@ struct QaWork {
         long long units[32];
         int tiles[32];
         int at[4];                          // request, tile, units before `begin`, last CTA
-        int longest;                        // most units of an item
         int first[kQcMaxBs + 1];            // first tile of every request
         int q0[kQcMaxBs], nq[kQcMaxBs], len[kQcMaxBs];
     };
@@ -116,6 +119,61 @@ struct QaWork {
         return chunks(p, s.nq[b], s.len[b], i - s.first[b]);
     }
 
+    // Pieces, if their estimate is the better one. Every warp works it out for itself, a lane an item.
+    static constexpr int kPieceItems = 160, kPieceRounds = kPieceItems / 32;
+    DS_DEVINL bool find_piece(const QaParams &p, const Scratch &s, int cta, int grid, int items) {
+        const int lane = threadIdx.x & 31;
+        int u[kPieceRounds], T = 0, longest = 0;
+#pragma unroll
+        for (int r = 0; r < kPieceRounds; ++r) {
+            u[r] = 0;
+            if (32 * r < items) u[r] = 32 * r + lane < items ? min(units_of(p, s, 32 * r + lane), 1 << 22) : 0;
+            T += min(u[r], 1 << 14);
+            longest = max(longest, u[r]);
+        }
+        T = (int)__reduce_add_sync(~0u, (unsigned)T);
+        longest = (int)__reduce_max_sync(~0u, (unsigned)longest);
+        if (longest >= 1 << 14) return false;  // (the counts below stay within 32 bits)
+        // tight: would do if items wasted half a piece each; loose: always does
+        const int loose = (T + grid - items - 1) / (grid - items);
+        const int tight = (2 * T + 2 * grid - items - 1) / (2 * grid - items);
+        int n = 0;
+#pragma unroll
+        for (int r = 0; r < kPieceRounds; ++r) n += (u[r] + tight - 1) / tight;
+        const int cut = (int)__reduce_add_sync(~0u, (unsigned)n) <= grid ? tight : loose;
+        if (min(cut, longest) > (T + grid - 1) / grid + kItemCost) return false;
+        int base = 0;
+#pragma unroll
+        for (int r = 0; r < kPieceRounds; ++r) {
+            if (32 * r >= items) break;
+            const int w = (u[r] + cut - 1) / cut;
+            int inc = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(~0u, inc, d);
+                if (lane >= d) inc += o;
+            }
+            const int k = cta - (base + inc - w);
+            const unsigned hit = __ballot_sync(~0u, k >= 0 && k < w);
+            if (hit) {
+                const int src = __ffs(hit) - 1, i = 32 * r + src;
+                const int units = __shfl_sync(~0u, u[r], src), of = __shfl_sync(~0u, w, src), kk = __shfl_sync(~0u, k, src);
+                item.b = request_of(p, s, i);
+                item.t = i - s.first[item.b];
+                item.q0 = s.q0[item.b];
+                item.nq = s.nq[item.b];
+                item.len = s.len[item.b];
+                item.chunks = units;
+                off = (int)((unsigned)kk * (unsigned)units / (unsigned)of);
+                begin = off;
+                end = (int)((unsigned)(kk + 1) * (unsigned)units / (unsigned)of);
+                piece_hi = cta - kk + of - 1;
+            }
+            base += __shfl_sync(~0u, inc, 31);
+        }
+        return true;
+    }
+
     // All threads of the block: this CTA's part of the work.
     DS_DEVINL void find(const QaParams &p, int cta, int grid, void *smem) {
         Scratch &s = *(Scratch *)smem;
@@ -123,6 +181,7 @@ struct QaWork {
         // requests: their tiles, and the first tile of each
         const int per = (p.bs + nt - 1) / nt, b0 = tid * per, b1 = min(p.bs, b0 + per);
         int mine = 0, all_tiles;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             int q0, nq, len;
             request(p, b, &q0, &nq, &len, cta == 0);
@@ -132,76 +191,44 @@ struct QaWork {
             mine += tiles(p, nq);
         }
         int at = scan(mine, s.tiles, &all_tiles);
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             s.first[b] = at;
             at += tiles(p, s.nq[b]);
         }
         if (tid == 0) s.first[p.bs] = all_tiles;
         __syncthreads();
-        // units of this thread's run of tiles
-        const int run = (all_tiles + nt - 1) / nt, i0 = min(all_tiles, tid * run), i1 = min(all_tiles, i0 + run);
-        auto walk = [&](long long from, bool seek) -> long long {
-            if (i0 >= i1) return from;
-            int b = request_of(p, s, i0);
-            for (int i = i0; i < i1; ++i) {
-                while (i >= s.first[b + 1]) ++b;
-                const int n = chunks(p, s.nq[b], s.len[b], i - s.first[b]);
-                if (seek && from <= begin && begin < from + n) {
-                    s.at[0] = b;
-                    s.at[1] = i - s.first[b];
-                    s.at[2] = (int)(begin - from);
-                }
-                from += n;
-            }
-            return from;
-        };
-        if (tid == 0) s.longest = 0;
-        // tight: the `per` that would do if items wasted half a piece each; loose: one that always does
-        const long long start = scan(walk(0, false), s.units, &total);
-        parts = (int)(total < grid ? total : grid);
         piece_hi = -1;
-        bool pieces = all_tiles < grid && total < (1ll << 22);
-        int cut = 0;
-        if (pieces) {  // the same in all threads
-            const int T = (int)total;
-            const int loose = (T + grid - all_tiles - 1) / (grid - all_tiles);
-            const int tight = (2 * T + 2 * grid - all_tiles - 1) / (2 * grid - all_tiles);
-            // an item a thread: all_tiles < grid <= 512 needs up to two rounds
-            int n_tight = 0;
-            for (int i = tid; i < all_tiles; i += nt) {
-                const int n = units_of(p, s, i);
-                n_tight += (n + tight - 1) / tight;
-                atomicMax(&s.longest, n);
-            }
-            int sum;
-            scan(n_tight, s.tiles, &sum);
-            cut = sum <= grid ? tight : loose;
-            pieces = min(cut, s.longest) <= (T + grid - 1) / grid + kItemCost;
+        parts = 0;
+        begin = end = 0;
+        total = 0;
+        if (all_tiles < min(grid, kPieceItems) && find_piece(p, s, cta, grid, all_tiles)) {
+            __syncthreads();  // the scratch is free
+            return;
         }
-        if (pieces) {
-            // running count of pieces; the thread whose item holds piece `cta` finds it
-            const int rounds = (all_tiles + nt - 1) / nt, j0 = min(all_tiles, tid * rounds), j1 = min(all_tiles, j0 + rounds);
-            int mine_p = 0, all_p;
-            for (int i = j0; i < j1; ++i) mine_p += (units_of(p, s, i) + cut - 1) / cut;
-            __syncthreads();  // scan's words are free again
-            int at_p = scan(mine_p, s.tiles, &all_p);
-            for (int i = j0; i < j1; ++i) {
-                const int n = units_of(p, s, i), w = (n + cut - 1) / cut, k = cta - at_p;
-                if (k >= 0 && k < w) {
-                    const int b = request_of(p, s, i);
-                    s.at[0] = b;
-                    s.at[1] = i - s.first[b];
-                    s.at[2] = (int)((unsigned)k * (unsigned)n / (unsigned)w);
-                    s.at[3] = at_p + w - 1;
-                    s.longest = (int)((unsigned)(k + 1) * (unsigned)n / (unsigned)w);  // where the piece ends
+        // ranges: units of this thread's run of tiles
+        const int run = (all_tiles + nt - 1) / nt, i0 = min(all_tiles, tid * run), i1 = min(all_tiles, i0 + run);
+        long long start = 0;
+#pragma unroll 1
+        for (int seek = 0; seek < 2; ++seek) {
+            long long from = start;
+            if (i0 < i1) {
+                int b = request_of(p, s, i0);
+#pragma unroll 1
+                for (int i = i0; i < i1; ++i) {
+                    while (i >= s.first[b + 1]) ++b;
+                    const int n = chunks(p, s.nq[b], s.len[b], i - s.first[b]);
+                    if (seek && from <= begin && begin < from + n) {
+                        s.at[0] = b;
+                        s.at[1] = i - s.first[b];
+                        s.at[2] = (int)(begin - from);
+                    }
+                    from += n;
                 }
-                at_p += w;
             }
-            __syncthreads();
-            begin = cta < all_p ? s.at[2] : 0;
-            end = cta < all_p ? s.longest : 0;
-            piece_hi = s.at[3];
-        } else {
+            if (seek) break;
+            start = scan(from, s.units, &total);
+            parts = (int)(total < grid ? total : grid);
             if (total < (1ll << 22)) {  // grid <= 512: 32-bit divisions
                 const unsigned T = (unsigned)total, P = max(1u, (unsigned)parts);
                 begin = cta < parts ? (unsigned)cta * T / P : T;
@@ -210,9 +237,8 @@ struct QaWork {
                 begin = cta < parts ? (long long)cta * total / parts : total;
                 end = cta < parts ? (long long)(cta + 1) * total / parts : total;
             }
-            walk(start, true);
-            __syncthreads();
         }
+        __syncthreads();
         if (begin < end) {
             item.b = s.at[0];
             item.t = s.at[1];

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 constexpr int kPer = kQtD / 8 / 4;  // 16-byte pieces of a row per lane
                 const int r = 8 * (warp - kQtSoft0) + (lane >> 2);
                 const bool in = r0 + r < R;
-                const int tq = in ? (r0 + r) / p.H : 0, hd = in ? (r0 + r) - tq * p.H : 0;
+                const int tq = in ? (int)W::token(p, r0 + r) : 0, hd = in ? (r0 + r) - tq * p.H : 0;
                 const uint4 *src = (const uint4 *)(p.q + (size_t)(it.q0 + tq) * p.q_stride + (size_t)hd * kQtD) + (lane & 3);
                 uint4 v[kPer];
 #pragma unroll
@@ -354,31 +354,38 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     ok = false;
                     break;
                 }
+                // three pieces a round: the loop stays small (instruction fetch, not arithmetic, is what
+                // straight-line code that runs once costs), the registers move up instead
+#pragma unroll 1
+                for (int j0 = 0; j0 < kPer; j0 += 3) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int pc = (lane & 3) + 4 * j;  // 8 elements each
-                    const uint32_t *u = (const uint32_t *)&v[j];
-                    uint32_t hi[2], lo[2];
+                    for (int j = 0; j < 3; ++j) {
+                        const int pc = (lane & 3) + 4 * (j0 + j);  // 8 elements each
+                        const uint32_t *u = (const uint32_t *)&v[j];
+                        uint32_t hi[2], lo[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t w[2], x[2];
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t w[2], x[2];
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t two = bad ? 0u : u[2 * i + k];
-                            const uint32_t h16 = f32x2_to_f16x2(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xffff0000u) * f);
-                            w[k] = f16x2_to_e4m3x2(h16);
-                            x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t two = bad ? 0u : u[2 * i + k];
+                                const uint32_t h16 = f32x2_to_f16x2(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xffff0000u) * f);
+                                w[k] = f16x2_to_e4m3x2(h16);
+                                x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));
+                            }
+                            hi[i] = w[0] | w[1] << 16;
+                            lo[i] = x[0] | x[1] << 16;
                         }
-                        hi[i] = w[0] | w[1] << 16;
-                        lo[i] = x[0] | x[1] << 16;
+                        // 16-byte pieces: c ^ (row & 7) in 128-byte rows, c ^ (row / 2 & 3) in the rope's 64-byte
+                        // rows; the same for row r + 64
+                        const int d = pc >> 4, c = (pc & 15) >> 1;
+                        const int rs = d < 4 ? 128 : 64, ch = d < 4 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                        uint8_t *at = sQ + d * kQtBox + r * rs + ch * 16 + (pc & 1) * 8;
+                        *(uint2 *)at = make_uint2(hi[0], hi[1]);
+                        *(uint2 *)(at + 64 * rs) = make_uint2(lo[0], lo[1]);
                     }
-                    // 16-byte pieces: c ^ (row & 7) in 128-byte rows, c ^ (row / 2 & 3) in the rope's 64-byte
-                    // rows; the same for row r + 64
-                    const int d = pc >> 4, c = (pc & 15) >> 1;
-                    const int rs = d < 4 ? 128 : 64, ch = d < 4 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
-                    uint8_t *at = sQ + d * kQtBox + r * rs + ch * 16 + (pc & 1) * 8;
-                    *(uint2 *)at = make_uint2(hi[0], hi[1]);
-                    *(uint2 *)(at + 64 * rs) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+                    for (int j = 0; j + 3 < kPer; ++j) v[j] = v[j + 3];
                 }
                 if ((lane & 3) == 0) {
                     ms.c[r] = bad ? -0.f : qc_pow2(-a) * p.scale_log2;
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) l[j] = 0.f;
             // every row of the tile sees at least what its first row sees
-            const int all_see = W::sees(p, it.nq, it.len, r0 / p.H);
+            const int all_see = W::sees(p, it.nq, it.len, (int)W::token(p, r0));
             for (int i = 0; i < take; ++i, ++ci) {
                 const int base = (wk.off + i) * kQtKeys, st = ci & 1;
                 ok = qt_warp_wait(&ms.s_full, ci & 1, abort) && qt_warp_wait(&ms.full[st][0], (ci >> 1) & 1, abort);
@@ -585,18 +592,19 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 if (!whole) {
                     p.part_ml[slot * kQaTile + row] = make_float2(mref, bad ? nan : lsum);
                 } else if (r < R && p.lse) {
-                    const int tq = it.q0 + r / p.H, hd = r % p.H;
+                    const int tk = (int)W::token(p, r), tq = it.q0 + tk, hd = r - tk * p.H;
                     p.lse[(size_t)tq * p.H + hd] = bad ? nan : lsum > 0.f ? (mref + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
                 }
             }
             if (!whole) {
                 float *dst = p.part_o + ((size_t)slot * kQaTile + 32 * g) * kQtDV + 32 * q4 + lane;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     float v[16];
                     tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+                    float *at = dst + 16 * (k & 1) * kQtDV + 128 * (k >> 1);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) dst[(16 * (k & 1) + j) * kQtDV + 128 * (k >> 1)] = v[j];
+                    for (int j = 0; j < 16; ++j) at[j * kQtDV] = v[j];
                 }
             } else {
                 // staged over the queries (every score is done), then whole rows
@@ -604,17 +612,18 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 inv[lane] = bad ? nan : lsum > 0.f ? 1.f / lsum : 0.f;
                 __syncwarp();
                 uint8_t *out = sQ + 32 * g * kQtOutPitch + (32 * q4 + lane) * 2;
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     float v[16];
                     tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+                    uint8_t *at = out + 16 * (k & 1) * kQtOutPitch + 256 * (k >> 1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 x = *(const float4 *)(inv + 16 * (k & 1) + j);
                         const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            *(__nv_bfloat16 *)(out + (16 * (k & 1) + j + y) * kQtOutPitch + 256 * (k >> 1)) = __float2bfloat16_rn(v[j + y] * f[y]);
+                            *(__nv_bfloat16 *)(at + (j + y) * kQtOutPitch) = __float2bfloat16_rn(v[j + y] * f[y]);
                     }
                 }
                 ok = group_sync();
@@ -623,7 +632,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 for (int k = 0; k < 8; ++k) {
                     const int rw = 32 * g + 8 * q4 + k;
                     if (r0 + rw >= R) break;
-                    const int tq = (r0 + rw) / p.H, hd = r0 + rw - tq * p.H;
+                    const int tq = (int)W::token(p, r0 + rw), hd = r0 + rw - tq * p.H;
                     uint4 *dst = (uint4 *)(p.o + (size_t)(it.q0 + tq) * p.o_stride + (size_t)hd * kQtDV);
                     const uint4 *from = (const uint4 *)(sQ + rw * kQtOutPitch);
                     dst[lane] = from[lane];

@@ -542,6 +542,11 @@ dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const ds
     p.cu_q = q->cu_q;
     p.length = q->length;
     p.H = q->n_heads;
+    // with 2^s >= H: ceil(2^(31 + s) / H) < 2^32, and the product errs by less than 1 / H for r < 2^31
+    int hs = 0;
+    while ((1 << hs) < q->n_heads) ++hs;
+    p.h_shift = 31 + hs;
+    p.h_mul = (uint32_t)(((1ull << (31 + hs)) + q->n_heads - 1) / (uint64_t)q->n_heads);
     p.bs = bs;
     p.total_q = q->total_q;
     p.causal = q->causal;

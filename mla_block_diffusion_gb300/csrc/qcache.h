@@ -33,6 +33,8 @@ struct QaParams {
     long long q_stride;
     const int32_t *cu_q, *length;
     int H, bs, total_q, causal;
+    uint32_t h_mul;                  // r / H = r * h_mul >> h_shift for r < 2^31
+    int h_shift;
     float scale_log2;                // softmax scale * log2(e)
     __nv_bfloat16 *o;
     long long o_stride;
