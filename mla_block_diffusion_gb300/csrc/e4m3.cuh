@@ -30,28 +30,16 @@ DS_DEVINL void mma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_
 DS_DEVINL uint32_t sdesc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | 1u << 16; }
 __host__ __device__ constexpr uint32_t sdesc_hi(uint32_t sbo, uint32_t type) { return (sbo >> 4) | 1u << 14 | type << 29; }
 
-// E4M3 MMA (kind::f8f6f4), descriptors as words: one 32-bit addition is all that
-// an operand costs the issuing thread.
-DS_DEVINL void mma_e4m3_w(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
-                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(alo), "r"(ahi), "r"(blo), "r"(bhi), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-// Block-scaled MMA, kind::mxf8f6f4: E4M3 A [M x 32] and B [N x 32], one E8M0
+// Block-scaled MMA, kind::mxf8f6f4, descriptors as words (one 32-bit addition is
+// all that an operand costs the issuing thread): E4M3 A [M x 32] and B [N x 32], one E8M0
 // scale 2^(byte - 127) per row and 32 k. Scale words lie in tensor memory: row r
 // at lane r % 32 of column r / 32 (the same in all four lane quarters), byte k of
 // the word for the k-block that the instruction descriptor selects (here: sfb; A's
-// byte 0). Both operands MN-major.
-__host__ __device__ constexpr uint32_t idesc_mx_e4m3_mn(int M, int N, int sfb) {
-    return ((uint32_t)sfb << 4) | (1u << 15) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(M >> 4) << 24);
+// byte 0). Both operands K-major, or with kIdescBothMN both MN-major.
+__host__ __device__ constexpr uint32_t idesc_mx_e4m3(int M, int N, int sfb) {
+    return ((uint32_t)sfb << 4) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
+constexpr uint32_t kIdescBothMN = 1u << 15 | 1u << 16;
 DS_DEVINL void mma_mx_e4m3_w(uint32_t d_tmem, uint32_t alo, uint32_t ahi, uint32_t blo, uint32_t bhi, uint32_t idesc,
                              uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     asm volatile(

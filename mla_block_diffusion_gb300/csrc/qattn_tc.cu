@@ -6,11 +6,12 @@
 // dimensions as the 128 rows of the accumulator and the query rows as its
 // columns, so that 64 rows (one token of 64 heads) fill the tensor core:
 //
-//   S^T [128 tokens, 64 hi | 64 lo] = K [128, 576] (Qhi | Qlo)^T    kind::f8f6f4
+//   S^T [128 tokens, 64 hi | 64 lo] = K [128, 576] (Qhi | Qlo)^T    kind::mxf8f6f4
 //     A query row times 2^a, its largest magnitude in [2^7, 2^8), is the sum of
 //     two E4M3 numbers, hi and lo / 16: exact for bf16 down to 2^-13 of the
-//     largest, below that to 2^-22 of it. s = hi + lo / 16.
-//   O^T [4 x 128 dims, 64] += V^T (Phi + Plo)^T                     kind::mxf8f6f4
+//     largest, below that to 2^-22 of it. The rows' E8M0 scales 2^-a and 2^-a-4
+//     undo it: s = hi + lo.
+//   O^T [4 x 128 dims, 64] += V^T (Phi + Plo)^T                     the same
 //     V is K's first 512 columns, read from the same bytes. For every row and 32
 //     tokens, b = round(max t) (t = s + e in the log2 domain, e the page scale's
 //     exponent), the weights 2^(t - b + 8) < 363 are the sum of two E4M3 numbers
@@ -59,7 +60,7 @@ constexpr int kQtStage = 4 * kQtBox + kQtRope;
 constexpr int kQtQ = 4 * kQtBox + kQtRope;         // (64 hi + 64 lo) rows x 576
 constexpr int kQtPlo = kQtKeys * 64;
 constexpr int kQtOutPitch = kQtDV * 2 + 16;           // staged output row, bytes
-constexpr int kQtColO = 0, kQtColS = 256, kQtColSfa = 384, kQtColSfb = 392;
+constexpr int kQtColO = 0, kQtColS = 256, kQtColSfa = 384, kQtColSfb = 392, kQtColSfq = 408;
 constexpr int kQtMoveLog2 = 60;
 
 struct QtMisc {
@@ -69,7 +70,7 @@ struct QtMisc {
     volatile int abort;
     uint8_t issued[2][8];              // loads in flight: 1 | parity << 1, per box
     int8_t e[2][2];                    // page scale exponents of a stage's pages
-    alignas(16) float c[kQaTile];      // score factor per row; -0 marks a non-finite query
+    int qe[kQaTile];                   // biased exponent that undoes a query row's scaling; 0: a non-finite query
     alignas(16) int lim[kQaTile];      // tokens that a row sees
     alignas(16) int16_t b[2][2][4][32];  // block exponents by group, chunk parity, lane quarter, row; at an item's
                                          // end the output factors of the group's warps
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             // everything about an operand but its stage is a constant added to one word: the
             // issuing thread shares its scheduler with softmax warps
             const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sK));
-            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4), id = idesc_e4m3_f32(128, 128);
+            constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4), id = idesc_mx_e4m3(128, 128, 0);
+            const uint32_t sfk = tmem + kQtColSfa, sfq = tmem + kQtColSfq;
             bool ok = true;
             for (uint32_t items = 0; left > 0 && ok; ++items) {
                 const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
@@ -243,12 +245,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         if (!ok) break;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, k > 0 ? 1u : (uint32_t)(d > 0));
+                            mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, sfk, sfq, k > 0 ? 1u : (uint32_t)(d > 0));
                     }
                     ok = ok && mbar_wait_bounded(&ms.full[st][4], par, abort);
                     if (!ok) break;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) mma_e4m3_w(tmem + kQtColS, a + 2 * k, kHi64, b + 2 * k, kHi64, id, 1);
+                    for (int k = 0; k < 2; ++k) mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi64, b + 2 * k, kHi64, id, sfk, sfq, 1);
                     mma_commit(&ms.s_full);
                 }
                 left -= take;
@@ -276,7 +278,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     for (int d = 0; d < 4; ++d, a += kQtBox >> 4, d_col += 64) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t id = idesc_mx_e4m3_mn(128, 64, k);
+                            const uint32_t id = idesc_mx_e4m3(128, 64, k) | kIdescBothMN;
                             mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, phi + 128 * k, kHi64, id, sfa, sfb, k > 0 ? 1u : first);
                             mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, p_lo + 128 * k, kHi64, id, sfa, sfb + 4, 1);
                         }
@@ -388,19 +390,22 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     for (int j = 0; j + 3 < kPer; ++j) v[j] = v[j + 3];
                 }
                 if ((lane & 3) == 0) {
-                    ms.c[r] = bad ? -0.f : qc_pow2(-a) * p.scale_log2;
+                    ms.qe[r] = bad ? 0 : 127 - a;  // a <= 100 and >= 7 - 127
                     ms.lim[r] = in ? W::sees(p, it.nq, it.len, tq) : 0;
                     if (bad && first) set_error(p.err, DSPARK_ERR_BAD_INPUT);
                 }
             }
             fence_async_smem();
+            ok = group_sync();  // qe and lim of the rows of this group come from its own four warps
+            if (!ok) break;
+            const int qe = ms.qe[32 * g + lane];
+            tmem_st1(tl + kQtColSfq + g, (uint32_t)max(qe, 4) * 0x01010101u);            // hi rows
+            tmem_st1(tl + kQtColSfq + 2 + g, (uint32_t)(max(qe, 4) - 4) * 0x01010101u);  // lo rows: 2^-4 of it
+            tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.q_ready);
-            ok = group_sync();  // c and lim of the rows of this group come from its own four warps
-            if (!ok) break;
 
-            const float c_own = ms.c[32 * g + lane];
             float l[32], mref = 0.f;  // mref: the reference of row 32 g + lane
 #pragma unroll
             for (int j = 0; j < 32; ++j) l[j] = 0.f;
@@ -408,7 +413,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int all_see = W::sees(p, it.nq, it.len, (int)W::token(p, r0));
             for (int i = 0; i < take; ++i, ++ci) {
                 const int base = (wk.off + i) * kQtKeys, st = ci & 1;
-                ok = qt_warp_wait(&ms.s_full, ci & 1, abort) && qt_warp_wait(&ms.full[st][0], (ci >> 1) & 1, abort);
+                ok = qt_warp_wait(&ms.full[st][0], (ci >> 1) & 1, abort);  // e; long done when the scores are
+                if (!ok) break;
+                const int e = ms.e[st][q4 >> 1];
+                const float fe = (float)e, c = fmaxf(qc_pow2(e) * p.scale_log2, 1.2e-38f);  // > 0: masked stays -inf
+                ok = qt_warp_wait(&ms.s_full, ci & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
                 float t[32];
@@ -424,13 +433,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     tmem_ld_wait_tied(b[1]);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        t[j] = __fmaf_rn(__uint_as_float(b[j >> 4][j & 15]), 0.0625f, __uint_as_float(a[j >> 4][j & 15]));
+                        t[j] = __uint_as_float(a[j >> 4][j & 15]) + __uint_as_float(b[j >> 4][j & 15]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.s_free);
-                const bool masked = base + kQtKeys > all_see;
-                if (masked) {
+                if (base + kQtKeys > all_see) {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         const int4 m = *(const int4 *)&ms.lim[32 * g + j];
@@ -458,10 +466,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     const float4 m = make_float4(redux_max(t[j]), redux_max(t[j + 1]), redux_max(t[j + 2]), redux_max(t[j + 3]));
                     if (lane == 0) *(float4 *)(wrow + j) = m;
                 }
-                const int e = ms.e[st][q4 >> 1];
-                const float fe = (float)e, ks = qc_pow2(e);
                 __syncwarp();
-                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c_own * ks, fe), -16384.f), 16383.f));
+                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c, fe), -16384.f), 16383.f));
                 ms.b[g][ci & 1][q4][lane] = (int16_t)(int)bf;
                 __syncwarp();
                 wrow[lane] = (fe + 8.f) - bf;
@@ -469,21 +475,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 // weights
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    const float4 c = *(const float4 *)&ms.c[32 * g + j], x = *(const float4 *)(wrow + j);
-                    t[j] = qt_ex2(__fmaf_rn(t[j], c.x * ks, x.x));
-                    t[j + 1] = qt_ex2(__fmaf_rn(t[j + 1], c.y * ks, x.y));
-                    t[j + 2] = qt_ex2(__fmaf_rn(t[j + 2], c.z * ks, x.z));
-                    t[j + 3] = qt_ex2(__fmaf_rn(t[j + 3], c.w * ks, x.w));
-                }
-                if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 32; j += 4) {
-                        const int4 m = *(const int4 *)&ms.lim[32 * g + j];
-                        if (base + tok >= m.x) t[j] = 0.f;
-                        if (base + tok >= m.y) t[j + 1] = 0.f;
-                        if (base + tok >= m.z) t[j + 2] = 0.f;
-                        if (base + tok >= m.w) t[j + 3] = 0.f;
-                    }
+                    const float4 x = *(const float4 *)(wrow + j);
+                    t[j] = qt_ex2(__fmaf_rn(t[j], c, x.x));
+                    t[j + 1] = qt_ex2(__fmaf_rn(t[j + 1], c, x.y));
+                    t[j + 2] = qt_ex2(__fmaf_rn(t[j + 2], c, x.z));
+                    t[j + 3] = qt_ex2(__fmaf_rn(t[j + 3], c, x.w));
                 }
                 // their two E4M3 terms
                 uint32_t hi[8], lo[8];
@@ -585,7 +581,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const float lsum = (ms.w[4 * g][lane] + ms.w[4 * g + 1][lane]) + (ms.w[4 * g + 2][lane] + ms.w[4 * g + 3][lane]);
-            const bool bad = __float_as_uint(c_own) == 0x80000000u;
+            const bool bad = qe == 0;
             const float nan = __uint_as_float(0x7fffffffu);
             const int row = 32 * g + lane, r = r0 + row;
             if (q4 == 0) {
