@@ -24,7 +24,7 @@
 //     usual rescaling of O whenever a maximum grows does not exist here.
 //     Row sums add the unrounded weights times 2^(b - 8 - M - e) in fp32.
 //
-// Tensor memory: O^T 4 x 64 columns, S^T 128, scale words. Shared memory: the
+// Tensor memory: O^T 5 x 64 columns, S^T 128, scale words. Shared memory: the
 // query tile 72 KB, two chunk stages of 72 KB (four boxes of 128 dims in the
 // 128-byte swizzle, K-major for S^T and MN-major for O^T; the rope box in the
 // 64-byte swizzle), Plo 8 KB; Phi takes the place of the chunk's rope box, which
@@ -60,12 +60,14 @@ constexpr int kQtStage = 4 * kQtBox + kQtRope;
 constexpr int kQtQ = 4 * kQtBox + kQtRope;         // (64 hi + 64 lo) rows x 576
 constexpr int kQtPlo = kQtKeys * 64;
 constexpr int kQtOutPitch = kQtDV * 2 + 16;           // staged output row, bytes
-constexpr int kQtColO = 0, kQtColS = 256, kQtColSfa = 384, kQtColSfb = 392, kQtColSfq = 408;
+// tensor-memory columns: O^T (its first tile twice, Phi's and Plo's share), S^T, scale words
+constexpr int kQtColO = 0, kQtColS = 320, kQtColSfa = 448, kQtColSfb = 452, kQtColSfq = 460;
+DS_DEVINL constexpr int qt_col_o(int d) { return kQtColO + (d ? 64 + 64 * d : 0); }
 constexpr int kQtMoveLog2 = 60;
 
 struct QtMisc {
     uint64_t full[2][5], free_[2][5];  // per stage: boxes 0..3, rope
-    uint64_t s_full, s_free, p_ready, pv_done, q_ready, item_done, mma_done, grp[2];
+    uint64_t s_full, s_free, hi_ready, lo_ready, pv_done, q_ready, item_done, mma_done, grp[2];
     uint32_t tmem;
     volatile int abort;
     uint8_t issued[2][8];              // loads in flight: 1 | parity << 1, per box
@@ -128,7 +130,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             }
         mbar_init(&ms.s_full, 1);
         mbar_init(&ms.s_free, 8);
-        mbar_init(&ms.p_ready, 8);
+        mbar_init(&ms.hi_ready, 8);
+        mbar_init(&ms.lo_ready, 8);
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.q_ready, 8);
         mbar_init(&ms.item_done, 8);
@@ -193,12 +196,13 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     const int st = ci & 1, n = max(0, min(2, npages - (first + 2 * i)));
                     const uint32_t par = ((ci >> 1) - 1) & 1;
                     uint8_t *dst = sK + st * kQtStage;
-                    for (int d = 0; d < 5; ++d) {
+                    for (int x = 0; x < 5; ++x) {
+                        const int d = x < 2 ? x ^ 1 : x == 2 ? 2 : 7 - x;  // 1, 0, 2, rope, 3
                         if (ci >= 2 && !mbar_wait_bounded(&ms.free_[st][d], par, abort)) {
                             ok = false;
                             break;
                         }
-                        if (d == 0) {
+                        if (x == 0) {
                             ms.e[st][0] = (int8_t)ea;
                             ms.e[st][1] = (int8_t)eb;
                         }
@@ -238,19 +242,28 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t st = ci & 1, par = (ci >> 1) & 1;
-                    uint32_t a = k_lo + st * (kQtStage >> 4), b = q_lo;
+                    const uint32_t a0 = k_lo + st * (kQtStage >> 4);
+                    // boxes in the order in which they come free
 #pragma unroll 1
-                    for (int d = 0; d < 4; ++d, a += kQtBox >> 4, b += kQtBox >> 4) {
+                    for (int x = 0; x < 3; ++x) {
+                        const int d = x < 2 ? x ^ 1 : 2;
                         ok = mbar_wait_bounded(&ms.full[st][d], par, abort);
                         if (!ok) break;
+                        const uint32_t a = a0 + d * (kQtBox >> 4), b = q_lo + d * (kQtBox >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, sfk, sfq, k > 0 ? 1u : (uint32_t)(d > 0));
+                            mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, sfk, sfq, k > 0 ? 1u : (uint32_t)(x > 0));
                     }
                     ok = ok && mbar_wait_bounded(&ms.full[st][4], par, abort);
                     if (!ok) break;
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi64, b + 2 * k, kHi64, id, sfk, sfq, 1);
+                    for (int k = 0; k < 2; ++k)
+                        mma_mx_e4m3_w(tmem + kQtColS, a0 + (4 * kQtBox >> 4) + 2 * k, kHi64, q_lo + (4 * kQtBox >> 4) + 2 * k, kHi64, id, sfk, sfq, 1);
+                    ok = mbar_wait_bounded(&ms.full[st][3], par, abort);
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_mx_e4m3_w(tmem + kQtColS, a0 + (3 * kQtBox >> 4) + 2 * k, kHi128, q_lo + (3 * kQtBox >> 4) + 2 * k, kHi128, id, sfk, sfq, 1);
                     mma_commit(&ms.s_full);
                 }
                 left -= take;
@@ -268,23 +281,43 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             while (left > 0 && ok) {
                 const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
                 for (int i = 0; i < take; ++i, ++ci) {
-                    ok = mbar_wait_bounded(&ms.p_ready, ci & 1, abort);
+                    // Two tiles' Phi products start while the split's second terms are made. The first
+                    // tile takes both terms at once (N = 128, its codes are read once); tensor memory
+                    // has no room for a second such tile.
+                    const uint32_t st = ci & 1, a0 = k_lo + st * (kQtStage >> 4), phi = a0 + (4 * kQtBox >> 4);
+                    const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 4 * st, first = i > 0;
+                    auto tile = [&](int d, uint32_t b, uint32_t sf, uint32_t acc) {
+                        const uint32_t a = a0 + d * (kQtBox >> 4), col = tmem + qt_col_o(1) + 64 * (d - 1);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mma_mx_e4m3_w(col, a + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 64, k) | kIdescBothMN, sfa, sf,
+                                          k > 0 ? 1u : acc);
+                    };
+                    ok = mbar_wait_bounded(&ms.hi_ready, ci & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = ci & 1, phi = k_lo + st * (kQtStage >> 4) + (4 * kQtBox >> 4);
-                    const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 8 * st, first = i > 0;
-                    uint32_t a = k_lo + st * (kQtStage >> 4), d_col = tmem + kQtColO;
-#pragma unroll 1
-                    for (int d = 0; d < 4; ++d, a += kQtBox >> 4, d_col += 64) {
+                    tile(1, phi, sfb, first);
+                    tile(2, phi, sfb, first);
+                    ok = mbar_wait_bounded(&ms.lo_ready, ci & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    tile(1, p_lo, sfb + 2, 1);
+                    mma_commit(&ms.free_[st][1]);
+                    {
+                        // Plo's 64 columns lie p_lo - phi behind Phi's: the distance of the operand's two halves
+                        const uint32_t b = (phi & 0xffffu) | (p_lo - phi) << 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t id = idesc_mx_e4m3(128, 64, k) | kIdescBothMN;
-                            mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, phi + 128 * k, kHi64, id, sfa, sfb, k > 0 ? 1u : first);
-                            mma_mx_e4m3_w(d_col, a + 256 * k, kHi128, p_lo + 128 * k, kHi64, id, sfa, sfb + 4, 1);
-                        }
-                        mma_commit(&ms.free_[st][d]);
+                        for (int k = 0; k < 4; ++k)
+                            mma_mx_e4m3_w(tmem + kQtColO, a0 + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 128, k) | kIdescBothMN,
+                                          sfa, sfb, k > 0 ? 1u : first);
                     }
+                    mma_commit(&ms.free_[st][0]);
+                    tile(3, phi, sfb, first);
                     mma_commit(&ms.free_[st][4]);
+                    tile(2, p_lo, sfb + 2, 1);
+                    mma_commit(&ms.free_[st][2]);
+                    tile(3, p_lo, sfb + 2, 1);
+                    mma_commit(&ms.free_[st][3]);
                     mma_commit(&ms.pv_done);
                 }
                 left -= take;
@@ -413,7 +446,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int all_see = W::sees(p, it.nq, it.len, (int)W::token(p, r0));
             for (int i = 0; i < take; ++i, ++ci) {
                 const int base = (wk.off + i) * kQtKeys, st = ci & 1;
-                ok = qt_warp_wait(&ms.full[st][0], (ci >> 1) & 1, abort);  // e; long done when the scores are
+                ok = qt_warp_wait(&ms.full[st][1], (ci >> 1) & 1, abort);  // e; long done when the scores are
                 if (!ok) break;
                 const int e = ms.e[st][q4 >> 1];
                 const float fe = (float)e, c = fmaxf(qc_pow2(e) * p.scale_log2, 1.2e-38f);  // > 0: masked stays -inf
@@ -481,20 +514,19 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     t[j + 2] = qt_ex2(__fmaf_rn(t[j + 2], c, x.z));
                     t[j + 3] = qt_ex2(__fmaf_rn(t[j + 3], c, x.w));
                 }
-                // their two E4M3 terms
-                uint32_t hi[8], lo[8];
+                // their first E4M3 terms
+                uint32_t h16[16], hi[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    uint32_t w[2], x[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint32_t h16 = f32x2_to_f16x2(t[4 * j + 2 * k], t[4 * j + 2 * k + 1]);
-                        w[k] = f16x2_to_e4m3x2(h16);
-                        x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));
-                    }
-                    hi[j] = w[0] | w[1] << 16;
-                    lo[j] = x[0] | x[1] << 16;
+                    h16[2 * j] = f32x2_to_f16x2(t[4 * j], t[4 * j + 1]);
+                    h16[2 * j + 1] = f32x2_to_f16x2(t[4 * j + 2], t[4 * j + 3]);
+                    hi[j] = f16x2_to_e4m3x2(h16[2 * j]) | f16x2_to_e4m3x2(h16[2 * j + 1]) << 16;
                 }
+                // Phi over the chunk's rope box (its scores are done)
+                const int sw = (tok >> 1) & 3;
+                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
+                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
                 ok = group_wait();
                 if (!ok) break;
                 int bq[4], bm = -32768;
@@ -515,7 +547,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) l[j] *= __shfl_sync(~0u, f, j);
 #pragma unroll 1
-                        for (int k = 0; k < 8; ++k) {
+                        for (int k = 0; k < 10; ++k) {
                             float v[16];
                             uint32_t u[16];
                             const uint32_t at = tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1);
@@ -532,15 +564,20 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     uint32_t wh = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) wh |= (uint32_t)min(max(bq[k] - m_int + (127 - 8), 4), 250) << (8 * k);
-                    tmem_st1(tl + kQtColSfb + 8 * st + g, wh);
-                    tmem_st1(tl + kQtColSfb + 8 * st + 4 + g, wh - 0x04040404u);
+                    tmem_st1(tl + kQtColSfb + 4 * st + g, wh);
+                    tmem_st1(tl + kQtColSfb + 4 * st + 2 + g, wh - 0x04040404u);
                 }
-                // Phi over the chunk's rope box (its scores are done)
-                const int sw = (tok >> 1) & 3;
-                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
-                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                // Plo once the chunk before has been read
+                fence_async_smem();
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.hi_ready);
+                // the second terms, once the chunk before has read its own
+                uint32_t lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    lo[j] = f16x2_to_e4m3x2(f16x2_sub_x16(h16[2 * j], e4m3x2_to_f16x2_(hi[j] & 0xffffu))) |
+                            f16x2_to_e4m3x2(f16x2_sub_x16(h16[2 * j + 1], e4m3x2_to_f16x2_(hi[j] >> 16))) << 16;
                 if (ci > 0 && !qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort)) {
                     ok = false;
                     break;
@@ -549,12 +586,10 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 *(uint4 *)(pl + ((2 * g) ^ sw) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 *(uint4 *)(pl + ((2 * g + 1) ^ sw) * 16) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 fence_async_smem();
-                tmem_st_wait();
-                tc_fence_before();
                 // lane j: what a weight of row j adds to the sum, 2^(b - 8 - M - e)
                 wrow[lane] = __int_as_float(max((int)bf - m_int - e + (127 - 8), 0) << 23);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.p_ready);
+                if (lane == 0) mbar_arrive(&ms.lo_ready);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 x = *(const float4 *)(wrow + j);
@@ -580,6 +615,19 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
+            // 16 rows of the output: tile d's, the first tile's two shares added
+            auto load_o = [&](int d, int half, float (&v)[16]) {
+                const uint32_t at = tl + kQtColO + 32 * g + 16 * half;
+                if (d == 0) {
+                    float x[16];
+                    tmem_ld16(at + 64, x);
+                    tmem_ld16(at, v);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += x[j];
+                } else {
+                    tmem_ld16(at + 64 + 64 * d, v);
+                }
+            };
             const float lsum = (ms.w[4 * g][lane] + ms.w[4 * g + 1][lane]) + (ms.w[4 * g + 2][lane] + ms.w[4 * g + 3][lane]);
             const bool bad = qe == 0;
             const float nan = __uint_as_float(0x7fffffffu);
@@ -597,7 +645,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     float v[16];
-                    tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+                    load_o(k >> 1, k & 1, v);
                     float *at = dst + 16 * (k & 1) * kQtDV + 128 * (k >> 1);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) at[j * kQtDV] = v[j];
@@ -611,7 +659,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll 1
                 for (int k = 0; k < 8; ++k) {
                     float v[16];
-                    tmem_ld16(tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1), v);
+                    load_o(k >> 1, k & 1, v);
                     uint8_t *at = out + 16 * (k & 1) * kQtOutPitch + 256 * (k >> 1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
