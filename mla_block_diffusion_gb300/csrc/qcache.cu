@@ -249,9 +249,16 @@ __global__ void __launch_bounds__(kPlanThreads) qcache_plan_kernel(const PlanPar
 // at least the page's present one if it holds earlier tokens; codes are
 // RN(x * 2^-e), exact but for the rounding since 2^-e is a power of two.
 // Earlier codes move by whole binades: exact unless they fall below 2^-6.
-// Bound: HBM (2 or 4 bytes read and one written per element).
+// Bound: HBM (2 or 4 bytes read and one written per element). The rows are read
+// once: a page's new elements wait in registers for their maximum (a whole page
+// of the full width: nine 16-byte pieces a thread in bf16, eighteen in fp32).
 // ---------------------------------------------------------------------------
-constexpr int kAppThreads = 256;
+template <typename T>
+struct AppCfg {
+    static constexpr int kThreads = 512;
+    static constexpr int kCtas = sizeof(T) == 2 ? 2 : 1;  // resident per SM
+    static constexpr int kPiece = 16 / sizeof(T);         // elements of one 16-byte load
+};
 
 struct AppendParams {
     uint8_t *codes[DSPARK_MAX_LAYERS];
@@ -259,29 +266,32 @@ struct AppendParams {
     const void *entries;
     long long row_stride, layer_stride;
     const int32_t *slots, *seg_row;
-    int rows, n_pages, D;
+    int rows, n_pages;
     int *err;
 };
 
-// 16 consecutive elements of a row as fp32.
-DS_DEVINL void load16(const __nv_bfloat16 *p, float (&v)[16]) {
-    const uint4 u[2] = {__ldg((const uint4 *)p), __ldg((const uint4 *)p + 1)};
-    const uint32_t *w = (const uint32_t *)u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+// Elements 2i and 2i + 1 of a 16-byte piece as fp32.
+DS_DEVINL float2 pair_of(const uint4 &u, int i, const __nv_bfloat16 *) {
+    const uint32_t w = ((const uint32_t *)&u)[i];
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-DS_DEVINL void load16(const float *p, float (&v)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 f = __ldg((const float4 *)p + i);
-        v[4 * i] = f.x;
-        v[4 * i + 1] = f.y;
-        v[4 * i + 2] = f.z;
-        v[4 * i + 3] = f.w;
-    }
+DS_DEVINL float2 pair_of(const uint4 &u, int i, const float *) {
+    const float *f = (const float *)&u;
+    return make_float2(f[2 * i], f[2 * i + 1]);
+}
+// Largest magnitude of a piece, as the bits of an fp32 number (a NaN is above every number).
+DS_DEVINL uint32_t amax_of(const uint4 &u, const __nv_bfloat16 *) {
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+}
+DS_DEVINL uint32_t amax_of(const uint4 &u, const float *) {
+    return max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu));
+}
+// A load that leaves no copy in L1 (each element is read once).
+DS_DEVINL uint4 ld_once(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
 }
 
 // Two floats to two E4M3 codes (round to nearest even, saturating), even low.
@@ -298,8 +308,11 @@ DS_DEVINL int amax_exponent(uint32_t bits) {
     return max(-kQcEmax, min(kQcEmax, e));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAppThreads) qcache_append_kernel(const AppendParams a) {
+template <typename T, int D>
+__global__ void __launch_bounds__(AppCfg<T>::kThreads, AppCfg<T>::kCtas) qcache_append_kernel(const AppendParams a) {
+    using C = AppCfg<T>;
+    constexpr int kPer = D / C::kPiece, kPairs = C::kPiece / 2;                // pieces per row, element pairs of one
+    constexpr int kHold = (kQcPage * kPer + C::kThreads - 1) / C::kThreads;    // pieces per thread
     __shared__ uint32_t s_amax;
     const int layer = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
@@ -318,22 +331,33 @@ __global__ void __launch_bounds__(kAppThreads) qcache_append_kernel(const Append
         if (tid == 0) set_error(a.err, DSPARK_ERR_OOB);
         return;
     }
-    __syncthreads();
-    const int D = a.D, per = D / 16;  // 16-element pieces per row
     const T *src = (const T *)a.entries + (long long)layer * a.layer_stride + (long long)r0 * a.row_stride;
     uint8_t *dst = a.codes[layer] + (size_t)page * kQcPage * D;
+    const int n = nr * kPer;
+    uint4 v[kHold];
+#pragma unroll
+    for (int j = 0; j < kHold; ++j) {
+        const int i = tid + j * C::kThreads, r = i / kPer, k = i % kPer;
+        v[j] = i < n ? ld_once((const uint4 *)(src + (long long)r * a.row_stride) + k) : make_uint4(0, 0, 0, 0);
+    }
+    const float old = off > 0 ? a.scales[layer][page] : 1.f;
     uint32_t mx = 0;
     bool bad = false;
-    for (int i = tid; i < nr * per; i += kAppThreads) {
-        float v[16];
-        load16(src + (long long)(i / per) * a.row_stride + (i % per) * 16, v);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const uint32_t u = __float_as_uint(v[j]) & 0x7fffffffu;
-            if (u >= 0x7f800000u) bad = true;
-            else mx = max(mx, u);
+    for (int j = 0; j < kHold; ++j) mx = max(mx, amax_of(v[j], (const T *)0));
+    if (mx >= 0x7f800000u) {  // an infinity or NaN among this thread's: the finite ones count
+        bad = true;
+        mx = 0;
+#pragma unroll 1
+        for (int i = tid; i < n; i += C::kThreads) {
+            const T *from = src + (long long)(i / kPer) * a.row_stride + (i % kPer) * C::kPiece;
+            for (int x = 0; x < C::kPiece; ++x) {
+                const uint32_t u = __float_as_uint((float)from[x]) & 0x7fffffffu;
+                if (u < 0x7f800000u) mx = max(mx, u);
+            }
         }
     }
+    __syncthreads();  // s_amax is zero; every thread has read the old scale
     mx = __reduce_max_sync(~0u, mx);
     if (lane == 0) atomicMax(&s_amax, mx);
     __syncthreads();
@@ -342,17 +366,16 @@ __global__ void __launch_bounds__(kAppThreads) qcache_append_kernel(const Append
     int e = amax_exponent(mx);
     if (off > 0) {
         int eo;
-        if (!qc_scale_exponent(a.scales[layer][page], &eo)) {
+        if (!qc_scale_exponent(old, &eo)) {
             bad = true;
             eo = e;
         }
-        __syncthreads();  // every thread has read the scale before it changes
         if (eo >= e) {
             e = eo;
         } else {
             // earlier tokens of the page move to the larger scale
-            const float f = qc_pow2(max(eo - e, -126));
-            for (int i = tid; i < off * per; i += kAppThreads) {
+            const float f = qc_pow2(eo - e);
+            for (int i = tid; i < off * (D / 16); i += C::kThreads) {
                 uint4 c = *(uint4 *)(dst + (size_t)i * 16);
                 uint32_t *w = (uint32_t *)&c;
 #pragma unroll
@@ -366,20 +389,35 @@ __global__ void __launch_bounds__(kAppThreads) qcache_append_kernel(const Append
         }
     }
     const float inv = qc_pow2(-e);
-    for (int i = tid; i < nr * per; i += kAppThreads) {
-        float v[16];
-        const int r = i / per, k = (i % per) * 16;
-        load16(src + (long long)r * a.row_stride + k, v);
-        uint32_t w[4];
+    uint8_t *to = dst + (size_t)off * D;  // a row's pieces are its codes in order, and the rows follow one another
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = isnan(v[j]) ? 0.f : v[j] * inv;
+    for (int j = 0; j < kHold; ++j) {
+        const int i = tid + j * C::kThreads;
+        if (i >= n) break;
+        uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            w[j] = f32x2_to_e4m3x2(v[4 * j], v[4 * j + 1]) | f32x2_to_e4m3x2(v[4 * j + 2], v[4 * j + 3]) << 16;
-        *(uint4 *)(dst + (size_t)(off + r) * D + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int x = 0; x < kPairs; ++x) {
+            float2 f = pair_of(v[j], x, (const T *)0);
+            if (bad) f = make_float2(isnan(f.x) ? 0.f : f.x, isnan(f.y) ? 0.f : f.y);
+            w[x / 2] |= f32x2_to_e4m3x2(f.x * inv, f.y * inv) << (16 * (x & 1));
+        }
+        if (kPairs == 4) *(uint2 *)(to + (size_t)i * 8) = make_uint2(w[0], w[1]);
+        else *(uint32_t *)(to + (size_t)i * 4) = w[0];
     }
     if (tid == 0) a.scales[layer][page] = qc_pow2(e);
     if (bad) set_error(a.err, DSPARK_ERR_BAD_INPUT);
+}
+
+template <typename T>
+static cudaError_t launch_append(const AppendParams &a, int n_seg, int layers, int D, cudaStream_t st) {
+    const dim3 grid(n_seg, layers), block(AppCfg<T>::kThreads);
+    switch (D) {
+        case 576: return launch_pdl(qcache_append_kernel<T, 576>, grid, block, 0, st, a);
+        case 288: return launch_pdl(qcache_append_kernel<T, 288>, grid, block, 0, st, a);
+        case 160: return launch_pdl(qcache_append_kernel<T, 160>, grid, block, 0, st, a);
+        case 80: return launch_pdl(qcache_append_kernel<T, 80>, grid, block, 0, st, a);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace ds
@@ -507,12 +545,9 @@ dspark_status dspark_qcache_append(const dspark_qcache_t *c, const void *entries
     a.seg_row = seg_row;
     a.rows = rows;
     a.n_pages = c->n_pages;
-    a.D = D;
     a.err = (int *)ws;
-    const dim3 grid(n_seg, c->n_layers);
-    return done(entry_type == DSPARK_ENTRY_BF16
-                    ? launch_pdl(qcache_append_kernel<__nv_bfloat16>, grid, dim3(kAppThreads), 0, (cudaStream_t)stream, a)
-                    : launch_pdl(qcache_append_kernel<float>, grid, dim3(kAppThreads), 0, (cudaStream_t)stream, a));
+    return done(entry_type == DSPARK_ENTRY_BF16 ? launch_append<__nv_bfloat16>(a, n_seg, c->n_layers, D, (cudaStream_t)stream)
+                                                : launch_append<float>(a, n_seg, c->n_layers, D, (cudaStream_t)stream));
 }
 
 dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const dspark_qattn_t *q, int bs, void *ws,
