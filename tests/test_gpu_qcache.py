@@ -268,7 +268,7 @@ class Attend:
             tol = 2.0 ** -8 * np.abs(wo) + (2.0 ** -8 + 2 * ds[..., None]) * absolute + 2.0 ** -17 * np.abs(k).max()
             assert np.all(np.abs(o[a:z] - wo) <= tol + 1e-30), (b, np.max(np.abs(o[a:z] - wo) / (tol + 1e-30)))
             fin = ~none
-            assert np.all(np.abs(lse[a:z] - wl)[fin] <= (ds + 2.0 ** -22 * (1 + np.abs(np.where(fin, wl, 0))))[fin]), b
+            assert np.all(np.abs(lse[a:z][fin] - wl[fin]) <= ds[fin] + 2.0 ** -22 * (1 + np.abs(wl[fin]))), b
 
 
 @pytest.mark.parametrize("kv,rope", LATENTS)
@@ -283,6 +283,32 @@ def test_attend(M, kv, rope, causal, H, length, nq):
     o, lse = t.run(causal)
     assert t.cache.check() == 0
     t.check(causal, o, lse)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("H,length,nq", [
+    (64, [300], [200]), (100, [130, 77, 2], [60, 77, 9]),  # more tiles than CTAs
+    (7, [40 * i % 700 for i in range(300)], [i % 3 for i in range(300)]),  # many small requests
+    (64, [12000, 100, 100, 100], [1, 1, 1, 1]),            # one request far longer than the others
+])
+def test_attend_divisions_of_the_work(M, kv, rope, H, length, nq):
+    t = Attend(M, kv, rope, H, length, nq, seed=13)
+    o, lse = t.run(True)
+    assert t.cache.check() == 0
+    t.check(True, o, lse)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+def test_attend_rows_of_every_magnitude(M, kv, rope):
+    # neighbouring query rows 2^-120 .. 2^8 times unit size, one all zero: none disturbs another
+    t = Attend(M, kv, rope, 20, [333], [4], seed=14)
+    e = torch.linspace(-120, 8, 80)[torch.randperm(80, generator=torch.Generator().manual_seed(1))].round()
+    q = t.q.float().reshape(80, t.D) * torch.exp2(e)[:, None]
+    q[17] = 0
+    t.q = q.reshape(4, 20, t.D).to(torch.bfloat16)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0
+    t.check(False, o, lse)
 
 
 @pytest.mark.parametrize("kv,rope", LATENTS)
@@ -413,6 +439,50 @@ def test_attend_reports_bad_input(M, kv, rope):
     t.dev[1][int(t.table[2, 0])] = 0.75
     t.run(False)
     assert t.cache.check() == 17
+
+
+def test_binding_refuses_what_does_not_fit(M):
+    t = Attend(M, 64, 16, 4, [100, 80], [2, 1], seed=15)
+    q, o, lse = t.q.cuda(), torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, 4, device="cuda")
+    cu, length = t.args
+    bad = [dict(q=q.half()), dict(q=q[:, :, :72]), dict(q=q.cpu()), dict(o=o[:2]), dict(o=o.float()), dict(lse=lse[:2]),
+           dict(lse=lse.double()), dict(cu=cu.long()), dict(cu=cu[:2]), dict(length=length.long()), dict(length=length.cpu()),
+           dict(q=q.transpose(0, 1)[:3]), dict(q=torch.zeros(3, 4, 160, dtype=torch.bfloat16, device="cuda")[:, :, ::2]),
+           dict(length=ints([1, 1, 1]), cu=ints([0, 1, 2, 3]))]
+    for kw in bad:
+        a = dict(q=q, cu=cu, length=length, o=o, lse=lse) | kw
+        with pytest.raises(ValueError):
+            t.cache.attend(0, a["q"], a["cu"], a["length"], a["o"], a["lse"])
+    with pytest.raises(M.DSparkError):
+        t.cache.attend(1, q, cu, length, o, lse)                       # no such layer
+    with pytest.raises(M.DSparkError):
+        t.cache.attend(0, q, cu, length, o, lse, scale=-1.0)
+    x, slots, seg = torch.zeros(1, 3, 80, device="cuda"), ints([0, 1, 2]), ints([0, 3])
+    for kw in (dict(x=x[0]), dict(x=x.half()), dict(x=x.cpu()), dict(x=x[:, :, :64]), dict(x=x.expand(2, 3, 80)),
+               dict(slots=slots.long()), dict(seg=seg.cpu()), dict(x=torch.zeros(1, 3, 160, device="cuda")[:, :, ::2])):
+        a = dict(x=x, slots=slots, seg=seg) | kw
+        with pytest.raises(ValueError):
+            t.cache.append(a["x"], a["slots"], a["seg"])
+    with pytest.raises(M.DSparkError):
+        t.cache.append(torch.zeros(1, 3, 82, device="cuda")[:, :, :80], slots, seg)  # rows off the 16-byte grid
+    g = Plan(M, [5, 6], [7, 8], np.zeros((2, 4)), np.zeros(8), (0, 8), 4, 4)
+    for i in range(9):                                                   # each argument in turn too short or of another type
+        args = list(g.inputs + g.outs)
+        for other in (args[i].long(), args[i][:0] if i not in (7, 8) else args[i].cpu()):
+            if other.numel() == 0 and i == 0:
+                continue                                                 # no requests at all: the library's own refusal
+            with pytest.raises(ValueError):
+                g.cache.plan(*(args[:i] + [other] + args[i + 1:]))
+    with pytest.raises(M.DSparkError):
+        g.cache.plan(ints([]), ints([]), *g.inputs[2:], *g.outs)
+    with pytest.raises(ValueError):
+        M.QCache(64, 16, [t.dev[0]], [], t.dev[2])
+    with pytest.raises(ValueError):
+        M.QCache(128, 32, [t.dev[0]], [t.dev[1]], t.dev[2])
+    with pytest.raises(ValueError):
+        M.QCache(64, 16, [t.dev[0]], [t.dev[1].double()], t.dev[2])
+    with pytest.raises(M.DSparkError):
+        M.QCache(64, 32, (), (), t.dev[2], n_pages=4)                    # no such latent width
 
 
 def test_attend_pages_past_32_bits(M):
