@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
     wk.find(p, cta, grid, qg_smem);
     long long left = wk.end - wk.begin, unit = wk.begin;
     QaSplit sp;
-    sp.b = sp.t = sp.lo_slot = 0;
+    sp.q0 = sp.r0 = sp.rows = sp.lo_slot = 0;
     sp.c_hi = -1;
     int slot = 2 * cta;
     for (; left > 0; slot = 2 * cta + 1) {
@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
         const int take = (int)min((long long)(it.chunks - wk.off), left);
         const bool first = wk.off == 0, whole = first && take == it.chunks;
         if (first && !whole) {
-            sp.b = it.b;
-            sp.t = it.t;
+            sp.q0 = it.q0;
+            sp.r0 = it.t * kQaTile;
+            sp.rows = it.nq * p.H - sp.r0;
             sp.lo_slot = slot;
             sp.c_hi = wk.last_cta(unit);
         }
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
 // ---------------------------------------------------------------------------
 // Combine: the rows of items that were split, one warp per two rows and 128
 // columns (all columns at the narrower widths), partials in CTA order. The warp's
-// lanes hold the partials' weights; eight partials of each row are in flight, the
-// first of them requested together with the weights. Bound: latency and L2 (the
+// lanes hold the partials' weights; sixteen partials are in flight, the first of
+// them requested together with the weights. Bound: latency and L2 (the
 // partials were just written).
 // ---------------------------------------------------------------------------
 constexpr int kQaCombineThreads = 256;
@@ -293,7 +294,6 @@ template <int DV>
 __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const QaParams p, int ctas) {
     __shared__ QaSplit s_list[kQaMaxGrid];
     __shared__ int s_first[kQaMaxGrid];
-    __shared__ int s_q0[kQaMaxGrid], s_rows[kQaMaxGrid];  // the item's first query token, rows from its start to the request's end
     __shared__ unsigned s_mask[kQaMaxGrid / 32];
     constexpr int kCols = DV < 128 ? DV : 128, kSub = DV / kCols;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -325,91 +325,88 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
         n_split += __popc(mask);
     }
     __syncthreads();
-    for (int i = tid; i < n_split; i += kQaCombineThreads) {
-        const int q0 = p.cu_q[s_list[i].b];
-        s_q0[i] = q0;
-        s_rows[i] = (p.cu_q[s_list[i].b + 1] - q0) * p.H - s_list[i].t * kQaTile;
-    }
-    __syncthreads();
-    constexpr int kRows = 2, kDeep = 8;  // rows a warp takes at once, partials of each in flight
+    constexpr int kRows = 2, kDeep = 16;  // rows of a task, partials in flight (of both rows, or of one when there are many)
     const int tasks = n_split * (kQaTile / kRows) * kSub, warps = gridDim.x * (kQaCombineThreads / 32);
     const bool on = 4 * lane < kCols;
     for (int task = blockIdx.x * (kQaCombineThreads / 32) + (tid >> 5); task < tasks; task += warps) {
         const int sub = task % kSub, row0 = task / kSub % (kQaTile / kRows) * kRows, li = task / kSub / (kQaTile / kRows);
-        const int left = s_rows[li] - row0;
-        if (left <= 0) continue;
         const QaSplit sp = s_list[li];
+        const int left = sp.rows - row0;
+        if (left <= 0) continue;
         const int c = s_first[li], n = sp.c_hi - c + 1;
         auto slot = [&](int k) { return (size_t)(k == 0 ? sp.lo_slot : 2 * (c + k)); };
         const float *src = p.part_o + (size_t)row0 * DV + sub * kCols + 4 * lane;
-        float4 v[kRows][kDeep];
-        auto fetch = [&](int k0) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                for (int j = 0; j < kDeep; ++j)
-                    v[i][j] = on && k0 + j < n ? __ldcg((const float4 *)(src + slot(k0 + j) * (kQaTile * DV) + i * DV))
-                                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto fetch = [&](int k, int i) {
+            return on && k < n ? __ldcg((const float4 *)(src + slot(k) * (kQaTile * DV) + i * DV)) : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        // references and sums, lane = partial; the first partials are requested with them
-        float2 ml[kRows];
-        float m[kRows], l[kRows], w[kRows];
+        // reference and sum, lane = partial
         auto stats = [&](int k0, int i) {
             return k0 + lane < n ? __ldcg(&p.part_ml[slot(k0 + lane) * kQaTile + row0 + i]) : make_float2(-INFINITY, 0.f);
         };
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) ml[i] = stats(0, i);
-        fetch(0);
-        float4 o[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            m[i] = ml[i].x;
-            for (int k0 = 32; k0 < n; k0 += 32) m[i] = fmaxf(m[i], stats(k0, i).x);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m[i] = fmaxf(m[i], __shfl_xor_sync(~0u, m[i], d));
-            if (m[i] == -INFINITY) m[i] = 0.f;
-            w[i] = qa_ex2(ml[i].x - m[i]);
-            l[i] = w[i] * ml[i].y;
-            o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        for (int k = 0; k < n; k += kDeep) {
-            if (k > 0) {
-                fetch(k);
-                if ((k & 31) == 0) {
-#pragma unroll
-                    for (int i = 0; i < kRows; ++i) {
-                        ml[i] = stats(k, i);
-                        w[i] = qa_ex2(ml[i].x - m[i]);
-                        l[i] += w[i] * ml[i].y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                for (int j = 0; j < kDeep; ++j) {
-                    const float wk = __shfl_sync(~0u, w[i], (k + j) & 31);
-                    o[i].x += wk * v[i][j].x;
-                    o[i].y += wk * v[i][j].y;
-                    o[i].z += wk * v[i][j].z;
-                    o[i].w += wk * v[i][j].w;
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (i >= left) break;
-            const float sum = warp_sum(l[i]);
+        auto store = [&](int i, const float4 &o, float m, float l) {
+            const float sum = warp_sum(l);
             const float inv = isnan(sum) ? sum : sum > 0.f ? 1.f / sum : 0.f;
-            const int r = sp.t * kQaTile + row0 + i, tq = (int)QaWork<kQaTile, kQcPage>::token(p, r), hd = r - tq * p.H, tok = s_q0[li] + tq;
+            const int r = sp.r0 + row0 + i, tq = (int)QaWork<kQaTile, kQcPage>::token(p, r), hd = r - tq * p.H, tok = sp.q0 + tq;
             if (on) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(o[i].x * inv, o[i].y * inv), hi = __floats2bfloat162_rn(o[i].z * inv, o[i].w * inv);
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
                 uint2 u;
                 u.x = *(const uint32_t *)&lo;
                 u.y = *(const uint32_t *)&hi;
                 *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + sub * kCols + 4 * lane) = u;
             }
             if (p.lse && sub == 0 && lane == 0)
-                p.lse[(size_t)tok * p.H + hd] = isnan(sum) ? sum : sum > 0.f ? (m[i] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+                p.lse[(size_t)tok * p.H + hd] = isnan(sum) ? sum : sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+        };
+        auto reference = [&](float m) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+            return m == -INFINITY ? 0.f : m;
+        };
+        auto add = [&](float4 &o, float w, const float4 &v) {
+            o.x += w * v.x;
+            o.y += w * v.y;
+            o.z += w * v.z;
+            o.w += w * v.w;
+        };
+        float4 v[kDeep];
+        if (n <= kDeep / 2) {  // both rows at once, everything requested together
+            const float2 ml[kRows] = {stats(0, 0), stats(0, 1)};
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) v[j] = fetch(j >> 1, j & 1);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const float m = reference(ml[i].x), w = qa_ex2(ml[i].x - m);
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < kDeep / 2; ++j) add(o, __shfl_sync(~0u, w, j), v[2 * j + i]);
+                if (i < left) store(i, o, m, w * ml[i].y);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int i = 0; i < min(kRows, left); ++i) {
+            float2 ml = stats(0, i);
+#pragma unroll
+            for (int j = 0; j < kDeep; ++j) v[j] = fetch(j, i);
+            float m = ml.x;
+            for (int k0 = 32; k0 < n; k0 += 32) m = fmaxf(m, stats(k0, i).x);
+            m = reference(m);
+            float w = qa_ex2(ml.x - m), l = w * ml.y;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = 0; k < n; k += kDeep) {
+                if (k > 0) {
+#pragma unroll
+                    for (int j = 0; j < kDeep; ++j) v[j] = fetch(k + j, i);
+                    if ((k & 31) == 0) {
+                        ml = stats(k, i);
+                        w = qa_ex2(ml.x - m);
+                        l += w * ml.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kDeep; ++j) add(o, __shfl_sync(~0u, w, (k + j) & 31), v[j]);
+            }
+            store(i, o, m, l);
         }
     }
 }

@@ -127,9 +127,11 @@ struct QaWork {
 #pragma unroll
         for (int r = 0; r < kPieceRounds; ++r) {
             u[r] = 0;
-            if (32 * r < items) u[r] = 32 * r + lane < items ? min(units_of(p, s, 32 * r + lane), 1 << 22) : 0;
-            T += min(u[r], 1 << 14);
-            longest = max(longest, u[r]);
+            if (32 * r < items) {
+                u[r] = 32 * r + lane < items ? units_of(p, s, 32 * r + lane) : 0;
+                T += min(u[r], 1 << 14);
+                longest = max(longest, u[r]);
+            }
         }
         T = (int)__reduce_add_sync(~0u, (unsigned)T);
         longest = (int)__reduce_max_sync(~0u, (unsigned)longest);
@@ -139,7 +141,8 @@ struct QaWork {
         const int tight = (2 * T + 2 * grid - items - 1) / (2 * grid - items);
         int n = 0;
 #pragma unroll
-        for (int r = 0; r < kPieceRounds; ++r) n += (u[r] + tight - 1) / tight;
+        for (int r = 0; r < kPieceRounds; ++r)
+            if (32 * r < items) n += (u[r] + tight - 1) / tight;
         const int cut = (int)__reduce_add_sync(~0u, (unsigned)n) <= grid ? tight : loose;
         if (min(cut, longest) > (T + grid - 1) / grid + kItemCost) return false;
         int base = 0;

@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         for (int k = 0; k < 4; ++k) tmem_st1(tl + kQtColSfa + k, 0x7f7f7f7fu);  // V is not scaled
         long long unit = wk.begin;
         QaSplit sp;
-        sp.b = sp.t = sp.lo_slot = 0;
+        sp.q0 = sp.r0 = sp.rows = sp.lo_slot = 0;
         sp.c_hi = -1;
         int slot = 2 * cta;
         bool ok = true;
@@ -356,8 +356,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int take = (int)min((long long)(it.chunks - wk.off), left);
             const bool first = wk.off == 0, whole = first && take == it.chunks;
             if (first && !whole) {
-                sp.b = it.b;
-                sp.t = it.t;
+                sp.q0 = it.q0;
+                sp.r0 = it.t * kQaTile;
+                sp.rows = it.nq * p.H - sp.r0;
                 sp.lo_slot = slot;
                 sp.c_hi = wk.last_cta(unit);
             }
@@ -527,6 +528,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
                 *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                fence_async_smem();
                 ok = group_wait();
                 if (!ok) break;
                 int bq[4], bm = -32768;
@@ -567,7 +569,6 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     tmem_st1(tl + kQtColSfb + 4 * st + g, wh);
                     tmem_st1(tl + kQtColSfb + 4 * st + 2 + g, wh - 0x04040404u);
                 }
-                fence_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();

@@ -23,7 +23,7 @@ DS_DEVINL bool qc_scale_exponent(float s, int *e) {
 DS_DEVINL float qc_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 struct QaSplit {
-    int b, t;        // the item: request, tile of kQaTile query rows
+    int q0, r0, rows;  // the item: its request's first query token, its first row, rows from there to the request's end
     int lo_slot;     // partial slot of the item's first CTA
     int c_hi;        // its last CTA (slots 2c beyond the first); < 0: none
 };
