@@ -46,7 +46,10 @@ template <int D, int DV>
 struct QgCfg {
     static constexpr int kThreads = 256;
     static constexpr int kRow = D * 2 + 16;                 // bytes per shared row: an odd number of 16-byte pieces
-    static constexpr int kSmem = (64 + kQcPage) * kRow + 64 * 8 + 1024;
+    static constexpr int kStages = 4;                       // pages of raw codes in flight
+    static constexpr int kRaw = kQcPage * D;
+    static constexpr int kSmem = (64 + kQcPage) * kRow + kStages * kRaw + 64 * 8;
+    static constexpr int kCtas = DV < 256 ? 2 : 1;          // resident per SM
     static constexpr int kPieces = kQcPage * D / 16;        // 16-byte pieces of a page
     static constexpr int kPer = (kPieces + kThreads - 1) / kThreads;
     static_assert((kRow / 16) % 2 == 1, "conflict-free row stride");
@@ -54,12 +57,12 @@ struct QgCfg {
 };
 
 template <int D, int DV>
-__global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const QaParams p) {
+__global__ void __launch_bounds__(QgCfg<D, DV>::kThreads, QgCfg<D, DV>::kCtas) qattn_any_kernel(const QaParams p) {
     using C = QgCfg<D, DV>;
     using W = QaWork<kQaTile, kQcPage>;
     extern __shared__ __align__(16) uint8_t qg_smem[];
-    uint8_t *sQ = qg_smem, *sK = sQ + 64 * C::kRow;
-    float *s_c = (float *)(sK + kQcPage * C::kRow);  // score factor of every row (NaN: a non-finite query)
+    uint8_t *sQ = qg_smem, *sK = sQ + 64 * C::kRow, *sR = sK + kQcPage * C::kRow;
+    float *s_c = (float *)(sR + C::kStages * C::kRaw);  // score factor of every row (NaN: a non-finite query)
     int *s_lim = (int *)(s_c + 64);                  // tokens every row sees
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rg = warp & 3, half = warp >> 2;
@@ -133,51 +136,78 @@ __global__ void __launch_bounds__(QgCfg<D, DV>::kThreads) qattn_any_kernel(const
 #pragma unroll
             for (int j = 0; j < 4; ++j) oacc[i][j] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        // pages: raw codes into registers one page ahead, decoded into shared memory
-        uint4 raw[C::kPer];
-        int e_next = 0;
-        auto load = [&](int c) {
-            const int n = it.len;
-            if (c * kQcPage >= n) return;  // nothing cached: the unit only writes its outputs
-            int pg = p.page_table[(size_t)it.b * p.max_pages + c];
+        // Pages: every thread copies its pieces of the raw codes into a ring three pages ahead, and
+        // decodes the same pieces for all, so the copies need no barrier of their own. Page numbers
+        // and scales: 32 pages at a time in the lanes of every warp, one block ahead.
+        const int npages = min((it.len + kQcPage - 1) / kQcPage, wk.off + take);
+        const int32_t *row = p.page_table + (size_t)it.b * p.max_pages;
+        auto page = [&](int c) {
+            int pg = c < npages ? row[c] : 0;
             if (pg < 0 || pg >= p.n_pages) {
-                if (tid == 0) set_error(p.err, DSPARK_ERR_OOB);
+                set_error(p.err, DSPARK_ERR_OOB);
                 pg = 0;
             }
-            if (!qc_scale_exponent(p.scales[pg], &e_next) && tid == 0) set_error(p.err, DSPARK_ERR_BAD_INPUT);
-            const uint4 *src = (const uint4 *)(p.codes + (size_t)pg * kQcPage * D);
-            const int used = min(kQcPage, n - c * kQcPage) * (D / 16);  // pieces of cached tokens
-#pragma unroll
-            for (int j = 0; j < C::kPer; ++j) {
-                const int i = tid + j * C::kThreads;
-                raw[j] = i < used ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-            }
+            return pg;
         };
-        load(wk.off);
-        for (int c = wk.off; c < wk.off + take; ++c) {
-            const int base = c * kQcPage;
-            const int e = e_next;
-            __syncthreads();  // the page before has been read
-            if (base < it.len) {
+        auto exponent = [&](int c, int pg) {
+            int x = 0;
+            if (c < npages && !qc_scale_exponent(p.scales[pg], &x)) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+            return x;
+        };
+        int pg_l = page(wk.off + lane), pg_n = 0, ex = exponent(wk.off + lane, pg_l), ex_n = 0;  // loads run ahead: pg_l is their block
+        auto load = [&](int i) {  // page wk.off + i into stage i % kStages
+            if (i > 0 && (i & 31) == 0) pg_l = pg_n;
+            const int c = wk.off + i, pg = __shfl_sync(~0u, pg_l, i & 31);
+            if (c < npages) {
+                const uint4 *src = (const uint4 *)(p.codes + (size_t)pg * kQcPage * D);
+                const int used = min(kQcPage, it.len - c * kQcPage) * (D / 16);  // pieces of cached tokens
+                const uint32_t dst = smem_u32(sR + (i % C::kStages) * C::kRaw);
 #pragma unroll
                 for (int j = 0; j < C::kPer; ++j) {
-                    const int i = tid + j * C::kThreads;
-                    if (i < C::kPieces) {
-                        const uint32_t *u = (const uint32_t *)&raw[j];
-                        uint8_t *dst = sK + (i / (D / 16)) * C::kRow + (i % (D / 16)) * 32;
+                    const int k = tid + j * C::kThreads;
+                    if (k < C::kPieces)  // zeros past the cached tokens
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 16), "l"(src + (k < used ? k : 0)),
+                                     "r"(k < used ? 16 : 0)
+                                     : "memory");
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll 1
+        for (int i = 0; i < C::kStages - 1; ++i) load(i);
+#pragma unroll 1
+        for (int i = 0; i < take; ++i) {
+            const int c = wk.off + i, base = c * kQcPage;
+            if ((i & 31) == 0) {
+                if (i > 0) ex = ex_n;
+                pg_n = page(wk.off + i + 32 + lane);
+            }
+            if ((i & 31) == 16) ex_n = exponent(wk.off + i + 16 + lane, pg_n);
+            const int e = __shfl_sync(~0u, ex, i & 31);
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 2) : "memory");
+            __syncthreads();  // the page before has been read
+            if (base < it.len) {
+                const uint8_t *raw = sR + (i % C::kStages) * C::kRaw;
+#pragma unroll
+                for (int j = 0; j < C::kPer; ++j) {
+                    const int k = tid + j * C::kThreads;
+                    if (k < C::kPieces) {
+                        const uint4 v = *(const uint4 *)(raw + k * 16);
+                        const uint32_t *u = (const uint32_t *)&v;
+                        uint8_t *dst = sK + (k / (D / 16)) * C::kRow + (k % (D / 16)) * 32;
                         uint32_t h[8];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            h[2 * k] = e4m3x2_to_f16x2_(u[k] & 0xffffu);
-                            h[2 * k + 1] = e4m3x2_to_f16x2_(u[k] >> 16);
+                        for (int x = 0; x < 4; ++x) {
+                            h[2 * x] = e4m3x2_to_f16x2_(u[x] & 0xffffu);
+                            h[2 * x + 1] = e4m3x2_to_f16x2_(u[x] >> 16);
                         }
                         *(uint4 *)dst = make_uint4(h[0], h[1], h[2], h[3]);
                         *(uint4 *)(dst + 16) = make_uint4(h[4], h[5], h[6], h[7]);
                     }
                 }
             }
+            load(i + C::kStages - 1);
             __syncthreads();
-            if (c + 1 < wk.off + take) load(c + 1);
             if (base >= it.len) continue;
             // scores of 16 rows x 64 tokens
             float s[8][4];
@@ -425,7 +455,7 @@ static cudaError_t any_width(const QaParams &p, int num_sms, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    const int grid = min(num_sms, kQaMaxGrid);
+    const int grid = min(num_sms * C::kCtas, kQaMaxGrid);
     const cudaError_t e = launch_pdl(qattn_any_kernel<D, DV>, dim3(grid), dim3(C::kThreads), (size_t)C::kSmem, st, p);
     return e != cudaSuccess ? e : combine<DV>(p, grid, num_sms, st);
 }
