@@ -1,8 +1,7 @@
-// Work division of the attention over the 8-bit latent cache, shared by its
-// kernels.
+// Work division of the attention over the 8-bit latent cache.
 //
-// An item is one tile of TILE query rows (token-major, heads inside) of one
-// request; its units are the chunks of CH cached tokens that its last query
+// An item is one tile of TILE = 64 query rows (token-major, heads inside) of one
+// request; its units are the chunks of CH = 128 cached tokens that its last query
 // sees (one unit if none: the item still writes its outputs). Two ways to divide
 // them, whatever the requests' lengths:
 //   - pieces: an item of n units is cut into ceil(n / per) equal pieces, one per
@@ -37,8 +36,8 @@ struct QaItem {
     int chunks;          // units
 };
 
-template <int TILE, int CH>
 struct QaWork {
+    static constexpr int TILE = kQaTile, CH = kQaChunk;
     static_assert((TILE & (TILE - 1)) == 0 && (CH & (CH - 1)) == 0, "powers of two");
     // Request b's queries and length; out of range: no queries (reported by `report`).
     static DS_DEVINL void request(const QaParams &p, int b, int *q0, int *nq, int *len, bool report = false) {

@@ -1,18 +1,18 @@
-// Attention over the 8-bit latent cache at the full latent width (512 + 64) on
-// the 5th-generation tensor core; codes go to it as they are stored.
+// Attention over the 8-bit latent cache on the 5th-generation tensor core; codes
+// go to it as they are stored.
 //
 // A CTA holds 64 query rows (token, head) and walks chunks of 128 cached tokens
 // (two pages). Both products are formed transposed, with tokens or value
 // dimensions as the 128 rows of the accumulator and the query rows as its
 // columns, so that 64 rows (one token of 64 heads) fill the tensor core:
 //
-//   S^T [128 tokens, 64 hi | 64 lo] = K [128, 576] (Qhi | Qlo)^T    kind::mxf8f6f4
+//   S^T [128 tokens, 64 hi | 64 lo] = K [128, D] (Qhi | Qlo)^T      kind::mxf8f6f4
 //     A query row times 2^a, its largest magnitude in [2^7, 2^8), is the sum of
 //     two E4M3 numbers, hi and lo / 16: exact for bf16 down to 2^-13 of the
 //     largest, below that to 2^-22 of it. The rows' E8M0 scales 2^-a and 2^-a-4
 //     undo it: s = hi + lo.
-//   O^T [4 x 128 dims, 64] += V^T (Phi + Plo)^T                     the same
-//     V is K's first 512 columns, read from the same bytes. For every row and 32
+//   O^T [tiles of 128 dims, 64] += V^T (Phi + Plo)^T                the same
+//     V is K's first columns, read from the same bytes. For every row and 32
 //     tokens, b = round(max t) (t = s + e in the log2 domain, e the page scale's
 //     exponent), the weights 2^(t - b + 8) < 363 are the sum of two E4M3 numbers
 //     hi and lo / 16 (8 significant bits, absolute error 2^-14), and the block's
@@ -24,17 +24,29 @@
 //     usual rescaling of O whenever a maximum grows does not exist here.
 //     Row sums add the unrounded weights times 2^(b - 8 - M - e) in fp32.
 //
-// Tensor memory: O^T 5 x 64 columns, S^T 128, scale words. Shared memory: the
-// query tile 72 KB, two chunk stages of 72 KB (four boxes of 128 dims in the
-// 128-byte swizzle, K-major for S^T and MN-major for O^T; the rope box in the
-// 64-byte swizzle), Plo 8 KB; Phi takes the place of the chunk's rope box, which
-// only S^T reads. A box goes back to the producer as soon as the products of its
-// dimensions are done.
+// The full width, 512 + 64. Tensor memory: O^T 5 x 64 columns, S^T 128, scale
+// words. Shared memory: the query tile 72 KB, two chunk stages of 72 KB (four
+// boxes of 128 dims in the 128-byte swizzle, K-major for S^T and MN-major for
+// O^T; the rope box in the 64-byte swizzle), Plo 8 KB; Phi takes the place of the
+// chunk's rope box, which only S^T reads. A box goes back to the producer as soon
+// as the products of its dimensions are done.
 //
-// Bound: the tensor core (128 products of 64 rows a chunk against 73 KB of
-// codes). Measured issue rates: 64.7 clocks a score step (N = 128, full rate), 51
-// an output step (N = 64, bound by the 6 KB of operands it reads from shared
-// memory), so a chunk is 1165 + 1629 clocks against 2177 at the full rate.
+// The smaller widths (256 + 32, 128 + 32, 64 + 16) take boxes of 128 dims
+// throughout, with zeros past the entry's end, and have room for three or four
+// stages, both terms of the weights in a buffer of their own and every output tile
+// in both terms at once (N = 128: V's codes are read once).
+//
+// Bound, full width: a chunk is 2650 tensor clocks (scores 65 a step of N = 128;
+// outputs 51 a step of N = 64, which the 6 KB of operands that it reads from shared
+// memory bind, and 65 of N = 128), but two stages allow no more than two chunks in
+// a loop of loads (~1000), scores, softmax (~1800) and outputs: ~3600 clocks a
+// chunk, and an item costs ~16000 more (queries converted ~5000, output ~6000, the
+// pipeline drained and refilled). A third stage does not fit
+// beside the queries. Prompt chunks of 1200 rows x 64 heads:
+// 1310 us, 1.3 PFLOP/s of the formulas' products. Bound, smaller widths: the
+// softmax, ~2700 clocks a chunk whatever the width (32 requests of 1K to 16K
+// tokens and 64 heads: 37, 34 and 34 us; products by mma.sync in f16, codes
+// widened on the way, took 130, 71 and 49).
 //
 // Roles (12 warps): warp 0 TMA producer; warp 1 issues the scores (and owns tensor
 // memory), warp 2 the outputs, so that whichever of the two is ready keeps the
@@ -49,40 +61,63 @@
 
 namespace ds {
 
-constexpr int kQtKeys = 128;                       // tokens per chunk
+constexpr int kQtKeys = kQaChunk;                  // tokens per chunk
 constexpr int kQtThreads = 384;
 constexpr int kQtSoft0 = 4;                        // first softmax warp; registers: 168 x 384 = 88 x 128 + 208 x 256
 constexpr int kQtRegsIssue = 88, kQtRegsSoft = 208;
-constexpr int kQtD = 576, kQtDV = 512;
 constexpr int kQtBox = kQtKeys * 128;              // bytes: 128 tokens x 128 dims
-constexpr int kQtRope = kQtKeys * 64;              // 128 tokens x 64 dims
-constexpr int kQtStage = 4 * kQtBox + kQtRope;
-constexpr int kQtQ = 4 * kQtBox + kQtRope;         // (64 hi + 64 lo) rows x 576
-constexpr int kQtPlo = kQtKeys * 64;
-constexpr int kQtOutPitch = kQtDV * 2 + 16;           // staged output row, bytes
-// tensor-memory columns: O^T (its first tile twice, Phi's and Plo's share), S^T, scale words
-constexpr int kQtColO = 0, kQtColS = 320, kQtColSfa = 448, kQtColSfb = 452, kQtColSfq = 460;
-DS_DEVINL constexpr int qt_col_o(int d) { return kQtColO + (d ? 64 + 64 * d : 0); }
+constexpr int kQtTerm = kQtKeys * 64;              // one E4M3 term of the weights: 128 tokens x 64 rows
 constexpr int kQtMoveLog2 = 60;
 
+// kWide: the full width, 512 + 64. The others leave room: more stages, whole
+// stages handed over at once, both terms of the weights in a buffer of their own
+// and every output tile taken in both terms at once.
+template <int KV, int ROPE>
+struct QtCfg {
+    static constexpr bool kWide = KV == 512;
+    static constexpr int kD = KV + ROPE;
+    static constexpr int kTiles = KV < 128 ? 1 : KV / 128;            // output tiles of 128 dims
+    static constexpr int kBoxes = kWide ? 4 : (kD + 127) / 128;       // boxes of 128 dims (zeros past the entry's end)
+    static constexpr int kRope = kWide ? kQtKeys * 64 : 0;            // the rope's box of 64 dims
+    static constexpr int kStage = kBoxes * kQtBox + kRope;
+    static constexpr int kStages = kWide ? 2 : KV == 256 ? 3 : 4;
+    static constexpr int kBars = kWide ? 5 : 1;                       // parts of a stage that are filled and freed
+    static constexpr int kQ = kStage;                                 // (64 hi + 64 lo) query rows, laid out like a stage
+    static constexpr int kP = kWide ? kQtTerm : 2 * kQtTerm;          // wide: Plo alone
+    static constexpr int kLastSteps = (kD - 128 * (kBoxes - 1) + 31) / 32;  // 32-dim steps of the last box (not wide)
+    static constexpr int kPer = ((kWide ? kD : 128 * (kBoxes - 1) + 32 * kLastSteps) / 8 + 3) / 4;  // query pieces a lane converts
+    static constexpr int kRound = kPer % 3 == 0 ? 3 : kPer;
+    static constexpr int kPitch = KV * 2 + 16;                        // staged output row, bytes
+    // tensor-memory columns: O^T (wide: its first tile twice, Phi's and Plo's share; else every tile twice), S^T, scale words
+    static constexpr int kColO = 0, kColS = kWide ? 320 : 128 * kTiles, kColSfa = kColS + 128, kColSfb = kColSfa + 4, kColSfq = kColSfb + 8;
+    static_assert(kColSfq + 4 <= 512, "tensor memory");
+    static_assert(kQaTile * kPitch <= kQ, "the staged output takes the place of the queries");
+    static_assert(QaWork::kScratch <= kStages * kStage, "scratch of the work division");
+};
+
+template <int STAGES, int BARS>
 struct QtMisc {
-    uint64_t full[2][5], free_[2][5];  // per stage: boxes 0..3, rope
+    uint64_t full[STAGES][BARS], free_[STAGES][BARS];  // wide: boxes 0..3, rope
     uint64_t s_full, s_free, hi_ready, lo_ready, pv_done, q_ready, item_done, mma_done, grp[2];
     uint32_t tmem;
     volatile int abort;
-    uint8_t issued[2][8];              // loads in flight: 1 | parity << 1, per box
-    int8_t e[2][2];                    // page scale exponents of a stage's pages
+    uint8_t issued[STAGES][8];         // loads in flight: 1 | parity << 1, per part
+    int8_t e[STAGES][2];               // page scale exponents of a stage's pages
     int qe[kQaTile];                   // biased exponent that undoes a query row's scaling; 0: a non-finite query
     alignas(16) int lim[kQaTile];      // tokens that a row sees
     alignas(16) int16_t b[2][2][4][32];  // block exponents by group, chunk parity, lane quarter, row; at an item's
                                          // end the output factors of the group's warps
     alignas(16) float w[8][32];        // per warp, one value per row
 };
-constexpr int kQtSmem = kQtQ + 2 * kQtStage + kQtPlo + (int)sizeof(QtMisc);
-static_assert(kQtSmem <= 232448, "shared memory");
-static_assert(kQaTile * kQtOutPitch <= kQtQ, "the staged output takes the place of the queries");
-static_assert(sizeof(QtMisc::b) == 8 * 32 * sizeof(float), "output factors");
-static_assert(QaWork<kQaTile, kQtKeys>::kScratch <= kQtStage, "scratch of the work division");
+template <int KV, int ROPE>
+constexpr int qt_smem_bytes() {
+    using C = QtCfg<KV, ROPE>;
+    using Misc = QtMisc<C::kStages, C::kBars>;
+    static_assert(sizeof(Misc::b) == 8 * 32 * sizeof(float), "output factors");
+    constexpr int n = C::kQ + C::kStages * C::kStage + C::kP + (int)sizeof(Misc);
+    static_assert(n <= 232448, "shared memory");
+    return n;
+}
 
 // One lane of the warp. A branch on it is known to hold a single thread, so an
 // MMA's operands are formed in uniform registers: 64 clocks a score step, against
@@ -110,20 +145,23 @@ DS_DEVINL bool qt_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
 }
 
+template <int KV, int ROPE>
 __global__ void __launch_bounds__(kQtThreads, 1)
     qattn_tc_kernel(const __grid_constant__ CUtensorMap tm_dims, const __grid_constant__ CUtensorMap tm_rope,
                     const QaParams p) {
-    using W = QaWork<kQaTile, kQtKeys>;
+    using C = QtCfg<KV, ROPE>;
+    using W = QaWork;
+    using Misc = QtMisc<C::kStages, C::kBars>;
     extern __shared__ __align__(1024) uint8_t qt_smem[];
-    uint8_t *sQ = qt_smem, *sK = sQ + kQtQ, *sP = sK + 2 * kQtStage;
-    QtMisc &ms = *(QtMisc *)(sP + kQtPlo);
+    uint8_t *sQ = qt_smem, *sK = sQ + C::kQ, *sP = sK + C::kStages * C::kStage;
+    Misc &ms = *(Misc *)(sP + C::kP);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, grid = gridDim.x;
 
     pdl_trigger();
     if (tid == 0) {
-        for (int s = 0; s < 2; ++s)
-            for (int d = 0; d < 5; ++d) {
+        for (int s = 0; s < C::kStages; ++s)
+            for (int d = 0; d < C::kBars; ++d) {
                 mbar_init(&ms.full[s][d], 1);
                 mbar_init(&ms.free_[s][d], 1);
                 ms.issued[s][d] = 0;
@@ -141,7 +179,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
         ms.abort = 0;
         fence_mbar_init();
         tma_prefetch_desc(&tm_dims);
-        tma_prefetch_desc(&tm_rope);
+        if (C::kWide) tma_prefetch_desc(&tm_rope);
     }
     if (warp == 1) tmem_alloc(&ms.tmem, 512);
     pdl_wait();
@@ -193,12 +231,13 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 const int pa = __shfl_sync(~0u, pg, 2 * j), pb = __shfl_sync(~0u, pg, 2 * j + 1);
                 const int ea = __shfl_sync(~0u, ex, 2 * j), eb = __shfl_sync(~0u, ex, 2 * j + 1);
                 if (lane == 0) {
-                    const int st = ci & 1, n = max(0, min(2, npages - (first + 2 * i)));
-                    const uint32_t par = ((ci >> 1) - 1) & 1;
-                    uint8_t *dst = sK + st * kQtStage;
-                    for (int x = 0; x < 5; ++x) {
-                        const int d = x < 2 ? x ^ 1 : x == 2 ? 2 : 7 - x;  // 1, 0, 2, rope, 3
-                        if (ci >= 2 && !mbar_wait_bounded(&ms.free_[st][d], par, abort)) {
+                    const int st = ci % C::kStages, n = max(0, min(2, npages - (first + 2 * i)));
+                    const uint32_t par = (ci / C::kStages) & 1;
+                    uint8_t *dst = sK + st * C::kStage;
+                    // wide: the parts in the order in which they come free
+                    for (int x = 0; x < C::kBars; ++x) {
+                        const int d = !C::kWide ? 0 : x < 2 ? x ^ 1 : x == 2 ? 2 : 7 - x;  // 1, 0, 2, rope, 3
+                        if (ci >= C::kStages && !mbar_wait_bounded(&ms.free_[st][d], par ^ 1, abort)) {
                             ok = false;
                             break;
                         }
@@ -207,17 +246,22 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                             ms.e[st][1] = (int8_t)eb;
                         }
                         uint64_t *bar = &ms.full[st][d];
-                        const int bytes = d < 4 ? kQtBox / 2 : kQtRope / 2;
-                        if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * bytes));
+                        const int bytes = d < 4 ? kQtBox / 2 : C::kRope / 2;
+                        if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * (C::kWide ? bytes : C::kStage / 2)));
                         else mbar_arrive(bar);
                         for (int k = 0; k < n; ++k) {
-                            uint8_t *to = dst + d * kQtBox + k * bytes;
                             const int y = (k ? pb : pa) * kQcPage;
-                            // 16-bit elements: 64 (32) of them a box row
-                            if (d < 4) tma_load_2d(to, &tm_dims, d * 64, y, bar);
-                            else tma_load_2d(to, &tm_rope, 256, y, bar);
+                            // 16-bit elements: 64 (the rope's box: 32) of them a box row
+                            if constexpr (C::kWide) {
+                                uint8_t *to = dst + d * kQtBox + k * bytes;
+                                if (d < 4) tma_load_2d(to, &tm_dims, d * 64, y, bar);
+                                else tma_load_2d(to, &tm_rope, 256, y, bar);
+                            } else {
+                                for (int d2 = 0; d2 < C::kBoxes; ++d2)
+                                    tma_load_2d(dst + d2 * kQtBox + k * (kQtBox / 2), &tm_dims, d2 * 64, y, bar);
+                            }
                         }
-                        ms.issued[st][d] = (uint8_t)(1 | ((ci >> 1) & 1) << 1);
+                        ms.issued[st][d] = (uint8_t)(1 | par << 1);
                     }
                 }
                 ok = __shfl_sync(~0u, (int)ok, 0) != 0;
@@ -232,7 +276,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             // issuing thread shares its scheduler with softmax warps
             const uint32_t q_lo = sdesc_lo(smem_u32(sQ)), k_lo = sdesc_lo(smem_u32(sK));
             constexpr uint32_t kHi128 = sdesc_hi(1024, 2), kHi64 = sdesc_hi(512, 4), id = idesc_mx_e4m3(128, 128, 0);
-            const uint32_t sfk = tmem + kQtColSfa, sfq = tmem + kQtColSfq;
+            const uint32_t sfk = tmem + C::kColSfa, sfq = tmem + C::kColSfq;
             bool ok = true;
             for (uint32_t items = 0; left > 0 && ok; ++items) {
                 const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
@@ -241,29 +285,40 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     ok = i == 0 || mbar_wait_bounded(&ms.s_free, (ci - 1) & 1, abort);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t st = ci & 1, par = (ci >> 1) & 1;
-                    const uint32_t a0 = k_lo + st * (kQtStage >> 4);
-                    // boxes in the order in which they come free
+                    const uint32_t st = ci % C::kStages, par = (ci / C::kStages) & 1;
+                    const uint32_t a0 = k_lo + st * (C::kStage >> 4);
+                    if constexpr (C::kWide) {
+                        // boxes in the order in which they come free
 #pragma unroll 1
-                    for (int x = 0; x < 3; ++x) {
-                        const int d = x < 2 ? x ^ 1 : 2;
-                        ok = mbar_wait_bounded(&ms.full[st][d], par, abort);
+                        for (int x = 0; x < 3; ++x) {
+                            const int d = x < 2 ? x ^ 1 : 2;
+                            ok = mbar_wait_bounded(&ms.full[st][d], par, abort);
+                            if (!ok) break;
+                            const uint32_t a = a0 + d * (kQtBox >> 4), b = q_lo + d * (kQtBox >> 4);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_mx_e4m3_w(tmem + C::kColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, sfk, sfq, k > 0 ? 1u : (uint32_t)(x > 0));
+                        }
+                        ok = ok && mbar_wait_bounded(&ms.full[st][4], par, abort);
                         if (!ok) break;
-                        const uint32_t a = a0 + d * (kQtBox >> 4), b = q_lo + d * (kQtBox >> 4);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            mma_mx_e4m3_w(tmem + C::kColS, a0 + (4 * kQtBox >> 4) + 2 * k, kHi64, q_lo + (4 * kQtBox >> 4) + 2 * k, kHi64, id, sfk, sfq, 1);
+                        ok = mbar_wait_bounded(&ms.full[st][3], par, abort);
+                        if (!ok) break;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_mx_e4m3_w(tmem + kQtColS, a + 2 * k, kHi128, b + 2 * k, kHi128, id, sfk, sfq, k > 0 ? 1u : (uint32_t)(x > 0));
+                            mma_mx_e4m3_w(tmem + C::kColS, a0 + (3 * kQtBox >> 4) + 2 * k, kHi128, q_lo + (3 * kQtBox >> 4) + 2 * k, kHi128, id, sfk, sfq, 1);
+                    } else {
+                        ok = mbar_wait_bounded(&ms.full[st][0], par, abort);
+                        if (!ok) break;
+#pragma unroll
+                        for (int d = 0; d < C::kBoxes; ++d)
+#pragma unroll
+                            for (int k = 0; k < (d + 1 < C::kBoxes ? 4 : C::kLastSteps); ++k)
+                                mma_mx_e4m3_w(tmem + C::kColS, a0 + d * (kQtBox >> 4) + 2 * k, kHi128, q_lo + d * (kQtBox >> 4) + 2 * k,
+                                              kHi128, id, sfk, sfq, d > 0 || k > 0);
                     }
-                    ok = ok && mbar_wait_bounded(&ms.full[st][4], par, abort);
-                    if (!ok) break;
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        mma_mx_e4m3_w(tmem + kQtColS, a0 + (4 * kQtBox >> 4) + 2 * k, kHi64, q_lo + (4 * kQtBox >> 4) + 2 * k, kHi64, id, sfk, sfq, 1);
-                    ok = mbar_wait_bounded(&ms.full[st][3], par, abort);
-                    if (!ok) break;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_mx_e4m3_w(tmem + kQtColS, a0 + (3 * kQtBox >> 4) + 2 * k, kHi128, q_lo + (3 * kQtBox >> 4) + 2 * k, kHi128, id, sfk, sfq, 1);
                     mma_commit(&ms.s_full);
                 }
                 left -= take;
@@ -281,43 +336,59 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             while (left > 0 && ok) {
                 const int take = (int)min((long long)(wk.item.chunks - wk.off), left);
                 for (int i = 0; i < take; ++i, ++ci) {
-                    // Two tiles' Phi products start while the split's second terms are made. The first
-                    // tile takes both terms at once (N = 128, its codes are read once); tensor memory
-                    // has no room for a second such tile.
-                    const uint32_t st = ci & 1, a0 = k_lo + st * (kQtStage >> 4), phi = a0 + (4 * kQtBox >> 4);
-                    const uint32_t sfa = tmem + kQtColSfa, sfb = tmem + kQtColSfb + 4 * st, first = i > 0;
-                    auto tile = [&](int d, uint32_t b, uint32_t sf, uint32_t acc) {
-                        const uint32_t a = a0 + d * (kQtBox >> 4), col = tmem + qt_col_o(1) + 64 * (d - 1);
+                    const uint32_t st = ci % C::kStages, a0 = k_lo + st * (C::kStage >> 4);
+                    const uint32_t sfa = tmem + C::kColSfa, sfb = tmem + C::kColSfb + 4 * (ci & 1), first = i > 0;
+                    if constexpr (C::kWide) {
+                        // Two tiles' Phi products start while the split's second terms are made. The first
+                        // tile takes both terms at once (N = 128, its codes are read once); tensor memory
+                        // has no room for a second such tile.
+                        const uint32_t phi = a0 + (4 * kQtBox >> 4);
+                        auto tile = [&](int d, uint32_t b, uint32_t sf, uint32_t acc) {
+                            const uint32_t a = a0 + d * (kQtBox >> 4), col = tmem + C::kColO + 64 + 64 * d;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_mx_e4m3_w(col, a + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 64, k) | kIdescBothMN, sfa, sf,
-                                          k > 0 ? 1u : acc);
-                    };
-                    ok = mbar_wait_bounded(&ms.hi_ready, ci & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    tile(1, phi, sfb, first);
-                    tile(2, phi, sfb, first);
-                    ok = mbar_wait_bounded(&ms.lo_ready, ci & 1, abort);
-                    if (!ok) break;
-                    tc_fence_after();
-                    tile(1, p_lo, sfb + 2, 1);
-                    mma_commit(&ms.free_[st][1]);
-                    {
-                        // Plo's 64 columns lie p_lo - phi behind Phi's: the distance of the operand's two halves
-                        const uint32_t b = (phi & 0xffffu) | (p_lo - phi) << 16;
+                            for (int k = 0; k < 4; ++k)
+                                mma_mx_e4m3_w(col, a + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 64, k) | kIdescBothMN, sfa, sf,
+                                              k > 0 ? 1u : acc);
+                        };
+                        ok = mbar_wait_bounded(&ms.hi_ready, ci & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        tile(1, phi, sfb, first);
+                        tile(2, phi, sfb, first);
+                        ok = mbar_wait_bounded(&ms.lo_ready, ci & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        tile(1, p_lo, sfb + 2, 1);
+                        mma_commit(&ms.free_[st][1]);
+                        {
+                            // Plo's 64 columns lie p_lo - phi behind Phi's: the distance of the operand's two halves
+                            const uint32_t b = (phi & 0xffffu) | (p_lo - phi) << 16;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_mx_e4m3_w(tmem + kQtColO, a0 + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 128, k) | kIdescBothMN,
-                                          sfa, sfb, k > 0 ? 1u : first);
+                            for (int k = 0; k < 4; ++k)
+                                mma_mx_e4m3_w(tmem + C::kColO, a0 + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 128, k) | kIdescBothMN,
+                                              sfa, sfb, k > 0 ? 1u : first);
+                        }
+                        mma_commit(&ms.free_[st][0]);
+                        tile(3, phi, sfb, first);
+                        mma_commit(&ms.free_[st][4]);
+                        tile(2, p_lo, sfb + 2, 1);
+                        mma_commit(&ms.free_[st][2]);
+                        tile(3, p_lo, sfb + 2, 1);
+                        mma_commit(&ms.free_[st][3]);
+                    } else {
+                        ok = mbar_wait_bounded(&ms.lo_ready, ci & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        // both terms at once: Plo's 64 columns lie kQtTerm behind Phi's
+                        const uint32_t b = (p_lo & 0xffffu) | (uint32_t)(kQtTerm >> 4) << 16;
+#pragma unroll 1
+                        for (int d = 0; d < C::kTiles; ++d)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_mx_e4m3_w(tmem + C::kColO + 128 * d, a0 + d * (kQtBox >> 4) + 256 * k, kHi128, b + 128 * k, kHi64,
+                                              idesc_mx_e4m3(128, 128, k) | kIdescBothMN, sfa, sfb, k > 0 ? 1u : first);
+                        mma_commit(&ms.free_[st][0]);
                     }
-                    mma_commit(&ms.free_[st][0]);
-                    tile(3, phi, sfb, first);
-                    mma_commit(&ms.free_[st][4]);
-                    tile(2, p_lo, sfb + 2, 1);
-                    mma_commit(&ms.free_[st][2]);
-                    tile(3, p_lo, sfb + 2, 1);
-                    mma_commit(&ms.free_[st][3]);
                     mma_commit(&ms.pv_done);
                 }
                 left -= take;
@@ -344,7 +415,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             return group_wait();
         };
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_st1(tl + kQtColSfa + k, 0x7f7f7f7fu);  // V is not scaled
+        for (int k = 0; k < 4; ++k) tmem_st1(tl + C::kColSfa + k, 0x7f7f7f7fu);  // V is not scaled
         long long unit = wk.begin;
         QaSplit sp;
         sp.q0 = sp.r0 = sp.rows = sp.lo_slot = 0;
@@ -365,14 +436,15 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int r0 = it.t * kQaTile, R = it.nq * p.H;
             // query rows as E4M3 pairs: 8 rows a warp, four lanes a row
             {
-                constexpr int kPer = kQtD / 8 / 4;  // 16-byte pieces of a row per lane
+                constexpr int kPer = C::kPer;  // 16-byte pieces of a row per lane
                 const int r = 8 * (warp - kQtSoft0) + (lane >> 2);
                 const bool in = r0 + r < R;
                 const int tq = in ? (int)W::token(p, r0 + r) : 0, hd = in ? (r0 + r) - tq * p.H : 0;
-                const uint4 *src = (const uint4 *)(p.q + (size_t)(it.q0 + tq) * p.q_stride + (size_t)hd * kQtD) + (lane & 3);
+                const uint4 *src = (const uint4 *)(p.q + (size_t)(it.q0 + tq) * p.q_stride + (size_t)hd * C::kD) + (lane & 3);
                 uint4 v[kPer];
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) v[j] = in ? __ldg(src + 4 * j) : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < kPer; ++j)
+                    v[j] = in && (4 * kPer * 8 == C::kD || (lane & 3) + 4 * j < C::kD / 8) ? __ldg(src + 4 * j) : make_uint4(0, 0, 0, 0);
                 uint32_t mx = 0;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
@@ -390,12 +462,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     ok = false;
                     break;
                 }
-                // three pieces a round: the loop stays small (instruction fetch, not arithmetic, is what
+                // a few pieces a round: the loop stays small (instruction fetch, not arithmetic, is what
                 // straight-line code that runs once costs), the registers move up instead
 #pragma unroll 1
-                for (int j0 = 0; j0 < kPer; j0 += 3) {
+                for (int j0 = 0; j0 < kPer; j0 += C::kRound) {
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) {
+                    for (int j = 0; j < C::kRound; ++j) {
                         const int pc = (lane & 3) + 4 * (j0 + j);  // 8 elements each
                         const uint32_t *u = (const uint32_t *)&v[j];
                         uint32_t hi[2], lo[2];
@@ -415,13 +487,14 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         // 16-byte pieces: c ^ (row & 7) in 128-byte rows, c ^ (row / 2 & 3) in the rope's 64-byte
                         // rows; the same for row r + 64
                         const int d = pc >> 4, c = (pc & 15) >> 1;
-                        const int rs = d < 4 ? 128 : 64, ch = d < 4 ? (c ^ (r & 7)) : (c ^ ((r >> 1) & 3));
+                        const bool rope = C::kWide && d == 4;
+                        const int rs = rope ? 64 : 128, ch = rope ? (c ^ ((r >> 1) & 3)) : (c ^ (r & 7));
                         uint8_t *at = sQ + d * kQtBox + r * rs + ch * 16 + (pc & 1) * 8;
                         *(uint2 *)at = make_uint2(hi[0], hi[1]);
                         *(uint2 *)(at + 64 * rs) = make_uint2(lo[0], lo[1]);
                     }
 #pragma unroll
-                    for (int j = 0; j + 3 < kPer; ++j) v[j] = v[j + 3];
+                    for (int j = 0; j + C::kRound < kPer; ++j) v[j] = v[j + C::kRound];
                 }
                 if ((lane & 3) == 0) {
                     ms.qe[r] = bad ? 0 : 127 - a;  // a <= 100 and >= 7 - 127
@@ -433,8 +506,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             ok = group_sync();  // qe and lim of the rows of this group come from its own four warps
             if (!ok) break;
             const int qe = ms.qe[32 * g + lane];
-            tmem_st1(tl + kQtColSfq + g, (uint32_t)max(qe, 4) * 0x01010101u);            // hi rows
-            tmem_st1(tl + kQtColSfq + 2 + g, (uint32_t)(max(qe, 4) - 4) * 0x01010101u);  // lo rows: 2^-4 of it
+            tmem_st1(tl + C::kColSfq + g, (uint32_t)max(qe, 4) * 0x01010101u);            // hi rows
+            tmem_st1(tl + C::kColSfq + 2 + g, (uint32_t)(max(qe, 4) - 4) * 0x01010101u);  // lo rows: 2^-4 of it
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -446,8 +519,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             // every row of the tile sees at least what its first row sees
             const int all_see = W::sees(p, it.nq, it.len, (int)W::token(p, r0));
             for (int i = 0; i < take; ++i, ++ci) {
-                const int base = (wk.off + i) * kQtKeys, st = ci & 1;
-                ok = qt_warp_wait(&ms.full[st][1], (ci >> 1) & 1, abort);  // e; long done when the scores are
+                const int base = (wk.off + i) * kQtKeys, st = ci % C::kStages;
+                ok = qt_warp_wait(&ms.full[st][C::kWide ? 1 : 0], (ci / C::kStages) & 1, abort);  // e; long done when the scores are
                 if (!ok) break;
                 const int e = ms.e[st][q4 >> 1];
                 const float fe = (float)e, c = fmaxf(qc_pow2(e) * p.scale_log2, 1.2e-38f);  // > 0: masked stays -inf
@@ -457,10 +530,10 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 float t[32];
                 {
                     uint32_t a[2][16], b[2][16];
-                    tmem_ld16_issue(tl + kQtColS + 32 * g, a[0]);
-                    tmem_ld16_issue(tl + kQtColS + 64 + 32 * g, b[0]);
-                    tmem_ld16_issue(tl + kQtColS + 32 * g + 16, a[1]);
-                    tmem_ld16_issue(tl + kQtColS + 64 + 32 * g + 16, b[1]);
+                    tmem_ld16_issue(tl + C::kColS + 32 * g, a[0]);
+                    tmem_ld16_issue(tl + C::kColS + 64 + 32 * g, b[0]);
+                    tmem_ld16_issue(tl + C::kColS + 32 * g + 16, a[1]);
+                    tmem_ld16_issue(tl + C::kColS + 64 + 32 * g + 16, b[1]);
                     tmem_ld_wait_tied(a[0]);
                     tmem_ld_wait_tied(a[1]);
                     tmem_ld_wait_tied(b[0]);
@@ -484,11 +557,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     const int nvalid = max(0, it.len - base);
                     if (nvalid < kQtKeys) {
                         // no tokens here: zero value rows, so that weights of 0 meet finite codes
-                        uint8_t *kb = sK + st * kQtStage + nvalid * 128;
+                        uint8_t *kb = sK + st * C::kStage + nvalid * 128;
                         const int pieces = (kQtKeys - nvalid) * 8;  // per box
                         for (int x = tid - 32 * kQtSoft0; x < pieces; x += 256)
 #pragma unroll
-                            for (int d = 0; d < 4; ++d) *(uint4 *)(kb + d * kQtBox + x * 16) = make_uint4(0, 0, 0, 0);
+                            for (int d = 0; d < C::kBoxes; ++d) *(uint4 *)(kb + d * kQtBox + x * 16) = make_uint4(0, 0, 0, 0);
                     }
                 }
                 // block maxima (the lanes' 32 tokens are one scale block of one page; the
@@ -523,12 +596,14 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     h16[2 * j + 1] = f32x2_to_f16x2(t[4 * j + 2], t[4 * j + 3]);
                     hi[j] = f16x2_to_e4m3x2(h16[2 * j]) | f16x2_to_e4m3x2(h16[2 * j + 1]) << 16;
                 }
-                // Phi over the chunk's rope box (its scores are done)
+                // wide: Phi over the chunk's rope box (its scores are done)
                 const int sw = (tok >> 1) & 3;
-                uint8_t *ph = sK + st * kQtStage + 4 * kQtBox + tok * 64;
-                *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                fence_async_smem();
+                uint8_t *ph = (C::kWide ? sK + st * C::kStage + 4 * kQtBox : sP) + tok * 64;
+                if constexpr (C::kWide) {
+                    *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    fence_async_smem();
+                }
                 ok = group_wait();
                 if (!ok) break;
                 int bq[4], bm = -32768;
@@ -549,10 +624,10 @@ __global__ void __launch_bounds__(kQtThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j) l[j] *= __shfl_sync(~0u, f, j);
 #pragma unroll 1
-                        for (int k = 0; k < 10; ++k) {
+                        for (int k = 0; k < (C::kColS - C::kColO) / 32; ++k) {
                             float v[16];
                             uint32_t u[16];
-                            const uint32_t at = tl + kQtColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1);
+                            const uint32_t at = tl + C::kColO + 64 * (k >> 1) + 32 * g + 16 * (k & 1);
                             tmem_ld16(at, v);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(v[j] * __shfl_sync(~0u, f, 16 * (k & 1) + j));
@@ -566,13 +641,15 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     uint32_t wh = 0;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) wh |= (uint32_t)min(max(bq[k] - m_int + (127 - 8), 4), 250) << (8 * k);
-                    tmem_st1(tl + kQtColSfb + 4 * st + g, wh);
-                    tmem_st1(tl + kQtColSfb + 4 * st + 2 + g, wh - 0x04040404u);
+                    tmem_st1(tl + C::kColSfb + 4 * (ci & 1) + g, wh);
+                    tmem_st1(tl + C::kColSfb + 4 * (ci & 1) + 2 + g, wh - 0x04040404u);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.hi_ready);
+                if constexpr (C::kWide) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.hi_ready);
+                }
                 // the second terms, once the chunk before has read its own
                 uint32_t lo[8];
 #pragma unroll
@@ -583,7 +660,13 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     ok = false;
                     break;
                 }
-                uint8_t *pl = sP + tok * 64;
+                uint8_t *pl = sP + (C::kWide ? 0 : kQtTerm) + tok * 64;
+                if constexpr (!C::kWide) {
+                    *(uint4 *)(ph + ((2 * g) ^ sw) * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *(uint4 *)(ph + ((2 * g + 1) ^ sw) * 16) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
                 *(uint4 *)(pl + ((2 * g) ^ sw) * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 *(uint4 *)(pl + ((2 * g + 1) ^ sw) * 16) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 fence_async_smem();
@@ -616,19 +699,18 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
-            // 16 rows of the output: tile d's, the first tile's two shares added
+            // 16 rows of the output: tile d's, the two terms' shares added where they are apart
             auto load_o = [&](int d, int half, float (&v)[16]) {
-                const uint32_t at = tl + kQtColO + 32 * g + 16 * half;
-                if (d == 0) {
+                const uint32_t at = tl + C::kColO + 32 * g + 16 * half + (C::kWide ? (d ? 64 + 64 * d : 0) : 128 * d);
+                tmem_ld16(at, v);
+                if (!C::kWide || d == 0) {
                     float x[16];
                     tmem_ld16(at + 64, x);
-                    tmem_ld16(at, v);
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] += x[j];
-                } else {
-                    tmem_ld16(at + 64 + 64 * d, v);
                 }
             };
+            const bool real = KV >= 128 || q4 < KV / 32;  // 64 dims: half of the tile
             const float lsum = (ms.w[4 * g][lane] + ms.w[4 * g + 1][lane]) + (ms.w[4 * g + 2][lane] + ms.w[4 * g + 3][lane]);
             const bool bad = qe == 0;
             const float nan = __uint_as_float(0x7fffffffu);
@@ -642,33 +724,33 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
             }
             if (!whole) {
-                float *dst = p.part_o + ((size_t)slot * kQaTile + 32 * g) * kQtDV + 32 * q4 + lane;
+                float *dst = p.part_o + ((size_t)slot * kQaTile + 32 * g) * KV + 32 * q4 + lane;
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 2 * C::kTiles && real; ++k) {
                     float v[16];
                     load_o(k >> 1, k & 1, v);
-                    float *at = dst + 16 * (k & 1) * kQtDV + 128 * (k >> 1);
+                    float *at = dst + 16 * (k & 1) * KV + 128 * (k >> 1);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) at[j * kQtDV] = v[j];
+                    for (int j = 0; j < 16; ++j) at[j * KV] = v[j];
                 }
             } else {
                 // staged over the queries (every score is done), then whole rows
                 float *inv = (float *)ms.b + 32 * (warp - kQtSoft0);  // no block exponent is read any more
                 inv[lane] = bad ? nan : lsum > 0.f ? 1.f / lsum : 0.f;
                 __syncwarp();
-                uint8_t *out = sQ + 32 * g * kQtOutPitch + (32 * q4 + lane) * 2;
+                uint8_t *out = sQ + 32 * g * C::kPitch + (32 * q4 + lane) * 2;
 #pragma unroll 1
-                for (int k = 0; k < 8; ++k) {
+                for (int k = 0; k < 2 * C::kTiles && real; ++k) {
                     float v[16];
                     load_o(k >> 1, k & 1, v);
-                    uint8_t *at = out + 16 * (k & 1) * kQtOutPitch + 256 * (k >> 1);
+                    uint8_t *at = out + 16 * (k & 1) * C::kPitch + 256 * (k >> 1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4) {
                         const float4 x = *(const float4 *)(inv + 16 * (k & 1) + j);
                         const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
-                            *(__nv_bfloat16 *)(at + (j + y) * kQtOutPitch) = __float2bfloat16_rn(v[j + y] * f[y]);
+                            *(__nv_bfloat16 *)(at + (j + y) * C::kPitch) = __float2bfloat16_rn(v[j + y] * f[y]);
                     }
                 }
                 ok = group_sync();
@@ -678,10 +760,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     const int rw = 32 * g + 8 * q4 + k;
                     if (r0 + rw >= R) break;
                     const int tq = (int)W::token(p, r0 + rw), hd = r0 + rw - tq * p.H;
-                    uint4 *dst = (uint4 *)(p.o + (size_t)(it.q0 + tq) * p.o_stride + (size_t)hd * kQtDV);
-                    const uint4 *from = (const uint4 *)(sQ + rw * kQtOutPitch);
-                    dst[lane] = from[lane];
-                    dst[lane + 32] = from[lane + 32];
+                    uint4 *dst = (uint4 *)(p.o + (size_t)(it.q0 + tq) * p.o_stride + (size_t)hd * KV);
+                    const uint4 *from = (const uint4 *)(sQ + rw * C::kPitch);
+#pragma unroll
+                    for (int x = 0; x < KV / 8; x += 32)
+                        if (KV >= 256 || x + lane < KV / 8) dst[x + lane] = from[x + lane];
                 }
             }
             tc_fence_before();
@@ -698,8 +781,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     if (ms.abort) {
         if (tid == 0) {
             set_error(p.err, DSPARK_ERR_TIMEOUT);
-            for (int s = 0; s < 2; ++s)
-                for (int d = 0; d < 5; ++d)
+            for (int s = 0; s < C::kStages; ++s)
+                for (int d = 0; d < C::kBars; ++d)
                     if (ms.issued[s][d]) mbar_drain(&ms.full[s][d], ms.issued[s][d] >> 1);
         }
         __syncthreads();
@@ -710,19 +793,32 @@ __global__ void __launch_bounds__(kQtThreads, 1)
     }
 }
 
-cudaError_t launch_qattn_tc(const QaParams &p, int grid, cudaStream_t st) {
+template <int KV, int ROPE>
+static cudaError_t launch_width(const QaParams &p, int grid, cudaStream_t st) {
+    using C = QtCfg<KV, ROPE>;
+    constexpr int kSmem = qt_smem_bytes<KV, ROPE>();
     static bool attr = false;
     if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(qattn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kQtSmem);
+        const cudaError_t e = cudaFuncSetAttribute(qattn_tc_kernel<KV, ROPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    // the pool as 16-bit elements: boxes of 128 (64) bytes of 64 tokens
+    // the pool as 16-bit elements: boxes of 128 (the rope's: 64) bytes of 64 tokens
     CUtensorMap dims, rope;
-    if (!encode_u16_map(&dims, p.codes, (uint64_t)p.n_pages * kQcPage, kQtD, 128, kQcPage) ||
-        !encode_u16_map(&rope, p.codes, (uint64_t)p.n_pages * kQcPage, kQtD, 64, kQcPage))
-        return cudaErrorInvalidValue;
-    return launch_pdl(qattn_tc_kernel, dim3(grid), dim3(kQtThreads), (size_t)kQtSmem, st, dims, rope, p);
+    if (!encode_u16_map(&dims, p.codes, (uint64_t)p.n_pages * kQcPage, C::kD, 128, kQcPage)) return cudaErrorInvalidValue;
+    if (!C::kWide) rope = dims;
+    else if (!encode_u16_map(&rope, p.codes, (uint64_t)p.n_pages * kQcPage, C::kD, 64, kQcPage)) return cudaErrorInvalidValue;
+    return launch_pdl(qattn_tc_kernel<KV, ROPE>, dim3(grid), dim3(kQtThreads), (size_t)kSmem, st, dims, rope, p);
+}
+
+cudaError_t launch_qattn_tc(const QaParams &p, int kv_lora, int grid, cudaStream_t st) {
+    switch (kv_lora) {
+        case 512: return launch_width<512, 64>(p, grid, st);
+        case 256: return launch_width<256, 32>(p, grid, st);
+        case 128: return launch_width<128, 32>(p, grid, st);
+        case 64: return launch_width<64, 16>(p, grid, st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace ds

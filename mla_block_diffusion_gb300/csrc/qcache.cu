@@ -630,7 +630,7 @@ dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const ds
     p.part_ml = (float2 *)((char *)ws + L.ml);
     p.part_o = (float *)((char *)ws + L.o);
     p.err = (int *)ws;
-    return done(launch_qattn(p, c->kv_lora, c->d_rope, sms, (cudaStream_t)stream));
+    return done(launch_qattn(p, c->kv_lora, sms, (cudaStream_t)stream));
 }
 
 dspark_status dspark_qcache_check(void *ws, void *stream) {

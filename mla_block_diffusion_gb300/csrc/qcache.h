@@ -9,6 +9,7 @@ constexpr int kQcPage = 64;       // tokens per page
 constexpr int kQcEmax = 60;       // scale exponents lie in [-kQcEmax, kQcEmax]
 constexpr int kQcMaxBs = 1024;
 constexpr int kQaTile = 64;       // query rows (token, head) per work item
+constexpr int kQaChunk = 128;     // cached tokens per unit of work: two pages
 constexpr int kQaMaxGrid = 512;   // CTAs of an attention launch at most
 constexpr size_t kQcCtlBytes = 1024;  // error word, zero-filled by the caller
 
@@ -49,8 +50,7 @@ struct QaParams {
     int *err;
 };
 
-// The full latent width (512 + 64) on the 5th-generation tensor core.
-cudaError_t launch_qattn_tc(const QaParams &p, int grid, cudaStream_t st);
-cudaError_t launch_qattn(const QaParams &p, int kv_lora, int d_rope, int num_sms, cudaStream_t st);
+cudaError_t launch_qattn_tc(const QaParams &p, int kv_lora, int grid, cudaStream_t st);
+cudaError_t launch_qattn(const QaParams &p, int kv_lora, int num_sms, cudaStream_t st);
 
 }  // namespace ds
