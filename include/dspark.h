@@ -366,7 +366,8 @@ typedef struct {
  * (decode) over a drafted block to a chunk of a prompt:
  *   o = softmax(scale * q k^T) v,  k = the cached entry, v = its first kv_lora elements.
  * A query that sees no token gives o = 0 and lse = -inf. Scores, maxima and
- * sums are fp32; q enters to the full bf16 (elements below 2^-13 of their
+ * sums are fp32, and scores (scale * q k^T) have to stay within +-5 * 10^6,
+ * about as far as fp32 tells neighbouring scores apart; q enters to the full bf16 (elements below 2^-13 of their
  * row's largest keep an absolute error of 2^-22 of it), the softmax weights with at least 8
  * significant bits. Cached elements must be finite (the append writes no
  * other); entries past a request's length are never used. The workspace holds

@@ -105,15 +105,15 @@ struct QtMisc {
     int8_t e[STAGES][2];               // page scale exponents of a stage's pages
     int qe[kQaTile];                   // biased exponent that undoes a query row's scaling; 0: a non-finite query
     alignas(16) int lim[kQaTile];      // tokens that a row sees
-    alignas(16) int16_t b[2][2][4][32];  // block exponents by group, chunk parity, lane quarter, row; at an item's
-                                         // end the output factors of the group's warps
-    alignas(16) float w[8][32];        // per warp, one value per row
+    // Per warp, one value per row. Chunk i has w[i & 1] for its maxima, then what it adds to the exponents (e + 8 - b,
+    // which tells the group's other warps b), and w[~i & 1] for the sums' factors, once the group has met: the others
+    // have then read the chunk before's. Row sums and output factors of an item's end take turns likewise.
+    alignas(16) float w[2][8][32];
 };
 template <int KV, int ROPE>
 constexpr int qt_smem_bytes() {
     using C = QtCfg<KV, ROPE>;
     using Misc = QtMisc<C::kStages, C::kBars>;
-    static_assert(sizeof(Misc::b) == 8 * 32 * sizeof(float), "output factors");
     constexpr int n = C::kQ + C::kStages * C::kStage + C::kP + (int)sizeof(Misc);
     static_assert(n <= 232448, "shared memory");
     return n;
@@ -132,6 +132,8 @@ DS_DEVINL float redux_max(float v) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
     return m;
 }
+// An integer 0 <= x < 2^8 held as a float: its bits, below those of 2^23.
+DS_DEVINL uint32_t qt_bits(float x) { return __float_as_uint(x + 0x1p23f); }
 DS_DEVINL float qt_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -567,15 +569,15 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 // block maxima (the lanes' 32 tokens are one scale block of one page; the
                 // factor is positive, so the maximum of the raw scores is the one), then
                 // lane j prepares row j: b, and the exponent's addend e + 8 - b
-                float *wrow = ms.w[warp - kQtSoft0];
+                float *wrow = ms.w[ci & 1][warp - kQtSoft0], *wsum = ms.w[~ci & 1][warp - kQtSoft0];
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 m = make_float4(redux_max(t[j]), redux_max(t[j + 1]), redux_max(t[j + 2]), redux_max(t[j + 3]));
                     if (lane == 0) *(float4 *)(wrow + j) = m;
                 }
                 __syncwarp();
-                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c, fe), -16384.f), 16383.f));
-                ms.b[g][ci & 1][q4][lane] = (int16_t)(int)bf;
+                // (up to 2^23 differences from b are exact: as far as fp32 tells scores apart)
+                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c, fe), -0x1p23f), 0x1p23f));
                 __syncwarp();
                 wrow[lane] = (fe + 8.f) - bf;
                 group_arrive();  // the wait comes after the weights
@@ -606,15 +608,15 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
                 ok = group_wait();
                 if (!ok) break;
-                int bq[4], bm = -32768;
+                float bq[4], bm = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    bq[k] = ms.b[g][ci & 1][k][lane];
-                    bm = max(bm, bq[k]);
+                    bq[k] = ((float)ms.e[st][k >> 1] + 8.f) - ms.w[ci & 1][4 * g + k][lane];
+                    bm = fmaxf(bm, bq[k]);
                 }
-                const bool move = i == 0 || (float)bm - mref > (float)kQtMoveLog2;
+                const bool move = i == 0 || bm - mref > (float)kQtMoveLog2;
                 if (__any_sync(~0u, move)) {  // the same in the group's four warps
-                    const float mnew = move ? (float)bm : mref;
+                    const float mnew = move ? bm : mref;
                     const float f = i == 0 ? 0.f : qt_ex2(mref - mnew);
                     mref = mnew;
                     if (i > 0) {
@@ -635,12 +637,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                         }
                     }
                 }
-                const int m_int = (int)mref;
                 // scale words of row 32 g + lane: 2^(b - 8 - M) for hi, 2^-4 of it for lo, one byte per 32 tokens
                 {
                     uint32_t wh = 0;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) wh |= (uint32_t)min(max(bq[k] - m_int + (127 - 8), 4), 250) << (8 * k);
+                    for (int k = 0; k < 4; ++k) wh |= (qt_bits(fminf(fmaxf(bq[k] - mref + (127.f - 8.f), 4.f), 250.f)) & 0xffu) << (8 * k);
                     tmem_st1(tl + C::kColSfb + 4 * (ci & 1) + g, wh);
                     tmem_st1(tl + C::kColSfb + 4 * (ci & 1) + 2 + g, wh - 0x04040404u);
                 }
@@ -671,12 +672,12 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 *(uint4 *)(pl + ((2 * g + 1) ^ sw) * 16) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
                 fence_async_smem();
                 // lane j: what a weight of row j adds to the sum, 2^(b - 8 - M - e)
-                wrow[lane] = __int_as_float(max((int)bf - m_int - e + (127 - 8), 0) << 23);
+                wsum[lane] = __uint_as_float(qt_bits(fmaxf(bf - mref - fe + (127.f - 8.f), 0.f)) << 23);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ms.lo_ready);
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
-                    const float4 x = *(const float4 *)(wrow + j);
+                    const float4 x = *(const float4 *)(wsum + j);
                     l[j] = __fmaf_rn(t[j], x.x, l[j]);
                     l[j + 1] = __fmaf_rn(t[j + 1], x.y, l[j + 1]);
                     l[j + 2] = __fmaf_rn(t[j + 2], x.z, l[j + 2]);
@@ -695,7 +696,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     l[k] = keep + __shfl_xor_sync(~0u, send, w);
                 }
             }
-            ms.w[warp - kQtSoft0][lane] = l[0];
+            float (*const sums)[32] = ms.w[ci & 1];
+            sums[warp - kQtSoft0][lane] = l[0];
             ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
             };
             const bool real = KV >= 128 || q4 < KV / 32;  // 64 dims: half of the tile
-            const float lsum = (ms.w[4 * g][lane] + ms.w[4 * g + 1][lane]) + (ms.w[4 * g + 2][lane] + ms.w[4 * g + 3][lane]);
+            const float lsum = (sums[4 * g][lane] + sums[4 * g + 1][lane]) + (sums[4 * g + 2][lane] + sums[4 * g + 3][lane]);
             const bool bad = qe == 0;
             const float nan = __uint_as_float(0x7fffffffu);
             const int row = 32 * g + lane, r = r0 + row;
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
             } else {
                 // staged over the queries (every score is done), then whole rows
-                float *inv = (float *)ms.b + 32 * (warp - kQtSoft0);  // no block exponent is read any more
+                float *inv = ms.w[~ci & 1][warp - kQtSoft0];
                 inv[lane] = bad ? nan : lsum > 0.f ? 1.f / lsum : 0.f;
                 __syncwarp();
                 uint8_t *out = sQ + 32 * g * C::kPitch + (32 * q4 + lane) * 2;

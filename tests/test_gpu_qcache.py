@@ -342,6 +342,30 @@ def test_attend_sharp_and_far_apart_scales(M, kv, rope, sharp):
 
 
 @pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("size", [2.0 ** 13, 2.0 ** 18, 2.0 ** 23])
+def test_attend_huge_scores(M, kv, rope, size):
+    # every query looks at the last element alone, which is 1 or -1: scores are size * scale or its negative, equal weights
+    # for the tokens on the winning side. Products and the exponent's differences are exact; the weights' two terms and the
+    # output round (2^-9 each), the score's factors, sum and logarithm in fp32 (eight roundings of 2^-24).
+    t = Attend(M, kv, rope, 6, [700, 130, 90], [3, 1, 2], seed=15)
+    for b, n in enumerate(t.length):
+        for j in range(n):
+            pg = t.table[b, j // 64]
+            up = (j >= 500, j < 64, True)[b]
+            t.codes[pg, j % 64, -1] = Q.e4m3_encode(np.float64((1 if up else -1) / t.scales[pg]))
+    t.dev[0].copy_(torch.from_numpy(t.codes))
+    t.q = torch.zeros_like(t.q)
+    t.q[..., -1] = size * torch.tensor([1.0, -1.0]).repeat(3)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0
+    for b, n in enumerate(t.length):
+        a, z = t.cu[b], t.cu[b + 1]
+        wo, wl, absolute, _ = Q.attend(t.codes, t.scales, t.table[b], n, t.q[a:z].double().numpy(), kv, False, t.scale)
+        assert np.all(np.abs(o[a:z].double().cpu().numpy() - wo) <= 2.0 ** -8 * (np.abs(wo) + absolute))
+        assert np.all(np.abs(lse[a:z].double().cpu().numpy() - wl) <= 2.0 ** -21 * (1 + np.abs(wl)))
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
 def test_attend_one_token_outweighs_the_rest(M, kv, rope):
     # the first token takes half of every row's weight, thousands of others share the rest
     t = Attend(M, kv, rope, 8, [6000], [1], seed=6, sharp=0.4, exps=(-4, -3))
