@@ -75,7 +75,7 @@ struct QaWork {
     // Block-wide exclusive sum; *sum gets the total. scratch: one word per warp.
     template <typename T>
     static DS_DEVINL T scan(T v, T *scratch, T *sum) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         T inc = v;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -85,7 +85,8 @@ struct QaWork {
         if (lane == 31) scratch[warp] = inc;
         __syncthreads();
         T base = 0, all = 0;
-        for (int w = 0; w < nw; ++w) {
+#pragma unroll
+        for (int w = 0; w < kQaThreads / 32; ++w) {
             const T x = scratch[w];
             if (w < warp) base += x;
             all += x;
@@ -118,6 +119,15 @@ struct QaWork {
         return chunks(p, s.nq[b], s.len[b], i - s.first[b]);
     }
 
+    // n / d for 0 <= n < 2^23, 0 < d < 2^23: the approximate quotient (2 ulp, each at most 1/2) is off by one at most.
+    // Half the latency of the integer division; six of them stand between a call's start and its first load.
+    static DS_DEVINL int div24(int n, int d) {
+        int q = (int)__fdividef((float)n, (float)d);
+        const int r = n - q * d;
+        if (r < 0) --q;
+        if (r >= d) ++q;
+        return q;
+    }
     // Pieces, if their estimate is the better one. Every warp works it out for itself, a lane an item.
     static constexpr int kPieceItems = 160, kPieceRounds = kPieceItems / 32;
     DS_DEVINL bool find_piece(const QaParams &p, const Scratch &s, int cta, int grid, int items) {
@@ -136,19 +146,19 @@ struct QaWork {
         longest = (int)__reduce_max_sync(~0u, (unsigned)longest);
         if (longest >= 1 << 14) return false;  // (the counts below stay within 32 bits)
         // tight: would do if items wasted half a piece each; loose: always does
-        const int loose = (T + grid - items - 1) / (grid - items);
-        const int tight = (2 * T + 2 * grid - items - 1) / (2 * grid - items);
+        const int loose = div24(T + grid - items - 1, grid - items);
+        const int tight = div24(2 * T + 2 * grid - items - 1, 2 * grid - items);
         int n = 0;
 #pragma unroll
         for (int r = 0; r < kPieceRounds; ++r)
-            if (32 * r < items) n += (u[r] + tight - 1) / tight;
+            if (32 * r < items) n += div24(u[r] + tight - 1, tight);
         const int cut = (int)__reduce_add_sync(~0u, (unsigned)n) <= grid ? tight : loose;
-        if (min(cut, longest) > (T + grid - 1) / grid + kItemCost) return false;
+        if (min(cut, longest) > div24(T + grid - 1, grid) + kItemCost) return false;
         int base = 0;
 #pragma unroll
         for (int r = 0; r < kPieceRounds; ++r) {
             if (32 * r >= items) break;
-            const int w = (u[r] + cut - 1) / cut;
+            const int w = div24(u[r] + cut - 1, cut);
             int inc = w;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -166,9 +176,9 @@ struct QaWork {
                 item.nq = s.nq[item.b];
                 item.len = s.len[item.b];
                 item.chunks = units;
-                off = (int)((unsigned)kk * (unsigned)units / (unsigned)of);
+                off = div24(kk * units, of);
                 begin = off;
-                end = (int)((unsigned)(kk + 1) * (unsigned)units / (unsigned)of);
+                end = div24((kk + 1) * units, of);
                 piece_hi = cta - kk + of - 1;
             }
             base += __shfl_sync(~0u, inc, 31);
@@ -179,7 +189,8 @@ struct QaWork {
     // All threads of the block: this CTA's part of the work.
     DS_DEVINL void find(const QaParams &p, int cta, int grid, void *smem) {
         Scratch &s = *(Scratch *)smem;
-        const int nt = blockDim.x, tid = threadIdx.x;
+        constexpr int nt = kQaThreads;
+        const int tid = threadIdx.x;
         // requests: their tiles, and the first tile of each
         const int per = (p.bs + nt - 1) / nt, b0 = tid * per, b1 = min(p.bs, b0 + per);
         int mine = 0, all_tiles;

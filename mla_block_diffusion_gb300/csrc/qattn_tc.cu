@@ -62,7 +62,7 @@
 namespace ds {
 
 constexpr int kQtKeys = kQaChunk;                  // tokens per chunk
-constexpr int kQtThreads = 384;
+constexpr int kQtThreads = kQaThreads;
 constexpr int kQtSoft0 = 4;                        // first softmax warp; registers: 168 x 384 = 88 x 128 + 208 x 256
 constexpr int kQtRegsIssue = 88, kQtRegsSoft = 208;
 constexpr int kQtBox = kQtKeys * 128;              // bytes: 128 tokens x 128 dims
@@ -458,7 +458,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 mx = max(mx, __shfl_xor_sync(~0u, mx, 2));
                 const bool bad = mx >= 0x7f800000u;
                 const int a = min(mx < 0x00800000u ? 0 : 7 - ((int)(mx >> 23) - 127), 100);
-                const float f = bad ? 0.f : qc_pow2(a);
+                const float f = qc_pow2(a);
+                if (bad) {  // the row's outputs are NaN whatever it is here; scores stay finite
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j) v[j] = make_uint4(0, 0, 0, 0);
+                }
                 // the item before: its staged output has been read
                 if (items > 0 && !qt_warp_wait(&ms.item_done, (items - 1) & 1, abort)) {
                     ok = false;
@@ -478,7 +482,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                             uint32_t w[2], x[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const uint32_t two = bad ? 0u : u[2 * i + k];
+                                const uint32_t two = u[2 * i + k];
                                 const uint32_t h16 = f32x2_to_f16x2(__uint_as_float(two << 16) * f, __uint_as_float(two & 0xffff0000u) * f);
                                 w[k] = f16x2_to_e4m3x2(h16);
                                 x[k] = f16x2_to_e4m3x2(f16x2_sub_x16(h16, e4m3x2_to_f16x2_(w[k])));

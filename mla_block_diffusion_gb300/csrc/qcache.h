@@ -10,6 +10,7 @@ constexpr int kQcEmax = 60;       // scale exponents lie in [-kQcEmax, kQcEmax]
 constexpr int kQcMaxBs = 1024;
 constexpr int kQaTile = 64;       // query rows (token, head) per work item
 constexpr int kQaChunk = 128;     // cached tokens per unit of work: two pages
+constexpr int kQaThreads = 384;    // of an attention CTA
 constexpr int kQaMaxGrid = 512;   // CTAs of an attention launch at most
 constexpr size_t kQcCtlBytes = 1024;  // error word, zero-filled by the caller
 
