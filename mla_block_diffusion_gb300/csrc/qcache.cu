@@ -299,20 +299,31 @@ DS_DEVINL int amax_exponent(uint32_t bits) {
     return max(-kQcEmax, min(kQcEmax, e));
 }
 
-// n 16-byte pieces of codes move to a scale 2^-d times theirs (d < 0), rounded to nearest even.
+// n 16-byte pieces of a page's codes move to a scale 2^-d times theirs (d < 0), rounded to nearest even. All
+// of a thread's pieces are requested at once: one trip to memory and back, not one for each (32 requests x 5 layers,
+// one token each, every page's scale growing: 6.3 us against 7.9; 4.5 when none grows).
+template <int D>
 DS_DEVINL void move_codes(uint8_t *codes, int n, int d) {
+    constexpr int kPer = ((kQcPage - 1) * (D / 16) + kAppThreads - 1) / kAppThreads;
     const float f = qc_pow2(d);
-#pragma unroll 1
-    for (int i = threadIdx.x; i < n; i += kAppThreads) {
-        uint4 c = *(uint4 *)(codes + (size_t)i * 16);
-        uint32_t *w = (uint32_t *)&c;
+    uint4 v[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = threadIdx.x + k * kAppThreads;
+        v[k] = i < n ? *(const uint4 *)(codes + (size_t)i * 16) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int i = threadIdx.x + k * kAppThreads;
+        if (i >= n) break;
+        uint32_t *w = (uint32_t *)&v[k];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t h[2] = {e4m3x2_to_f16x2_(w[j] & 0xffffu), e4m3x2_to_f16x2_(w[j] >> 16)};
             const float2 x = __half22float2(*(const __half2 *)&h[0]), y = __half22float2(*(const __half2 *)&h[1]);
             w[j] = f32x2_to_e4m3x2(x.x * f, x.y * f) | f32x2_to_e4m3x2(y.x * f, y.y * f) << 16;
         }
-        *(uint4 *)(codes + (size_t)i * 16) = c;
+        *(uint4 *)(codes + (size_t)i * 16) = v[k];
     }
 }
 
@@ -407,7 +418,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) qcache_append_kernel(const App
             eo = e;
         }
         if (eo >= e) e = eo;
-        else move_codes(dst, off * (D / 16), eo - e);
+        else move_codes<D>(dst, off * (D / 16), eo - e);
     }
     const float inv = qc_pow2(-e);
     uint8_t *to = dst + (size_t)off * D;  // a row's pieces are its codes in order, and the rows follow one another
