@@ -17,7 +17,8 @@ DS_DEVINL float qa_ex2(float x) {
 // columns (all columns at the narrower widths), partials in CTA order. The warp's
 // lanes hold the partials' weights; sixteen partials are in flight, the first of
 // them requested together with the weights. Bound: latency and L2 (the
-// partials were just written).
+// partials were just written): 15 MB of partials (a block of 7 x 64 rows in 16
+// pieces each) add about 5 us to the attention.
 // ---------------------------------------------------------------------------
 constexpr int kQaCombineThreads = 256;
 

@@ -36,16 +36,21 @@
 // stages, both terms of the weights in a buffer of their own and every output tile
 // in both terms at once (N = 128: V's codes are read once).
 //
-// Bound, full width: a chunk is 2650 tensor clocks (scores 65 a step of N = 128;
-// outputs 51 a step of N = 64, which the 6 KB of operands that it reads from shared
-// memory bind, and 65 of N = 128), but two stages allow no more than two chunks in
-// a loop of loads (~1000), scores, softmax (~1800) and outputs: ~3600 clocks a
-// chunk, and an item costs ~16000 more (queries converted ~5000, output ~6000, the
-// pipeline drained and refilled). A third stage does not fit
-// beside the queries. Prompt chunks of 1200 rows x 64 heads:
-// 1310 us, 1.3 PFLOP/s of the formulas' products. Bound, smaller widths: the
-// softmax, ~2700 clocks a chunk whatever the width (32 requests of 1K to 16K
-// tokens and 64 heads: 37, 34 and 34 us; products by mma.sync in f16, codes
+// Bound, full width: shared memory's port. Operands of a chunk's products are 2560
+// wavefronts of 128 bytes (scores 18 steps of 8 KB, outputs 24 of 6 KB and 4 of
+// 8 KB; at 2650 clocks the tensor core alone would take little less), its load
+// writes 576, the softmax reads and writes about 500: 3640 against the 3600 clocks
+// that a chunk takes. An item costs ~16000 more (queries converted ~5000, output
+// ~6000, the pipeline drained and refilled). Two prompt
+// chunks of 700 to 1024 tokens x 64 heads over 4-8K tokens: 1318 us, 1.29 PFLOP/s
+// of the formulas' products; a block of 7 x 64 rows over 95000 tokens 87 us; 32
+// requests of 1-16K tokens, 64 rows each, 59 us, 3.1 TB/s.
+// Pairs of output products that share V (Phi's and Plo's of a tile) could take it
+// from the tensor core's collector, 39 clocks a product against 48; that needs
+// nothing issued between them, hence one issuing thread, and with one thread for
+// scores and outputs the prompt chunks take 1500 us. Bound, smaller widths: the
+// softmax, ~2500 clocks a chunk whatever the width (32 requests of 1K to 16K
+// tokens and 64 heads: 38, 35 and 34 us; products by mma.sync in f16, codes
 // widened on the way, took 130, 71 and 49).
 //
 // Roles (12 warps): warp 0 TMA producer; warp 1 issues the scores (and owns tensor

@@ -25,7 +25,9 @@ namespace ds {
 // Bound: latency (a dependent chain of two loads, a block scan and the search
 // of a token's request in shared memory) until the slot maps are long, then
 // their stores. Every CTA repeats the scan (up to 1024 requests, four a
-// thread) and fills its share of the outputs, so no CTA waits for another.
+// thread) and fills its share of the outputs, so no CTA waits for another. Cold and
+// alone, one request 6 us, 500 requests of 1 to 8192 tokens 10.5, 64 prompts 8;
+// back to back the host call is longer (8 to 9 us).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 constexpr int kPlanPer = kQcMaxBs / kPlanThreads;
