@@ -36,15 +36,18 @@
 // stages, both terms of the weights in a buffer of their own and every output tile
 // in both terms at once (N = 128: V's codes are read once).
 //
-// Bound, full width: shared memory's port. Operands of a chunk's products are 2560
-// wavefronts of 128 bytes (scores 18 steps of 8 KB, outputs 24 of 6 KB and 4 of
-// 8 KB; at 2650 clocks the tensor core alone would take little less), its load
-// writes 576, the softmax reads and writes about 500: 3640 against the 3600 clocks
-// that a chunk takes. An item costs ~16000 more (queries converted ~5000, output
-// ~6000, the pipeline drained and refilled). Two prompt
-// chunks of 700 to 1024 tokens x 64 heads over 4-8K tokens: 1318 us, 1.29 PFLOP/s
-// of the formulas' products; a block of 7 x 64 rows over 95000 tokens 87 us; 32
-// requests of 1-16K tokens, 64 rows each, 59 us, 3.1 TB/s.
+// Bound, full width: the loop of a stage, ~6700 clocks for the two chunks that the
+// stages hold, against 5300 of tensor work. From a part freed to a part full 1300;
+// scores 2000 (1165 alone; the other chunk's outputs run among them); softmax 2700
+// (its shared-memory accesses wait behind the products' operand reads, which take
+// the port's 2560 of 2650 clocks); first part free 600 later. A third stage, which
+// would hide it, does not fit beside the queries. No one part of it is enough by
+// itself: with half of the bytes loaded 6 % less, with 192 tensor clocks a chunk left
+// out 1 %. An item costs ~16000 clocks more (queries converted ~5000, output
+// ~6000, the pipeline drained and refilled). Two prompt chunks of 700 to 1024 tokens
+// x 64 heads over 4-8K tokens: 1290 us, 1.32 PFLOP/s of the formulas' products; a
+// block of 7 x 64 rows over 95000 tokens 86 us; 32 requests of 1-16K tokens, 64
+// rows each, 58 us, 3.2 TB/s.
 // Pairs of output products that share V (Phi's and Plo's of a tile) could take it
 // from the tensor core's collector, 39 clocks a product against 48; that needs
 // nothing issued between them, hence one issuing thread, and with one thread for
@@ -237,41 +240,49 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 if (j == 8) ex_n = exponent(first + 2 * (i + 8) + lane, pg_n);
                 const int pa = __shfl_sync(~0u, pg, 2 * j), pb = __shfl_sync(~0u, pg, 2 * j + 1);
                 const int ea = __shfl_sync(~0u, ex, 2 * j), eb = __shfl_sync(~0u, ex, 2 * j + 1);
-                if (lane == 0) {
+                if (qt_elect()) {
                     const int st = ci % C::kStages, n = max(0, min(2, npages - (first + 2 * i)));
                     const uint32_t par = (ci / C::kStages) & 1;
                     uint8_t *dst = sK + st * C::kStage;
+                    const int ya = pa * kQcPage, yb = pb * kQcPage;
                     // wide: the parts in the order in which they come free
+#pragma unroll
                     for (int x = 0; x < C::kBars; ++x) {
                         const int d = !C::kWide ? 0 : x < 2 ? x ^ 1 : x == 2 ? 2 : 7 - x;  // 1, 0, 2, rope, 3
                         if (ci >= C::kStages && !mbar_wait_bounded(&ms.free_[st][d], par ^ 1, abort)) {
                             ok = false;
                             break;
                         }
+                        uint64_t *bar = &ms.full[st][d];
+                        // 16-bit elements: 64 (the rope's box: 32) of them a box row
+                        if constexpr (C::kWide) {
+                            const int bytes = d < 4 ? kQtBox / 2 : C::kRope / 2;
+                            uint8_t *to = dst + d * kQtBox;
+                            if (n > 0) tma_load_2d(to, d < 4 ? &tm_dims : &tm_rope, d < 4 ? d * 64 : 256, ya, bar);
+                            if (n > 1) tma_load_2d(to + bytes, d < 4 ? &tm_dims : &tm_rope, d < 4 ? d * 64 : 256, yb, bar);
+                        } else {
+#pragma unroll
+                            for (int d2 = 0; d2 < C::kBoxes; ++d2) {
+                                if (n > 0) tma_load_2d(dst + d2 * kQtBox, &tm_dims, d2 * 64, ya, bar);
+                                if (n > 1) tma_load_2d(dst + d2 * kQtBox + kQtBox / 2, &tm_dims, d2 * 64, yb, bar);
+                            }
+                        }
                         if (x == 0) {
+                            // Every part's barrier at once, behind the first loads: each has completed its last phase (the
+                            // stage's scores are done when its first part is free), and none completes without this.
                             ms.e[st][0] = (int8_t)ea;
                             ms.e[st][1] = (int8_t)eb;
-                        }
-                        uint64_t *bar = &ms.full[st][d];
-                        const int bytes = d < 4 ? kQtBox / 2 : C::kRope / 2;
-                        if (n > 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * (C::kWide ? bytes : C::kStage / 2)));
-                        else mbar_arrive(bar);
-                        for (int k = 0; k < n; ++k) {
-                            const int y = (k ? pb : pa) * kQcPage;
-                            // 16-bit elements: 64 (the rope's box: 32) of them a box row
-                            if constexpr (C::kWide) {
-                                uint8_t *to = dst + d * kQtBox + k * bytes;
-                                if (d < 4) tma_load_2d(to, &tm_dims, d * 64, y, bar);
-                                else tma_load_2d(to, &tm_rope, 256, y, bar);
-                            } else {
-                                for (int d2 = 0; d2 < C::kBoxes; ++d2)
-                                    tma_load_2d(dst + d2 * kQtBox + k * (kQtBox / 2), &tm_dims, d2 * 64, y, bar);
+#pragma unroll
+                            for (int y = 0; y < C::kBars; ++y) {
+                                const int part = !C::kWide ? C::kStage : y < 4 ? kQtBox : C::kRope;
+                                if (n > 0) mbar_arrive_expect_tx(&ms.full[st][y], (uint32_t)(n * (part / 2)));
+                                else mbar_arrive(&ms.full[st][y]);
                             }
                         }
                         ms.issued[st][d] = (uint8_t)(1 | par << 1);
                     }
                 }
-                ok = __shfl_sync(~0u, (int)ok, 0) != 0;
+                ok = __all_sync(~0u, ok);
             }
             left -= take;
             if (left > 0) wk.next(p);
