@@ -8,12 +8,14 @@
 //     CTA, with the least `per` that the grid holds by either of two estimates;
 //   - ranges: the units of all items, in order, are cut into one equal range per
 //     CTA, which leaves no CTA idle but gives many of them two or more items.
-// A further item costs a CTA about QaWork::kItemCost units (its queries in, its
-// output out, the pipeline drained and refilled), so the division with the
-// smaller maximum of units, items counted so, is taken: pieces when items are
-// fewer than CTAs and of like size, ranges otherwise. (One block of 7 tokens and
-// 64 heads over 4096 tokens: 7 items of 32 chunks in 16 pieces each, against
-// ranges of 1.5 chunks that give six CTAs a second item.)
+// Ranges cost a CTA about QaWork::kItemCost units for its further items (queries
+// in, output out, the pipeline drained and refilled, partials written and read), so
+// pieces are taken unless they leave a CTA that many more units than an equal range:
+// when items are fewer than CTAs and not of too different sizes. Measured with costs
+// of 1, 4, 8, 14 and 24: 64 requests of 1K to 8K tokens 79, 66, 65, 65, 65 us; 100 of
+// 1K to 4K -, 76, 67, 67, 66; 140 of 1K to 4K 91, 91, 91, 82, 82; 20 blocks of 5
+// tokens over 500 to 9000 -, -, 101, 84, 81; 64 requests of 200 to 16K tokens, whose
+// longest is three times an equal range, -, -, 103, 102, 122.
 // An item that one CTA holds whole is finished there; one that is cut leaves a
 // partial per CTA (fp32 output, reference and sum per row) for the combine
 // kernel, which adds them in CTA order: the result does not depend on timing. A
@@ -64,7 +66,7 @@ struct QaWork {
         return max(1, (int)((seen + CH - 1) / CH));
     }
 
-    static constexpr int kItemCost = 4;
+    static constexpr int kItemCost = 14;
     long long begin, end;  // this CTA's units
     long long total;
     int parts;             // CTAs with units: never more than there are units, so that no range is empty

@@ -342,6 +342,20 @@ def test_attend_sharp_and_far_apart_scales(M, kv, rope, sharp):
 
 
 @pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("H,length,nq", [
+    (64, [20000], [1]), (20, [9000, 5000], [1, 2]), (5, [7000, 0, 64], [1, 1, 1]), (33, [4500], [3]), (64, [9000, 2049], [1, 1]),
+])
+def test_attend_few_long_requests(M, kv, rope, H, length, nq):
+    # one to four tiles in many pieces each: several warps add up a row
+    t = Attend(M, kv, rope, H, length, nq, seed=16)
+    o, lse = t.run(True)
+    assert t.cache.check() == 0
+    t.check(True, o, lse)
+    o2, lse2 = t.run(True)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
 @pytest.mark.parametrize("size", [2.0 ** 13, 2.0 ** 18, 2.0 ** 23])
 def test_attend_huge_scores(M, kv, rope, size):
     # every query looks at the last element alone, which is 1 or -1: scores are size * scale or its negative, equal weights
