@@ -106,7 +106,11 @@ struct QtCfg {
 template <int STAGES, int BARS>
 struct QtMisc {
     uint64_t full[STAGES][BARS], free_[STAGES][BARS];  // wide: boxes 0..3, rope
-    uint64_t s_full, s_free, hi_ready, lo_ready, pv_done, q_ready, item_done, mma_done, grp[2];
+    // Arrivals of one chunk on a barrier must not mix with those of the next. Scores, second terms and outputs follow one
+    // another through all warps; first terms do not (a group of warps may be one chunk ahead of the other, which
+    // may be moving its references), so they take turns on two barriers: the one of chunk i is used again
+    // for chunk i + 2, behind the outputs of chunk i.
+    uint64_t s_full, s_free, hi_ready[2], lo_ready, pv_done, q_ready, item_done, mma_done, grp[2];
     uint32_t tmem;
     volatile int abort;
     uint8_t issued[STAGES][8];         // loads in flight: 1 | parity << 1, per part
@@ -178,7 +182,8 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             }
         mbar_init(&ms.s_full, 1);
         mbar_init(&ms.s_free, 8);
-        mbar_init(&ms.hi_ready, 8);
+        mbar_init(&ms.hi_ready[0], 8);
+        mbar_init(&ms.hi_ready[1], 8);
         mbar_init(&ms.lo_ready, 8);
         mbar_init(&ms.pv_done, 1);
         mbar_init(&ms.q_ready, 8);
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                                 mma_mx_e4m3_w(col, a + 256 * k, kHi128, b + 128 * k, kHi64, idesc_mx_e4m3(128, 64, k) | kIdescBothMN, sfa, sf,
                                               k > 0 ? 1u : acc);
                         };
-                        ok = mbar_wait_bounded(&ms.hi_ready, ci & 1, abort);
+                        ok = mbar_wait_bounded(&ms.hi_ready[ci & 1], (ci >> 1) & 1, abort);
                         if (!ok) break;
                         tc_fence_after();
                         tile(1, phi, sfb, first);
@@ -669,7 +674,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ms.hi_ready);
+                    if (lane == 0) mbar_arrive(&ms.hi_ready[ci & 1]);
                 }
                 // the second terms, once the chunk before has read its own
                 uint32_t lo[8];

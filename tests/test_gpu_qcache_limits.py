@@ -1,0 +1,70 @@
+"""The 8-bit latent cache on the GPU at the ends of its documented ranges, and where it reports instead of answering.
+
+Attention is compared at the tolerances of test_gpu_qcache.Attend.check, which that file derives."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import qcache as Q
+from oracle.formats import E4M3_TABLE
+from test_gpu_qcache import LATENTS, Attend, M, ints  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+class Laid(Attend):
+    """Attention inputs from given pages: codes [n, 64, D], scales [n], table [bs, pages], q [total, H, D]."""
+
+    def __init__(self, M, kv, codes, scales, table, length, nq, q):
+        self.kv, self.D, self.H, self.length, self.nq = kv, codes.shape[2], q.shape[1], length, nq
+        self.codes, self.scales, self.table = codes, np.asarray(scales, dtype=np.float32), np.asarray(table, dtype=np.int32)
+        self.cu = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
+        self.q, self.scale = torch.from_numpy(q).to(torch.bfloat16), 1.3 / np.sqrt(self.D)
+        self.dev = [torch.from_numpy(codes).cuda(), torch.from_numpy(self.scales).cuda(), ints(self.table)]
+        self.cache = M.QCache(kv, self.D - kv, [self.dev[0]], [self.dev[1]], self.dev[2], n_heads=self.H)
+        self.args = (ints(self.cu), ints(length))
+
+
+def page(rng, kv, D, e, last, size=1.0):
+    """A page at scale 2^e: normal values, zero key-only elements but for the last, which steers the scores."""
+    v = np.zeros((64, D))
+    v[:, :kv] = rng.normal(0, size, (64, kv))
+    v[:, -1] = last
+    return Q.e4m3_encode(v * 2.0 ** -e)
+
+
+def check_steered(t, o, lse):
+    """Like Attend.check, for queries whose last element alone is not zero: both its terms are exact, so that the scores
+    lose only what fp32 does."""
+    o, lse, q = o.double().cpu().numpy(), lse.double().cpu().numpy(), t.q.double().numpy()
+    for b, n in enumerate(t.length):
+        a, z = t.cu[b], t.cu[b + 1]
+        wo, wl, absolute, top = Q.attend(t.codes, t.scales, t.table[b], n, q[a:z], t.kv, False, t.scale)
+        ds, v = 2.0 ** -16 * top, (E4M3_TABLE[t.codes] * t.scales[:, None, None])[:, :, :t.kv]
+        tol = 2.0 ** -8 * np.abs(wo) + (2.0 ** -8 + 2 * ds[..., None]) * absolute + 2.0 ** -17 * np.abs(v).max()
+        assert np.all(np.abs(o[a:z] - wo) <= tol), b
+        assert np.all(np.abs(lse[a:z] - wl) <= ds + 2.0 ** -22 * (1 + np.abs(wl))), b
+
+
+# Divisions of the work on 152 SMs: with 304 requests of 11 chunks every CTA holds whole requests; 76 requests of 24
+# chunks are cut in two pieces of 12 chunks.
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("H", [2, 34])
+def test_attend_references_that_move_with_every_chunk(M, kv, rope, H):
+    # Scores of the first two heads grow by 2^70 from chunk to chunk, so that what came before is scaled away, while the
+    # others' stay at zero: the warps of those rows fall behind the others', whose references stay. The result is right,
+    # and the same every time.
+    D, bs, rng = kv + rope, 76, np.random.default_rng(20)
+    levels = [-(448 - 32 * i) / 256 for i in range(12)]
+    codes = np.stack([page(rng, kv, D, -8, x) for x in levels])
+    row = np.repeat(list(range(12)) * 2, 2)
+    q = np.zeros((bs, H, D))
+    q[:, :2, -1] = 14 * 70 * np.log(2) / (1.75 * 1.3 / np.sqrt(D))
+    t = Laid(M, kv, codes, [2.0 ** -8] * 12, [row] * bs, [3072] * bs, [1] * bs, q)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0
+    check_steered(t, o, lse)
+    for _ in range(20):
+        o2, lse2 = t.run(False)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert t.cache.check() == 0
