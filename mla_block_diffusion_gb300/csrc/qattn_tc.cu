@@ -18,11 +18,13 @@
 //     hi and lo / 16 (8 significant bits, absolute error 2^-14), and the block's
 //     E8M0 scale is 2^(b - 8 - M) with M the row's reference: E4M3 alone spans 17
 //     binades, too few beside a token that outweighs thousands of others; the
-//     scale of every 32 tokens follows their own size. M is the first chunk's
-//     maximum and moves only when a block exceeds it by 2^60 (O and the sum are
-//     then rescaled), since E8M0 and the fp32 accumulator have the range: the
-//     usual rescaling of O whenever a maximum grows does not exist here.
-//     Row sums add the unrounded weights times 2^(b - 8 - M - e) in fp32.
+//     scale of every 32 tokens follows their own size. Row sums add the unrounded
+//     weights times 2^(b - 8 - M - e) in fp32, so M is the first chunk's maximum of
+//     b and b - e (an all-zero page has e = -60: its tokens weigh 2^60 times as much
+//     in the sum as in O). It moves only when a block exceeds it by 2^60 (O and the
+//     sum are then rescaled): E8M0 holds that, and a token's share of an element of
+//     O stays below 2^70, its share of the sum below 2^61. The usual rescaling of O
+//     whenever a maximum grows does not exist here.
 //
 // The full width, 512 + 64. Tensor memory: O^T 5 x 64 columns, S^T 128, scale
 // words. Shared memory: the query tile 72 KB, two chunk stages of 72 KB (four
@@ -636,8 +638,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 float bq[4], bm = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    bq[k] = ((float)ms.e[st][k >> 1] + 8.f) - ms.w[ci & 1][4 * g + k][lane];
-                    bm = fmaxf(bm, bq[k]);
+                    const float ek = (float)ms.e[st][k >> 1], s = 8.f - ms.w[ci & 1][4 * g + k][lane];  // s = b - e
+                    bq[k] = s + ek;
+                    bm = fmaxf(bm, s + fmaxf(ek, 0.f));
                 }
                 const bool move = i == 0 || bm - mref > (float)kQtMoveLog2;
                 if (__any_sync(~0u, move)) {  // the same in the group's four warps

@@ -68,3 +68,25 @@ def test_attend_references_that_move_with_every_chunk(M, kv, rope, H):
         o2, lse2 = t.run(False)
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert t.cache.check() == 0
+
+
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("bs,chunks", [(304, 11), (76, 24)])
+def test_attend_zero_pages_behind_low_scores(M, kv, rope, bs, chunks):
+    # Scores of 2^-110 on pages of scale 2^-8, then 1280 tokens and more on all-zero pages (scale 2^-60), where the
+    # scores are zero; one normal page at the end of the longer ones. The zero pages outweigh what comes first by 2^110,
+    # and value scales are 2^52 apart.
+    D, H, rng = kv + rope, 2, np.random.default_rng(21)
+    codes = np.stack([page(rng, kv, D, -8, -1.75), page(rng, kv, D, -8, -1.75), np.zeros((64, D), dtype=np.uint8),
+                      page(rng, kv, D, -7, 0.0)])
+    row = [0, 1] + [2] * (2 * chunks - 2)
+    if chunks == 24:
+        row[-1] = 3
+    q = np.zeros((bs, H, D))
+    q[:, :, -1] = np.linspace(76.0, 76.9, bs * H).reshape(bs, H) / (1.75 * 1.3 / np.sqrt(D))
+    t = Laid(M, kv, codes, [2.0 ** -8, 2.0 ** -8, 2.0 ** -60, 2.0 ** -7], [row] * bs, [128 * chunks] * bs, [1] * bs, q)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0 and torch.isfinite(lse).all()
+    check_steered(t, o, lse)
