@@ -21,6 +21,11 @@ DS_DEVINL float qa_ex2(float x) {
 // pieces each) add about 5 us to the attention.
 // ---------------------------------------------------------------------------
 constexpr int kQaCombineThreads = 256;
+// Partials are weighed by 2^(their reference - the largest + 20). A piece's sum may lie 2^60 above its reference
+// (scores that rose behind its first chunk) or below it (pages of scale 2^60), so a piece whose reference is 2^-126 of
+// the largest one can still count; with 2^20 more a flushed weight stands for less than 2^-25 of the row's sum a token.
+// The most that a sum can reach is then 2^(70 + 31 + 20), an element of O over 2^31 tokens.
+constexpr float kQaHeadroom = 20.f;
 
 // A task of the combine for warps that share it: a pair of rows and up to 128 columns of one split item. (The loop of
 // the kernel for one warp a task keeps its own: one kernel with both forms cost the other calls 1 to 3 us.)
@@ -62,7 +67,7 @@ struct QaTask {
     static DS_DEVINL float reference(float m) {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-        return m == -INFINITY ? 0.f : m;
+        return m == -INFINITY ? 0.f : m - kQaHeadroom;
     }
     static DS_DEVINL void add(float4 &o, float w, const float4 &v) {
         o.x += w * v.x;
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
         auto reference = [&](float m) {
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-            return m == -INFINITY ? 0.f : m;
+            return m == -INFINITY ? 0.f : m - kQaHeadroom;
         };
         auto add = [&](float4 &o, float w, const float4 &v) {
             o.x += w * v.x;

@@ -90,3 +90,18 @@ def test_attend_zero_pages_behind_low_scores(M, kv, rope, bs, chunks):
     o, lse = t.run(False)
     assert t.cache.check() == 0 and torch.isfinite(lse).all()
     check_steered(t, o, lse)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+def test_attend_pieces_at_both_ends_of_the_page_scales(M, kv, rope):
+    # The first of two pieces begins with a page of scale 2^60 and scores of zero, the second with scores of 2^-67 on a
+    # page of 2^-8 and goes on with 2^-8: together those tokens weigh a sixteenth of the first page.
+    D, H, bs, rng = kv + rope, 2, 76, np.random.default_rng(22)
+    codes = np.stack([page(rng, kv, D, 60, 0.0, size=2.0 ** 60), page(rng, kv, D, -8, -1.75), page(rng, kv, D, -8, -56 / 256)])
+    row = [0, 1] + [2] * 22 + [1, 1] + [2] * 22
+    q = np.zeros((bs, H, D))
+    q[:, :, -1] = np.linspace(46.5, 46.9, bs * H).reshape(bs, H) / (1.75 * 1.3 / np.sqrt(D))
+    t = Laid(M, kv, codes, [2.0 ** 60, 2.0 ** -8, 2.0 ** -8], [row] * bs, [3072] * bs, [1] * bs, q)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0
+    check_steered(t, o, lse)
