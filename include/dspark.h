@@ -366,15 +366,17 @@ typedef struct {
  * (decode) over a drafted block to a chunk of a prompt:
  *   o = softmax(scale * q k^T) v,  k = the cached entry, v = its first kv_lora elements.
  * A query that sees no token gives o = 0 and lse = -inf. Scores, maxima and
- * sums are fp32, and scores (scale * q k^T) have to stay within +-5 * 10^6,
- * about as far as fp32 tells neighbouring scores apart; q enters to the full bf16 (elements below 2^-13 of their
- * row's largest keep an absolute error of 2^-22 of it), the softmax weights with at least 8
- * significant bits. Cached elements must be finite (the append writes no
+ * sums are fp32. Scores (scale * q k^T) have to stay within +-5 * 10^6, about as
+ * far as fp32 tells neighbouring scores apart; a row is NaN if the largest score of
+ * 32 tokens that it sees (32i .. 32i + 31 of its request) lies beyond +-5.9 * 10^6.
+ * q enters to the full bf16 (elements below 2^-13 of their row's largest keep an
+ * absolute error of 2^-22 of it), the softmax weights with at least 8 significant
+ * bits. Cached elements must be finite (the append writes no
  * other); entries past a request's length are never used. The workspace holds
  * split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of
  * range (those requests' queries are skipped) or a page number out of range
  * (read as page 0), DSPARK_ERR_BAD_INPUT for a non-finite query (its row's
- * outputs are NaN) or a scale that is no power of two in range,
+ * outputs are NaN), scores out of range or a scale that is no power of two in range,
  * DSPARK_ERR_TIMEOUT. */
 dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const dspark_qattn_t *a, int bs, void *ws,
                                    size_t ws_bytes, void *stream);

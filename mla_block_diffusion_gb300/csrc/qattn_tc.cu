@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             if (lane == 0) mbar_arrive(&ms.q_ready);
 
             float l[32], mref = 0.f;  // mref: the reference of row 32 g + lane
+            bool lost = false;        // that row has no answer
 #pragma unroll
             for (int j = 0; j < 32; ++j) l[j] = 0.f;
             // every row of the tile sees at least what its first row sees
@@ -603,8 +604,11 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                     if (lane == 0) *(float4 *)(wrow + j) = m;
                 }
                 __syncwarp();
-                // (up to 2^23 differences from b are exact: as far as fp32 tells scores apart)
-                const float bf = rintf(fminf(fmaxf(__fmaf_rn(wrow[lane], c, fe), -0x1p23f), 0x1p23f));
+                // (up to 2^23 differences from b are exact: as far as fp32 tells scores apart; a block that the row sees
+                // and whose maximum lies beyond that, or is none, makes the row NaN)
+                const float bx = __fmaf_rn(wrow[lane], c, fe);
+                if (!(fabsf(bx) <= 0x1p23f)) lost |= ms.lim[32 * g + lane] > base + 32 * q4;
+                const float bf = rintf(fminf(fmaxf(bx, -0x1p23f), 0x1p23f));
                 __syncwarp();
                 wrow[lane] = (fe + 8.f) - bf;
                 group_arrive();  // the wait comes after the weights
@@ -725,7 +729,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
             }
             float (*const sums)[32] = ms.w[ci & 1];
-            sums[warp - kQtSoft0][lane] = l[0];
+            const float nan = __uint_as_float(0x7fffffffu);
+            sums[warp - kQtSoft0][lane] = lost ? nan : l[0];
+            if (lost) set_error(p.err, DSPARK_ERR_BAD_INPUT);
             ok = group_sync() && qt_warp_wait(&ms.pv_done, (ci - 1) & 1, abort);
             if (!ok) break;
             tc_fence_after();
@@ -742,8 +748,7 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             };
             const bool real = KV >= 128 || q4 < KV / 32;  // 64 dims: half of the tile
             const float lsum = (sums[4 * g][lane] + sums[4 * g + 1][lane]) + (sums[4 * g + 2][lane] + sums[4 * g + 3][lane]);
-            const bool bad = qe == 0;
-            const float nan = __uint_as_float(0x7fffffffu);
+            const bool bad = qe == 0 || isnan(lsum);
             const int row = 32 * g + lane, r = r0 + row;
             if (q4 == 0) {
                 if (!whole) {

@@ -105,3 +105,29 @@ def test_attend_pieces_at_both_ends_of_the_page_scales(M, kv, rope):
     o, lse = t.run(False)
     assert t.cache.check() == 0
     check_steered(t, o, lse)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("length", [[700, 130, 90], [9000, 130, 90]])
+def test_attend_reports_scores_beyond_the_range(M, kv, rope, length):
+    # A query that looks at the last element alone, which is 1 or -1: scores of +-12 million or infinite. Its row is NaN
+    # and reported; no other row changes.
+    t = Attend(M, kv, rope, 6, length, [3, 1, 2], seed=23)
+    for b, n in enumerate(t.length):
+        for j in range(n):
+            pg = t.table[b, j // 64]
+            up = (j >= 500, j < 64, True)[b]
+            t.codes[pg, j % 64, -1] = Q.e4m3_encode(np.float64((1 if up else -1) / t.scales[pg]))
+    t.dev[0].copy_(torch.from_numpy(t.codes))
+    o, lse = t.run(True)
+    assert t.cache.check() == 0
+    t.check(True, o, lse)
+    hit = torch.zeros(6, 6, dtype=torch.bool, device="cuda")
+    for i, h, value in ((0, 1, 1.2e7), (1, 5, -1.2e7), (2, 0, 3e38 * t.scale), (3, 3, -3e38 * t.scale), (4, 2, 1.2e7), (5, 4, -1.2e7)):
+        t.q[i, h] = 0
+        t.q[i, h, -1] = value / t.scale
+        hit[i, h] = True
+    o2, lse2 = t.run(True)
+    assert t.cache.check() == 17
+    assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
+    assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
