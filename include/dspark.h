@@ -375,9 +375,10 @@ typedef struct {
  * other); entries past a request's length are never used. The workspace holds
  * split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of
  * range (those requests' queries are skipped) or a page number out of range
- * (read as page 0), DSPARK_ERR_BAD_INPUT for a non-finite query (its row's
- * outputs are NaN), scores out of range or a scale that is no power of two in range,
- * DSPARK_ERR_TIMEOUT. */
+ * (it is not read, and the outputs of rows that see its tokens are NaN),
+ * DSPARK_ERR_BAD_INPUT for a non-finite query (its row's outputs are NaN), scores
+ * out of range or a page's scale that is no power of two in range (the outputs of
+ * rows that see its tokens are NaN), DSPARK_ERR_TIMEOUT. */
 dspark_status dspark_qcache_attend(const dspark_qcache_t *c, int layer, const dspark_qattn_t *a, int bs, void *ws,
                                    size_t ws_bytes, void *stream);
 

@@ -78,6 +78,7 @@ constexpr int kQtRegsIssue = 88, kQtRegsSoft = 208;
 constexpr int kQtBox = kQtKeys * 128;              // bytes: 128 tokens x 128 dims
 constexpr int kQtTerm = kQtKeys * 64;              // one E4M3 term of the weights: 128 tokens x 64 rows
 constexpr int kQtMoveLog2 = 60;
+constexpr int kQtLost = kQcEmax + 1;               // in the place of a page's exponent: rows that see the page are NaN
 
 // kWide: the full width, 512 + 64. The others leave room: more stages, whole
 // stages handed over at once, both terms of the weights in a buffer of their own
@@ -221,17 +222,24 @@ __global__ void __launch_bounds__(kQtThreads, 1)
             const int take = (int)min((long long)(it.chunks - wk.off), left);
             const int npages = (it.len + kQcPage - 1) / kQcPage, first = 2 * wk.off;
             const int32_t *row = p.page_table + (size_t)it.b * p.max_pages;
-            auto page = [&](int i) {  // page number i of the request (0 past its end)
+            // page number i of the request (0 past its end; one outside the pool becomes the first behind the pool, where
+            // the copy reads nothing and fills in zeros)
+            auto page = [&](int i) {
                 int pg = i < npages && i < first + 2 * take ? row[i] : 0;
                 if (pg < 0 || pg >= p.n_pages) {
                     set_error(p.err, DSPARK_ERR_OOB);
-                    pg = 0;
+                    pg = p.n_pages;
                 }
                 return pg;
             };
+            // its scale's exponent; kQtLost: a page without a number or a scale
             auto exponent = [&](int i, int pg) {
                 int e = 0;
-                if (i < npages && i < first + 2 * take && !qc_scale_exponent(p.scales[pg], &e)) set_error(p.err, DSPARK_ERR_BAD_INPUT);
+                if (pg == p.n_pages) return kQtLost;
+                if (i < npages && i < first + 2 * take && !qc_scale_exponent(p.scales[pg], &e)) {
+                    set_error(p.err, DSPARK_ERR_BAD_INPUT);
+                    return kQtLost;
+                }
                 return e;
             };
             int pg = page(first + lane), ex = exponent(first + lane, pg), pg_n = 0, ex_n = 0;
@@ -605,9 +613,9 @@ __global__ void __launch_bounds__(kQtThreads, 1)
                 }
                 __syncwarp();
                 // (up to 2^23 differences from b are exact: as far as fp32 tells scores apart; a block that the row sees
-                // and whose maximum lies beyond that, or is none, makes the row NaN)
+                // and whose maximum lies beyond that, or is none, makes the row NaN; so does a lost page)
                 const float bx = __fmaf_rn(wrow[lane], c, fe);
-                if (!(fabsf(bx) <= 0x1p23f)) lost |= ms.lim[32 * g + lane] > base + 32 * q4;
+                if (!(fabsf(bx) <= 0x1p23f) || e == kQtLost) lost |= ms.lim[32 * g + lane] > base + 32 * q4;
                 const float bf = rintf(fminf(fmaxf(bx, -0x1p23f), 0x1p23f));
                 __syncwarp();
                 wrow[lane] = (fe + 8.f) - bf;

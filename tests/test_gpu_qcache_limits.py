@@ -131,3 +131,36 @@ def test_attend_reports_scores_beyond_the_range(M, kv, rope, length):
     assert t.cache.check() == 17
     assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
     assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("length,nq,at", [
+    ([80, 200, 100], [1, 150, 2], 2),          # many tiles; causal: the first 78 queries end before the bad page
+    ([80, 20000, 100], [1, 1, 2], 100),        # one request in many pieces
+    ([80, 65, 100], [1, 3, 2], 1),             # the last page, one token
+])
+def test_attend_marks_rows_over_bad_pages(M, kv, rope, causal, length, nq, at):
+    # a page number outside the pool, or a scale that is no power of two in range: the rows that see that page are NaN,
+    # and no others
+    t = Attend(M, kv, rope, 4, length, nq, seed=24)
+    o, lse = t.run(causal)
+    assert t.cache.check() == 0
+    t.check(causal, o, lse)
+    i = np.arange(nq[1])
+    sees = length[1] - nq[1] + i + 1 if causal else np.full(nq[1], length[1])
+    hit = torch.zeros(sum(nq), dtype=torch.bool, device="cuda")
+    hit[1:1 + nq[1]] = torch.from_numpy(sees > 64 * at).cuda()
+
+    def check(status):
+        o2, lse2 = t.run(causal)
+        assert t.cache.check() == status
+        assert torch.isnan(o2[hit]).all() and torch.isnan(lse2[hit]).all()
+        assert torch.equal(o2[~hit], o[~hit]) and torch.equal(lse2[~hit], lse[~hit])
+    for number in (-1, len(t.scales), 1 << 30, -(1 << 31)):
+        t.dev[2][1, at] = number
+        check(18)
+    t.dev[2].copy_(ints(t.table))
+    for scale in (0.75, 0.0, -1.0, float("nan"), float("inf"), 2.0 ** 61, 2.0 ** -61):
+        t.dev[1][int(t.table[1, at])] = scale
+        check(17)
