@@ -324,7 +324,9 @@ typedef struct {
  * Device errors (DSPARK_ERR_OOB): a length or want outside [0, 64 max_pages]
  * (that request stays as it is), ring_state outside the ring (no page is
  * taken), more pages than the ring holds given back (the rest is dropped), a
- * page number outside [0, n_pages) in the ring (its tokens get slot -1). */
+ * page number outside [0, n_pages) that is taken from the ring or given back, or
+ * whose page new tokens go to (the number itself moves between ring and page table
+ * as it is, so each call that meets it reports it; its tokens get slot -1). */
 dspark_status dspark_qcache_plan(const dspark_qcache_t *c, const dspark_qplan_t *p, int bs, int max_new, int max_seg,
                                  void *ws, size_t ws_bytes, void *stream);
 

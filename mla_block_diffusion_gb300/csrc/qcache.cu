@@ -197,7 +197,9 @@ __global__ void __launch_bounds__(kPlanThreads) qcache_plan_kernel(const PlanPar
         const int at = (s_want[b] + kQcPage - 1) / kQcPage + (int)(i - s_give[b]);
         unsigned to = (unsigned)head + (unsigned)count + i;
         if (to >= (unsigned)a.n_pages) to -= (unsigned)a.n_pages;
-        a.p.ring[to] = a.page_table[(size_t)b * a.max_pages + at];
+        const int pg = a.page_table[(size_t)b * a.max_pages + at];
+        if (pg < 0 || pg >= a.n_pages) set_error(a.err, DSPARK_ERR_OOB);
+        a.p.ring[to] = pg;
     }
     // slots and positions, four tokens a thread
     for (int i0 = 4 * gt; i0 < a.max_new; i0 += 4 * gn) {

@@ -7,7 +7,7 @@ import torch
 
 from oracle import qcache as Q
 from oracle.formats import E4M3_TABLE
-from test_gpu_qcache import LATENTS, Attend, M, ints  # noqa: F401
+from test_gpu_qcache import LATENTS, Attend, M, Plan, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -164,3 +164,11 @@ def test_attend_marks_rows_over_bad_pages(M, kv, rope, causal, length, nq, at):
     for scale in (0.75, 0.0, -1.0, float("nan"), float("inf"), 2.0 ** 61, 2.0 ** -61):
         t.dev[1][int(t.table[1, at])] = scale
         check(17)
+
+
+def test_plan_reports_a_bad_page_when_it_comes_back(M):
+    # a ring that holds a page outside the pool: reported when it is taken, and again when its request gives it back
+    g = Plan(M, [0], [2], np.zeros((1, 4)), np.full(8, 8), (0, 1), 4, 4)
+    assert g.run() == 18 and g.outs[0].item() == 2 and g.outs[3].cpu().tolist() == [-1] * 4
+    h = Plan(M, [2], [0], g.t.cpu().numpy(), g.ring.cpu().numpy(), tuple(g.outs[1].tolist()), 4, 4)
+    assert h.run() == 18 and h.outs[0].item() == 0
