@@ -339,10 +339,11 @@ enum { DSPARK_ENTRY_BF16 = 0, DSPARK_ENTRY_FP32 = 1 };
  * amax <= 448 * 2^e over its new rows, or its present scale if that is larger
  * and the page holds tokens before the first new one; the codes of those are
  * then moved to the new scale. Rounding is to nearest even, saturating.
- * Rows with slot -1 are skipped. row_stride and layer_stride count elements
+ * The slots of such a run of rows follow one another, or all are -1: then it is
+ * skipped. row_stride and layer_stride count elements
  * (multiples of 8 for bf16, 4 for fp32; layer_stride is unused for one layer).
- * Device errors: DSPARK_ERR_OOB for a slot or row outside its range
- * (that page's rows are not written), DSPARK_ERR_BAD_INPUT for an element that
+ * Device errors: DSPARK_ERR_OOB for a slot or row outside its range or a run whose
+ * slots do not follow one another (its rows are not written), DSPARK_ERR_BAD_INPUT for an element that
  * is not finite or above 448 * 2^60 (NaN is stored as 0, the others as +-448)
  * or a held page's scale that is no power of two in range. */
 dspark_status dspark_qcache_append(const dspark_qcache_t *c, const void *entries, int entry_type, int64_t row_stride,

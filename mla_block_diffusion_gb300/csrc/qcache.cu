@@ -361,8 +361,13 @@ __global__ void __launch_bounds__(kAppThreads, 2) qcache_append_kernel(const App
         if (tid == 0) set_error(a.err, DSPARK_ERR_OOB);
         return;
     }
-    const int slot = a.slots[r0], nr = r1 - r0;
-    if (slot == -1) return;
+    const int nr = r1 - r0, slot = a.slots[r0], mine = a.slots[r0 + min(tid, nr - 1)];
+    if (slot == -1) {  // skipped, which has to hold for every row of the span
+        bool skip = true;
+        for (int i = tid; i < nr; i += kAppThreads) skip = skip && a.slots[r0 + i] == -1;
+        if (!__syncthreads_and(skip) && tid == 0) set_error(a.err, DSPARK_ERR_OOB);
+        return;
+    }
     const int page = slot / kQcPage, off = slot % kQcPage;
     if (slot < 0 || page >= a.n_pages || off + nr > kQcPage) {
         if (tid == 0) set_error(a.err, DSPARK_ERR_OOB);
@@ -380,7 +385,7 @@ __global__ void __launch_bounds__(kAppThreads, 2) qcache_append_kernel(const App
         }
     }
     const float old = off > 0 ? a.scales[layer][page] : 1.f;
-    __syncthreads();  // the barrier is set up
+    const bool run = __syncthreads_and(tid >= nr || mine == slot + tid);  // (and the barrier is set up)
     if (!mbar_wait_bounded(&s_bar, 0, &s_abort)) {
         if (tid == 0) {
             set_error(a.err, DSPARK_ERR_TIMEOUT);
@@ -389,6 +394,10 @@ __global__ void __launch_bounds__(kAppThreads, 2) qcache_append_kernel(const App
     }
     __syncthreads();
     if (s_abort) return;
+    if (!run) {  // the rows' slots do not follow one another
+        if (tid == 0) set_error(a.err, DSPARK_ERR_OOB);
+        return;
+    }
     const int n = nr * kPer;
     uint32_t mx = 0;
     bool bad = false;

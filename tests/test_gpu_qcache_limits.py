@@ -172,3 +172,31 @@ def test_plan_reports_a_bad_page_when_it_comes_back(M):
     assert g.run() == 18 and g.outs[0].item() == 2 and g.outs[3].cpu().tolist() == [-1] * 4
     h = Plan(M, [2], [0], g.t.cpu().numpy(), g.ring.cpu().numpy(), tuple(g.outs[1].tolist()), 4, 4)
     assert h.run() == 18 and h.outs[0].item() == 0
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_refuses_spans_that_are_not_one_run_of_slots(M, kv, rope, dtype):
+    # rows of a span whose slots do not follow one another: reported, and nothing of that page is written
+    D, rng = kv + rope, np.random.default_rng(25)
+    x = torch.from_numpy(rng.normal(0, 1, (1, 64, D))).to(dtype).cuda()
+
+    def go(slots, seg):
+        codes, scales = torch.zeros(4, 64, D, dtype=torch.uint8, device="cuda"), torch.ones(4, device="cuda")
+        cache = M.QCache(kv, rope, [codes], [scales], ints([[0, 1, 2, 3]]))
+        cache.append(x, ints(slots), ints(seg))
+        return cache.check(), codes.cpu().numpy(), scales.cpu().numpy()
+    whole = list(range(64, 128))
+    assert go(whole, [0, 64])[0] == 0
+    for at, value in ((1, -1), (63, -1), (63, 126), (5, 70), (40, 1 << 30), (2, 66 + 64), (1, 64), (7, -(1 << 31))):
+        slots = list(whole)
+        slots[at] = value
+        st, c, s = go(slots, [0, 64])
+        assert st == 18 and not c.any() and np.all(s == 1), (at, value)
+    st, c, s = go([-1, 65, 66], [0, 3])                      # a skipped first row takes no others with it unseen
+    assert st == 18 and not c.any()
+    st, c, s = go([-1, -1, -1, 130, 131, 9, 11], [0, 3, 5, 7])
+    assert st == 18 and not c[0].any() and not c[1].any() and c[2, 2:4].any(1).all()
+    assert np.all(s == 1)                                    # page 2 holds tokens under the larger scale of 1
+    st, c, s = go([-1, -1, 130, 131], [0, 2, 4])
+    assert st == 0 and c[2, 2:4].any(1).all()
