@@ -19,8 +19,8 @@ namespace ds {
 // place. A growing request is served if its inclusive sums fit, and then all
 // growing requests before it are served too, so the exclusive sums of a served
 // request are the same whether those not served are counted or not: one scan.
-// Sums saturate at 2^30 (saturating addition of non-negative numbers is
-// associative), which no capacity exceeds.
+// Sums saturate at 2^30 + 1 (saturating addition of non-negative numbers is
+// associative), which no capacity reaches.
 //
 // Bound: latency (a dependent chain of two loads, a block scan and the search
 // of a token's request in shared memory) until the slot maps are long, then
@@ -31,7 +31,7 @@ namespace ds {
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 constexpr int kPlanPer = kQcMaxBs / kPlanThreads;
-constexpr unsigned kPlanSat = 1u << 30;
+constexpr unsigned kPlanSat = (1u << 30) + 1;
 
 struct PlanParams {
     dspark_qplan_t p;

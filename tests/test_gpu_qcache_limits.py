@@ -200,3 +200,18 @@ def test_append_refuses_spans_that_are_not_one_run_of_slots(M, kv, rope, dtype):
     assert np.all(s == 1)                                    # page 2 holds tokens under the larger scale of 1
     st, c, s = go([-1, -1, 130, 131], [0, 2, 4])
     assert st == 0 and c[2, 2:4].any(1).all()
+
+
+def test_plan_fills_the_largest_slot_map_exactly(M):
+    # max_new at its limit, 2^30: one request takes all of it, the next must wait (its one token has no slot)
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("needs 16 GB of free device memory")
+    most, n_pages = 1 << 30, (1 << 24) + 8
+    e = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = M.QCache(512, 64, (), (), torch.zeros(2, 1 << 24, dtype=torch.int32, device="cuda"), n_pages=n_pages)
+    out, state, cu, slots, pos, seg = e(2), e(2), e(3), e(most), e(most), e((1 << 24) + 9)
+    cache.plan(ints([0, 0]), ints([most, 5]), torch.arange(n_pages, dtype=torch.int32, device="cuda"), ints([0, n_pages]),
+               out, state, cu, slots, pos, seg)
+    assert cache.check() == 0
+    assert out.tolist() == [most, 0] and state.tolist() == [1 << 24, 8] and cu.tolist() == [0, most, most]
+    assert slots[-1].item() == most - 1 and pos[-1].item() == most - 1 and seg[-8:].tolist() == [most] * 8
