@@ -67,6 +67,7 @@
 
 #include "e4m3.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "qattn.cuh"
 
 namespace ds {
@@ -840,12 +841,10 @@ template <int KV, int ROPE>
 static cudaError_t launch_width(const QaParams &p, int grid, cudaStream_t st) {
     using C = QtCfg<KV, ROPE>;
     constexpr int kSmem = qt_smem_bytes<KV, ROPE>();
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(qattn_tc_kernel<KV, ROPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e =
+        once([] { return cudaFuncSetAttribute(qattn_tc_kernel<KV, ROPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    if (e != cudaSuccess) return e;
     // the pool as 16-bit elements: boxes of 128 (the rope's: 64) bytes of 64 tokens
     CUtensorMap dims, rope;
     if (!encode_u16_map(&dims, p.codes, (uint64_t)p.n_pages * kQcPage, C::kD, 128, kQcPage)) return cudaErrorInvalidValue;

@@ -5,6 +5,7 @@
 
 #include "e4m3.cuh"
 #include "internal.h"
+#include "per_device.h"
 #include "qcache.h"
 
 using namespace ds;
@@ -456,12 +457,10 @@ __global__ void __launch_bounds__(kAppThreads, 2) qcache_append_kernel(const App
 template <typename T, int D>
 static cudaError_t launch_append_width(const AppendParams &a, int n_seg, int layers, cudaStream_t st) {
     constexpr int kSmem = kQcPage * D * (int)sizeof(T);
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(qcache_append_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static OncePerDevice once;
+    const cudaError_t e =
+        once([] { return cudaFuncSetAttribute(qcache_append_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem); });
+    if (e != cudaSuccess) return e;
     return launch_pdl(qcache_append_kernel<T, D>, dim3(n_seg, layers), dim3(kAppThreads), (size_t)kSmem, st, a);
 }
 
