@@ -271,17 +271,18 @@ class DSpark:
 _I32 = torch.int32
 
 
-def _int32(name: str, t: torch.Tensor, n: int):
-    """t holds at least n contiguous int32 values on the GPU."""
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name}: a contiguous int32 CUDA tensor of at least {n} elements")
+def _int32(name: str, t: torch.Tensor, n: int, dev: int):
+    """t holds at least n contiguous int32 values on GPU dev."""
+    if t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: a contiguous int32 tensor of at least {n} elements on cuda:{dev}")
 
 
 class QCache:
     """A paged latent cache in E4M3 with one power-of-two scale per page of 64 tokens.
 
     ``codes``: per layer uint8 (or float8_e4m3fn) [n_pages, 64, kv_lora + d_rope]; ``scales``: per layer fp32
-    [n_pages]; ``page_table`` int32 [bs, max_pages]. All belong to the caller and are written in place. The three
+    [n_pages]; ``page_table`` int32 [bs, max_pages]. All belong to the caller and are written in place; they and every
+    call's tensors lie on one GPU, the current one at each call (kernels read no other GPU's memory). The three
     calls are the page plan, the quantising append (every layer) and the attention over one layer; they run on the
     current stream and do not wait. ``check()`` reads the error word that their kernels set. Without ``n_heads`` the
     workspace serves the plan and the append alone; a zero-filled ``workspace`` (uint8) may be given instead, and
@@ -293,20 +294,22 @@ class QCache:
                  workspace: Optional[torch.Tensor] = None):
         if len(codes) != len(scales) or len(codes) > MAX_LAYERS:
             raise ValueError("one code pool and one scale vector per layer, at most %d layers" % MAX_LAYERS)
-        self.D, self.kv, self.layers = kv_lora + d_rope, kv_lora, len(codes)
+        self.D, self.kv, self.layers, self.dev = kv_lora + d_rope, kv_lora, len(codes), page_table.get_device()
+        if self.dev < 0:
+            raise ValueError("page_table: a CUDA tensor")
         if n_pages is None:
             if not len(codes):
                 raise ValueError("n_pages is needed without code pools")
             n_pages = int(codes[0].shape[0])
         for t, u in zip(codes, scales):
             if (t.dtype not in (torch.uint8, torch.float8_e4m3fn) or tuple(t.shape) != (n_pages, 64, self.D)
-                    or not t.is_contiguous() or not t.is_cuda):
-                raise ValueError(f"codes: contiguous uint8 or float8_e4m3fn CUDA tensors [{n_pages}, 64, {self.D}]")
-            if u.dtype != torch.float32 or u.numel() != n_pages or not u.is_contiguous() or not u.is_cuda:
-                raise ValueError(f"scales: contiguous fp32 CUDA tensors [{n_pages}]")
+                    or not t.is_contiguous() or t.get_device() != self.dev):
+                raise ValueError(f"codes: contiguous uint8 or float8_e4m3fn tensors [{n_pages}, 64, {self.D}] on cuda:{self.dev}")
+            if u.dtype != torch.float32 or u.numel() != n_pages or not u.is_contiguous() or u.get_device() != self.dev:
+                raise ValueError(f"scales: contiguous fp32 tensors [{n_pages}] on cuda:{self.dev}")
         if page_table.dim() != 2:
             raise ValueError("page_table: int32 [bs, max_pages]")
-        _int32("page_table", page_table, 1)
+        _int32("page_table", page_table, 1, self.dev)
         c = QCacheStruct(kv_lora=kv_lora, d_rope=d_rope, page_size=64, n_layers=len(codes), n_pages=n_pages,
                          page_table=page_table.data_ptr(), max_pages=int(page_table.shape[1]))
         for l, (t, u) in enumerate(zip(codes, scales)):
@@ -319,9 +322,15 @@ class QCache:
             raise DSparkError("dspark_qcache_workspace_bytes", 3)
         if workspace is None:
             workspace = torch.zeros(need, dtype=torch.uint8, device=page_table.device)
-        if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous uint8 CUDA tensor, zero-filled before its first use")
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != self.dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{self.dev}, zero-filled before its first use")
         self.ws, self.ws_ptr, self.ws_bytes = workspace, C.c_void_p(workspace.data_ptr()), workspace.numel()
+
+    def _device(self) -> int:
+        dev = torch._C._cuda_getDevice()
+        if dev != self.dev:
+            raise ValueError(f"the cache lies on cuda:{self.dev}, the current device is cuda:{dev}")
+        return dev
 
     def plan(self, length: torch.Tensor, want: torch.Tensor, ring: torch.Tensor, ring_state: torch.Tensor,
              length_out: torch.Tensor, ring_state_out: torch.Tensor, cu_new: torch.Tensor,
@@ -332,22 +341,22 @@ class QCache:
         [bs], ``ring_state_out`` [2], ``cu_new`` [bs + 1], ``slots`` and ``positions`` (one per new token, then -1;
         their size is the most new tokens served), ``seg_row`` (first new token of every touched page, then their
         number; its size less one is the most pages served)."""
-        bs, n, seg = length.numel(), self.n_pages, seg_row.numel()
+        dev, bs, n, seg = self._device(), length.numel(), self.n_pages, seg_row.numel()
         max_new = 0 if slots is None else slots.numel()
         if bs > self.rows:
             raise ValueError("more requests than rows of the page table")
-        _int32("length", length, bs)
-        _int32("want", want, bs)
-        _int32("ring", ring, n)
-        _int32("ring_state", ring_state, 2)
-        _int32("length_out", length_out, bs)
-        _int32("ring_state_out", ring_state_out, 2)
-        _int32("cu_new", cu_new, bs + 1)
-        _int32("seg_row", seg_row, 1)
+        _int32("length", length, bs, dev)
+        _int32("want", want, bs, dev)
+        _int32("ring", ring, n, dev)
+        _int32("ring_state", ring_state, 2, dev)
+        _int32("length_out", length_out, bs, dev)
+        _int32("ring_state_out", ring_state_out, 2, dev)
+        _int32("cu_new", cu_new, bs + 1, dev)
+        _int32("seg_row", seg_row, 1, dev)
         ps = pp = None
         if max_new:
-            _int32("slots", slots, 0)
-            _int32("positions", positions, max_new)
+            _int32("slots", slots, 0, dev)
+            _int32("positions", positions, max_new, dev)
             ps, pp = slots.data_ptr(), positions.data_ptr()
         a = QPlanArgs(length.data_ptr(), want.data_ptr(), ring.data_ptr(), ring_state.data_ptr(), length_out.data_ptr(),
                       ring_state_out.data_ptr(), cu_new.data_ptr(), ps, pp, seg_row.data_ptr())
@@ -358,17 +367,17 @@ class QCache:
     def append(self, entries: torch.Tensor, slots: torch.Tensor, seg_row: torch.Tensor):
         """Quantise entries [n_layers, rows, kv_lora + d_rope] (bf16 or fp32, any row and layer stride) into the slots
         of dspark_qcache_plan, raising the scales of pages that need it."""
-        shape = entries.shape
-        if len(shape) != 3 or shape[0] != self.layers or shape[2] != self.D or not entries.is_cuda:
-            raise ValueError(f"entries: CUDA tensor [{self.layers}, rows, {self.D}]")
+        dev, shape = self._device(), entries.shape
+        if len(shape) != 3 or shape[0] != self.layers or shape[2] != self.D or entries.get_device() != dev:
+            raise ValueError(f"entries: tensor [{self.layers}, rows, {self.D}] on cuda:{dev}")
         kind = 0 if entries.dtype is torch.bfloat16 else 1
         if kind and entries.dtype is not torch.float32:
             raise ValueError("entries: bf16 or fp32")
         layer_stride, row_stride, one = entries.stride()
         if one != 1:
             raise ValueError("entries: the elements of a row are contiguous")
-        _int32("slots", slots, 0)
-        _int32("seg_row", seg_row, 1)
+        _int32("slots", slots, 0, dev)
+        _int32("seg_row", seg_row, 1, dev)
         rows = min(shape[1], slots.numel())
         if shape[1] <= 1:
             row_stride = self.D  # torch leaves the stride of one row open
@@ -382,12 +391,12 @@ class QCache:
         """o = softmax(scale q k^T) v over one layer: q bf16 [total_q, n_heads, kv_lora + d_rope] (any token stride),
         request b's queries at cu_q[b] .. cu_q[b+1]-1, ``length`` cached tokens each; o bf16 [total_q, n_heads,
         kv_lora], lse fp32 [total_q, n_heads]."""
-        D, kv, shape = self.D, self.kv, q.shape
-        if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or not q.is_cuda:
-            raise ValueError(f"q: bf16 CUDA tensor [total_q, n_heads, {D}]")
+        dev, D, kv, shape = self._device(), self.D, self.kv, q.shape
+        if len(shape) != 3 or shape[2] != D or q.dtype is not torch.bfloat16 or q.get_device() != dev:
+            raise ValueError(f"q: bf16 tensor [total_q, n_heads, {D}] on cuda:{dev}")
         n, h, _ = shape
-        if o.shape != (n, h, kv) or o.dtype is not torch.bfloat16 or not o.is_cuda:
-            raise ValueError(f"o: bf16 CUDA tensor [{n}, {h}, {kv}]")
+        if o.shape != (n, h, kv) or o.dtype is not torch.bfloat16 or o.get_device() != dev:
+            raise ValueError(f"o: bf16 tensor [{n}, {h}, {kv}] on cuda:{dev}")
         qs, qh, q1 = q.stride()
         os, oh, o1 = o.stride()
         if n and (q1 != 1 or o1 != 1 or h > 1 and (qh != D or oh != kv)):
@@ -396,14 +405,14 @@ class QCache:
             qs, os = h * D, h * kv
         pl = None
         if lse is not None:
-            if lse.dtype is not torch.float32 or lse.numel() != n * h or not lse.is_contiguous() or not lse.is_cuda:
-                raise ValueError(f"lse: contiguous fp32 CUDA tensor [{n}, {h}]")
+            if lse.dtype is not torch.float32 or lse.numel() != n * h or not lse.is_contiguous() or lse.get_device() != dev:
+                raise ValueError(f"lse: contiguous fp32 tensor [{n}, {h}] on cuda:{dev}")
             pl = lse.data_ptr() or None
         bs = length.numel()
         if bs > self.rows:
             raise ValueError("more requests than rows of the page table")
-        _int32("length", length, 1)
-        _int32("cu_q", cu_q, bs + 1)
+        _int32("length", length, 1, dev)
+        _int32("cu_q", cu_q, bs + 1, dev)
         a = QAttnArgs(q.data_ptr() or None, qs, cu_q.data_ptr(), length.data_ptr(), h, n, 1 if causal else 0, scale,
                       o.data_ptr() or None, os, pl)
         st = lib().dspark_qcache_attend(self.ref, layer, C.byref(a), bs, self.ws_ptr, self.ws_bytes, _stream())
@@ -412,4 +421,5 @@ class QCache:
 
     def check(self) -> int:
         """Synchronise and return (and clear) the device error word."""
+        self._device()
         return lib().dspark_qcache_check(_p(self.ws), _stream())
