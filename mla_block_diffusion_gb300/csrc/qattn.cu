@@ -27,8 +27,7 @@ constexpr int kQaCombineThreads = 256;
 // The most that a sum can reach is then 2^(70 + 31 + 20), an element of O over 2^31 tokens.
 constexpr float kQaHeadroom = 20.f;
 
-// A task of the combine for warps that share it: a pair of rows and up to 128 columns of one split item. (The loop of
-// the kernel for one warp a task keeps its own: one kernel with both forms cost the other calls 1 to 3 us.)
+// A task of the combine: a pair of rows and up to 128 columns of one split item.
 template <int DV>
 struct QaTask {
     static constexpr int kCols = DV < 128 ? DV : 128, kSub = DV / kCols, kRows = 2;
@@ -134,7 +133,7 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
     __shared__ alignas(16) QaSplit s_list[kQaMaxGrid];
     __shared__ int s_first[kQaMaxGrid];
     __shared__ unsigned s_mask[kQaMaxGrid / 32];
-    constexpr int kCols = DV < 128 ? DV : 128, kSub = DV / kCols;
+    constexpr int kSub = QaTask<DV>::kSub;
     const int tid = threadIdx.x, lane = tid & 31;
     pdl_trigger();
     pdl_wait();
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
         n_split += __popc(mask);
     }
     __syncthreads();
-    constexpr int kRows = 2, kDeep = 16;  // rows of a task, partials in flight (of both rows, or of one when there are many)
+    constexpr int kRows = QaTask<DV>::kRows, kDeep = 16;  // partials in flight (of both rows, or of one when there are many)
     const int tasks = n_split * (kQaTile / kRows) * kSub, warps = gridDim.x * (kQaCombineThreads / 32);
     if constexpr (FEW) {
         int most = 0, share_log2 = 0;  // about a flight of partials a warp
@@ -175,86 +174,49 @@ __global__ void __launch_bounds__(kQaCombineThreads) qattn_combine_kernel(const 
             return;
         }
     }
-    const bool on = 4 * lane < kCols;
     for (int task = blockIdx.x * (kQaCombineThreads / 32) + (tid >> 5); task < tasks; task += warps) {
-        const int sub = task % kSub, row0 = task / kSub % (kQaTile / kRows) * kRows, li = task / kSub / (kQaTile / kRows);
-        const QaSplit sp = s_list[li];
-        const int left = sp.rows - row0;
+        const QaTask<DV> t(p, s_list, s_first, task, lane);
+        const int left = t.sp.rows - t.row0, n = t.n;
         if (left <= 0) continue;
-        const int c = s_first[li], n = sp.c_hi - c + 1;
-        auto slot = [&](int k) { return (size_t)(k == 0 ? sp.lo_slot : 2 * (c + k)); };
-        const float *src = p.part_o + (size_t)row0 * DV + sub * kCols + 4 * lane;
-        auto fetch = [&](int k, int i) {
-            return on && k < n ? __ldcg((const float4 *)(src + slot(k) * (kQaTile * DV) + i * DV)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        // reference and sum, lane = partial
-        auto stats = [&](int k0, int i) {
-            return k0 + lane < n ? __ldcg(&p.part_ml[slot(k0 + lane) * kQaTile + row0 + i]) : make_float2(-INFINITY, 0.f);
-        };
-        auto store = [&](int i, const float4 &o, float m, float l) {
-            const float sum = warp_sum(l);
-            const float inv = isnan(sum) ? sum : sum > 0.f ? 1.f / sum : 0.f;
-            const int r = sp.r0 + row0 + i, tq = (int)QaWork::token(p, r), hd = r - tq * p.H, tok = sp.q0 + tq;
-            if (on) {
-                const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-                uint2 u;
-                u.x = *(const uint32_t *)&lo;
-                u.y = *(const uint32_t *)&hi;
-                *(uint2 *)(p.o + (size_t)tok * p.o_stride + (size_t)hd * DV + sub * kCols + 4 * lane) = u;
-            }
-            if (p.lse && sub == 0 && lane == 0)
-                p.lse[(size_t)tok * p.H + hd] = isnan(sum) ? sum : sum > 0.f ? (m + log2f(sum)) * 0.6931471805599453f : -INFINITY;
-        };
-        auto reference = [&](float m) {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-            return m == -INFINITY ? 0.f : m - kQaHeadroom;
-        };
-        auto add = [&](float4 &o, float w, const float4 &v) {
-            o.x += w * v.x;
-            o.y += w * v.y;
-            o.z += w * v.z;
-            o.w += w * v.w;
-        };
         float4 v[kDeep];
         if (n <= kDeep / 2) {  // both rows at once, everything requested together
-            const float2 ml[kRows] = {stats(0, 0), stats(0, 1)};
+            const float2 ml[kRows] = {t.stats(0, 0), t.stats(0, 1)};
 #pragma unroll
-            for (int j = 0; j < kDeep; ++j) v[j] = fetch(j >> 1, j & 1);
+            for (int j = 0; j < kDeep; ++j) v[j] = t.fetch(j >> 1, j & 1);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                const float m = reference(ml[i].x), w = qa_ex2(ml[i].x - m);
+                const float m = t.reference(ml[i].x), w = qa_ex2(ml[i].x - m);
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int j = 0; j < kDeep / 2; ++j) add(o, __shfl_sync(~0u, w, j), v[2 * j + i]);
-                if (i < left) store(i, o, m, w * ml[i].y);
+                for (int j = 0; j < kDeep / 2; ++j) t.add(o, __shfl_sync(~0u, w, j), v[2 * j + i]);
+                if (i < left) t.store(i, o, m, w * ml[i].y);
             }
             continue;
         }
 #pragma unroll 1
         for (int i = 0; i < min(kRows, left); ++i) {
-            float2 ml = stats(0, i);
+            float2 ml = t.stats(0, i);
 #pragma unroll
-            for (int j = 0; j < kDeep; ++j) v[j] = fetch(j, i);
+            for (int j = 0; j < kDeep; ++j) v[j] = t.fetch(j, i);
             float m = ml.x;
-            for (int k0 = 32; k0 < n; k0 += 32) m = fmaxf(m, stats(k0, i).x);
-            m = reference(m);
+            for (int k0 = 32; k0 < n; k0 += 32) m = fmaxf(m, t.stats(k0, i).x);
+            m = t.reference(m);
             float w = qa_ex2(ml.x - m), l = w * ml.y;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k = 0; k < n; k += kDeep) {
                 if (k > 0) {
 #pragma unroll
-                    for (int j = 0; j < kDeep; ++j) v[j] = fetch(k + j, i);
+                    for (int j = 0; j < kDeep; ++j) v[j] = t.fetch(k + j, i);
                     if ((k & 31) == 0) {
-                        ml = stats(k, i);
+                        ml = t.stats(k, i);
                         w = qa_ex2(ml.x - m);
                         l += w * ml.y;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kDeep; ++j) add(o, __shfl_sync(~0u, w, (k + j) & 31), v[j]);
+                for (int j = 0; j < kDeep; ++j) t.add(o, __shfl_sync(~0u, w, (k + j) & 31), v[j]);
             }
-            store(i, o, m, l);
+            t.store(i, o, m, l);
         }
     }
 }

@@ -215,3 +215,148 @@ def test_plan_fills_the_largest_slot_map_exactly(M):
     assert cache.check() == 0
     assert out.tolist() == [most, 0] and state.tolist() == [1 << 24, 8] and cu.tolist() == [0, most, most]
     assert slots[-1].item() == most - 1 and pos[-1].item() == most - 1 and seg[-8:].tolist() == [most] * 8
+
+
+# --- forms that a server meets -------------------------------------------------------------------------------------
+def test_append_take_back_and_append_again(M):
+    # a draft-and-verify loop: tokens are drafted, some are taken back, others come in their place. A page's scale never
+    # falls while the page holds tokens, and its codes are those of the same steps on the host.
+    kv, rope, D, rng = 128, 32, 160, np.random.default_rng(26)
+    codes, scales = np.zeros((6, 64, D), dtype=np.uint8), np.ones(6, dtype=np.float32)
+    dev = [torch.from_numpy(codes).cuda(), torch.from_numpy(scales).cuda()]
+    table, ring = np.zeros((1, 3), dtype=np.int32), np.array([3, 1, 5, 0, 2, 4], dtype=np.int32)
+    cache = M.QCache(kv, rope, [dev[0]], [dev[1]], ints(table))
+    ring_d, length, state = ints(ring), ints([0]), ints([0, 6])
+    host_length, host_state = [0], (0, 6)
+    want = 0
+    kept = []                                                # the tokens as they came
+    for step in range(40):
+        new = int(rng.integers(1, 9))
+        fresh = [want + new, max(0, want + new - int(rng.integers(0, new + 1)))]   # drafted, then what is accepted
+        for w in fresh:
+            outs = [torch.empty(n, dtype=torch.int32, device="cuda") for n in (1, 2, 2, 8, 8, 4)]
+            cache.plan(length, ints([w]), ring_d, state, *outs)
+            got = Q.plan(host_length, [w], table, ring, host_state, 8, 3)
+            assert cache.check() == 0
+            for a, b in zip(outs, got):
+                assert a.cpu().tolist() == list(b)
+            if w > host_length[0]:
+                x = rng.normal(0, 1, (1, 8, D)) * 2.0 ** rng.integers(-6, 6)
+                x = torch.from_numpy(x).to(torch.bfloat16)
+                cache.append(x.cuda(), outs[3], outs[5])
+                assert cache.check() == 0
+                Q.append(codes, scales, x[0].double().numpy(), got[3], got[5])
+                kept = kept[:host_length[0]] + list(x[0, :w - host_length[0]].double().numpy())
+            length, state, host_length, host_state, want = outs[0], outs[1], [w], got[1], w
+            assert np.array_equal(dev[1].cpu().numpy(), scales)
+            assert np.array_equal(E4M3_TABLE[dev[0].cpu().numpy()], E4M3_TABLE[codes])
+    # what all raises together cost: one rounding, 2^-4 of an element, and less than 2^(e - 9) once it is below the
+    # normal range of its page (each raise to 2^e' rounds by at most half the smallest step, 2^(e' - 10), and e' differ)
+    for p in range(want):
+        pg = table[0, p // 64]
+        got, s = E4M3_TABLE[codes[pg, p % 64]] * scales[pg], float(scales[pg])
+        assert np.all(np.abs(got - kept[p]) <= 2.0 ** -4 * np.abs(kept[p]) + s * 2.0 ** -9)
+
+
+def test_whole_step_in_a_graph(M):
+    # plan, append and attention captured together, replayed while the wanted lengths change on the device
+    kv, rope, H, bs, most, D = 256, 32, 16, 3, 96, 288
+    rng = np.random.default_rng(27)
+    n_pages, width = 20, 8
+    codes, scales = torch.zeros(n_pages, 64, D, dtype=torch.uint8, device="cuda"), torch.ones(n_pages, device="cuda")
+    table = torch.zeros(bs, width, dtype=torch.int32, device="cuda")
+    cache = M.QCache(kv, rope, [codes], [scales], table, n_heads=H)
+    length, state, want, ring = ints([0] * bs), ints([3, n_pages]), ints([0] * bs), ints(rng.permutation(n_pages))
+    e = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    after, state_after, cu, slots, pos, seg = e(bs), e(2), e(bs + 1), e(most), e(most), e(10)
+    x = torch.zeros(1, most, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(most, H, D, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.zeros(most, H, kv, dtype=torch.bfloat16, device="cuda"), torch.zeros(most, H, device="cuda")
+    host = {"length": [0] * bs, "state": (3, n_pages), "table": np.zeros((bs, width), dtype=np.int32), "ring": ring.cpu().numpy(),
+            "codes": codes.cpu().numpy(), "scales": scales.cpu().numpy()}
+
+    def step():
+        cache.plan(length, want, ring, state, after, state_after, cu, slots, pos, seg)
+        cache.append(x, slots, seg)
+        cache.attend(0, q, cu, after, o, lse, causal=True, scale=0.07)
+        length.copy_(after)
+        state.copy_(state_after)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()                                               # nothing wanted: nothing changes
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for wanted in ([70, 0, 3], [71, 20, 4], [72, 21, 60], [60, 0, 70], [64, 33, 129], [128, 34, 130], [0, 200, 131], [1, 35, 0]):
+        want.copy_(ints(wanted))
+        x.copy_(torch.from_numpy(rng.normal(0, 1, (1, most, D)) * 2.0 ** rng.integers(-2, 3)))
+        q.copy_(torch.from_numpy(rng.normal(0, 1, (most, H, D))))
+        g.replay()
+        assert cache.check() == 0
+        before = host["length"]
+        out, host["state"], host_cu, host_slots, _, host_seg = Q.plan(before, wanted, host["table"], host["ring"], host["state"], most, 9)
+        host["length"] = out.tolist()
+        Q.append(host["codes"], host["scales"], x[0].double().cpu().numpy(), host_slots, host_seg)
+        assert length.tolist() == host["length"] and state.tolist() == list(host["state"]) and cu.tolist() == host_cu.tolist()
+        assert np.array_equal(codes.cpu().numpy(), host["codes"]) and np.array_equal(scales.cpu().numpy(), host["scales"])
+        total = int(host_cu[-1])
+        t = Laid(M, kv, host["codes"], host["scales"], host["table"], host["length"], np.diff(host_cu).tolist(),
+                 q[:total].double().cpu().numpy())
+        t.scale = 0.07
+        t.check(True, o[:total], lse[:total])
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+def test_attend_a_thousand_requests(M, kv, rope):
+    # several requests a thread where the work is divided
+    rng = np.random.default_rng(28)
+    t = Attend(M, kv, rope, 5, rng.integers(0, 200, 1000).tolist(), rng.integers(0, 3, 1000).tolist(), seed=28)
+    o, lse = t.run(True)
+    assert t.cache.check() == 0
+    t.check(True, o, lse)
+
+
+def test_attend_any_layer(M):
+    t = Attend(M, 128, 32, 8, [300, 90], [2, 1], seed=29)
+    empty = torch.full_like(t.dev[0], 0x7F)
+    cache = M.QCache(128, 32, [empty, empty, t.dev[0], empty], [t.dev[1] * 3, t.dev[1], t.dev[1], t.dev[1]], t.dev[2], n_heads=8)
+    o, lse = t.run(False)
+    t.cache = cache
+    o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+    cache.attend(2, t.q.cuda(), *t.args, o2, lse2, causal=False, scale=t.scale)
+    assert cache.check() == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    t.check(False, o2, lse2)
+
+
+def test_attend_more_chunks_than_32_bit_divisions_hold(M):
+    # 1024 requests of 524300 tokens, 4.2 million chunks; the pages repeat, so that 4096 tokens with multiplicities are the
+    # reference. Row sums add 4097 weights a thread and the output's accumulators four products of 32 tokens a chunk:
+    # at most 4 * 4097 roundings of 2^-23 in sequence.
+    kv, rope, D, H, bs, n = 64, 16, 80, 64, 1024, 524_300
+    rng = np.random.default_rng(30)
+    codes = np.stack([Q.e4m3_encode(rng.normal(0, 32, (64, D))) for _ in range(64)])
+    row = rng.integers(0, 64, -(-n // 64)).astype(np.int32)
+    q = torch.from_numpy(rng.normal(0, 1, (bs, H, D))).to(torch.bfloat16)
+    dev = [torch.from_numpy(codes).cuda(), torch.full((64,), 2.0 ** -5, device="cuda")]
+    cache = M.QCache(kv, rope, [dev[0]], [dev[1]], ints(row)[None].expand(bs, -1).contiguous(), n_heads=H)
+    o, lse = torch.zeros(bs, H, kv, dtype=torch.bfloat16, device="cuda"), torch.zeros(bs, H, device="cuda")
+    scale = 1.3 / np.sqrt(D)
+    cache.attend(0, q.cuda(), ints(np.arange(bs + 1)), ints([n] * bs), o, lse, causal=True, scale=scale)
+    assert cache.check() == 0
+    count = np.zeros((64, 64))
+    for j, pg in enumerate(row):
+        count[pg, :min(64, n - 64 * j)] += 1
+    k, count = E4M3_TABLE[codes].reshape(-1, D) * 2.0 ** -5, count.reshape(-1)
+    for b in (0, 1, 7, 150, 511, 512, 1000, 1022, 1023):
+        s = scale * q[b].double().numpy() @ k.T
+        top = scale * (np.abs(q[b].double().numpy()) @ np.abs(k).T).max(1)
+        m = s.max(1, keepdims=True)
+        w = np.exp(s - m) * count
+        want, absolute = w @ k[:, :kv] / w.sum(1)[:, None], w @ np.abs(k[:, :kv]) / w.sum(1)[:, None]
+        ds = 2.0 ** -16 * top + 2.0 ** -18 * np.abs(q[b].double().numpy()).max(1) * scale * np.abs(k).sum(1).max()
+        sums = 4 * 4097 * 2.0 ** -23
+        tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * ds[:, None] + 2 * sums) * absolute + 2.0 ** -17 * np.abs(k).max()
+        assert np.all(np.abs(o[b].double().cpu().numpy() - want) <= tol)
+        assert np.all(np.abs(lse[b].double().cpu().numpy() - (m[:, 0] + np.log(w.sum(1)))) <= ds + sums + 2.0 ** -20)
