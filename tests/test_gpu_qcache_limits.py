@@ -360,3 +360,30 @@ def test_attend_more_chunks_than_32_bit_divisions_hold(M):
         tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2 * ds[:, None] + 2 * sums) * absolute + 2.0 ** -17 * np.abs(k).max()
         assert np.all(np.abs(o[b].double().cpu().numpy() - want) <= tol)
         assert np.all(np.abs(lse[b].double().cpu().numpy() - (m[:, 0] + np.log(w.sum(1)))) <= ds + sums + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("bs,length,nq", [(1, 12000, 1), (5, 3000, 2), (200, 700, 1), (2, 5, 3), (20, 200, 30)])
+def test_attend_pages_of_all_scales(M, kv, rope, bs, length, nq):
+    # zero pages, pages whose tokens score far below and far above them, value scales 2^63 apart, in any order
+    D, H, rng = kv + rope, 3, np.random.default_rng(31 + bs)
+    kinds = [(-8, -1.75, 1.0), (-60, 0.0, 0.0), (-7, 0.0, 1.0), (3, 0.0, 1000.0), (-9, 0.75, 0.3), (-50, 0.0, 2.0 ** -45)]
+    codes = np.stack([page(rng, kv, D, e, last, size) for e, last, size in kinds])
+    rows = rng.integers(0, len(kinds), (bs, -(-length // 64)))
+    q = np.zeros((bs * nq, H, D))
+    q[:, :, -1] = rng.choice([0.0, 60.0, 800.0, -800.0, 5000.0], (bs * nq, H))
+    t = Laid(M, kv, codes, [2.0 ** e for e, _, _ in kinds], rows, [length] * bs, [nq] * bs, q)
+    o, lse = t.run(False)
+    assert t.cache.check() == 0
+    check_steered(t, o, lse)
+    o2, lse2 = t.run(False)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("kv,rope", LATENTS)
+@pytest.mark.parametrize("H", [333, 1024])
+def test_attend_many_heads(M, kv, rope, H):
+    t = Attend(M, kv, rope, H, [130, 0, 77], [2, 1, 1], seed=32)
+    o, lse = t.run(True)
+    assert t.cache.check() == 0
+    t.check(True, o, lse)
