@@ -338,14 +338,18 @@ enum { DSPARK_ENTRY_BF16 = 0, DSPARK_ENTRY_FP32 = 1 };
  * page's scale becomes the least power of two 2^e, -60 <= e <= 60, with
  * amax <= 448 * 2^e over its new rows, or its present scale if that is larger
  * and the page holds tokens before the first new one; the codes of those are
- * then moved to the new scale. Rounding is to nearest even, saturating.
+ * then moved to the new scale. Rounding is to nearest even, saturating. The scale
+ * stays while the page holds tokens, also when the one that raised it is taken
+ * back; all raises together cost an earlier element less than 2^(e - 9), e the
+ * last exponent, beside its own rounding.
  * The slots of such a run of rows follow one another, or all are -1: then it is
  * skipped. row_stride and layer_stride count elements
  * (multiples of 8 for bf16, 4 for fp32; layer_stride is unused for one layer).
  * Device errors: DSPARK_ERR_OOB for a slot or row outside its range or a run whose
- * slots do not follow one another (its rows are not written), DSPARK_ERR_BAD_INPUT for an element that
- * is not finite or above 448 * 2^60 (NaN is stored as 0, the others as +-448)
- * or a held page's scale that is no power of two in range. */
+ * slots do not follow one another (its rows are not written), DSPARK_ERR_BAD_INPUT
+ * for an element that is not finite or above 448 * 2^60 (NaN is stored as 0, the
+ * others as +-448) or a held page's scale that is no power of two in range (the
+ * new rows' scale replaces it). */
 dspark_status dspark_qcache_append(const dspark_qcache_t *c, const void *entries, int entry_type, int64_t row_stride,
                                    int64_t layer_stride, const int32_t *slots, int rows, const int32_t *seg_row,
                                    int n_seg, void *ws, size_t ws_bytes, void *stream);
@@ -373,10 +377,10 @@ typedef struct {
  * far as fp32 tells neighbouring scores apart; a row is NaN if the largest score of
  * 32 tokens that it sees (32i .. 32i + 31 of its request) lies beyond +-5.9 * 10^6.
  * q enters to the full bf16 (elements below 2^-13 of their row's largest keep an
- * absolute error of 2^-22 of it), the softmax weights with at least 8 significant
- * bits. Cached elements must be finite (the append writes no
- * other); entries past a request's length are never used. The workspace holds
- * split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of
+ * absolute error of 2^-22 of it; in rows whose largest is below 2^-93, one of 2^-114),
+ * the softmax weights with at least 8 significant bits. Cached elements must be
+ * finite (the append writes no other); entries past a request's length are never
+ * used. The workspace holds split partials. Device errors: DSPARK_ERR_OOB for cu_q or length out of
  * range (those requests' queries are skipped) or a page number out of range
  * (it is not read, and the outputs of rows that see its tokens are NaN),
  * DSPARK_ERR_BAD_INPUT for a non-finite query (its row's outputs are NaN), scores

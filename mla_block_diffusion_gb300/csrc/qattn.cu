@@ -226,7 +226,8 @@ static cudaError_t combine(const QaParams &p, int grid, int num_sms, cudaStream_
     // A bound on the items, and one on an item's pieces: with up to four items of more than sixteen pieces, warps share a
     // task (one token of 64 heads over 40000 tokens 45 -> 27 us, two requests 38 -> 30, four of 30000 tokens 38 either
     // way). The form without that is the faster one for everything else (32 requests 57 against 60 us, a block of 7 tokens
-    // over 4096 21.2 against 22).
+    // over 4096 21.2 against 22). The lengths are on the device: a short request under a table of more than 32 pages pays for
+    // the first form (one token over 100 tokens: 16.3 us, under a narrower table 14.1).
     const long long rows = (long long)p.total_q * p.H, items = (rows + (long long)min(p.bs, p.total_q) * (kQaTile - 1)) / kQaTile;
     const bool few = items <= 4 && p.max_pages > 2 * 16;
     return few ? launch_pdl(qattn_combine_kernel<DV, true>, dim3(2 * num_sms), dim3(kQaCombineThreads), 0, st, p, grid)

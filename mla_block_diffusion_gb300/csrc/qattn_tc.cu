@@ -47,16 +47,17 @@
 // itself: with half of the bytes loaded 6 % less, with 192 tensor clocks a chunk left
 // out 1 %. An item costs ~16000 clocks more (queries converted ~5000, output
 // ~6000, the pipeline drained and refilled). Two prompt chunks of 700 to 1024 tokens
-// x 64 heads over 4-8K tokens: 1290 us, 1.32 PFLOP/s of the formulas' products; a
+// x 64 heads over 4-8K tokens: 1308 us, 1.30 PFLOP/s of the formulas' products; a
 // block of 7 x 64 rows over 95000 tokens 86 us; 32 requests of 1-16K tokens, 64
 // rows each, 58 us, 3.2 TB/s.
 // Pairs of output products that share V (Phi's and Plo's of a tile) could take it
 // from the tensor core's collector, 39 clocks a product against 48; that needs
 // nothing issued between them, hence one issuing thread, and with one thread for
 // scores and outputs the prompt chunks take 1500 us. Bound, smaller widths: the
-// softmax, ~2500 clocks a chunk whatever the width (32 requests of 1K to 16K
-// tokens and 64 heads: 38, 35 and 34 us; products by mma.sync in f16, codes
-// widened on the way, took 130, 71 and 49).
+// latency of the softmax's chain on two warps a scheduler, ~2500 clocks a chunk
+// whatever the width (32 requests of 1K to 16K tokens and 64 heads: 39, 36 and 35
+// us; products by mma.sync in f16, codes widened on the way, took 130, 71 and 49; two
+// prompt chunks of 600 tokens over 4-8K 505, 471 and 462).
 //
 // Roles (12 warps): warp 0 TMA producer; warp 1 issues the scores (and owns tensor
 // memory), warp 2 the outputs, so that whichever of the two is ready keeps the

@@ -26,9 +26,9 @@ namespace ds {
 // Bound: latency (a dependent chain of two loads, a block scan and the search
 // of a token's request in shared memory) until the slot maps are long, then
 // their stores. Every CTA repeats the scan (up to 1024 requests, four a
-// thread) and fills its share of the outputs, so no CTA waits for another. Cold and
-// alone, one request 6 us, 500 requests of 1 to 8192 tokens 10.5, 64 prompts 8;
-// back to back the host call is longer (8 to 9 us).
+// thread) and fills its share of the outputs, so no CTA waits for another. In a graph
+// over eight plans in turn: one request 3.6 us, 32 4.6, 500 of 1 to 8192 tokens 7.9, 64
+// prompts 5.9 (with L2 flushed before: 5.1, 7.1, 10.5, 7.3); the host call takes 8 to 9.
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 constexpr int kPlanPer = kQcMaxBs / kPlanThreads;
@@ -259,7 +259,9 @@ __global__ void __launch_bounds__(kPlanThreads) qcache_plan_kernel(const PlanPar
 // in flight are bounded by shared memory (three bf16 pages of the full width an
 // SM), not by registers, and each element is read once. 24 prompts of 700 to 8192
 // tokens, bf16: 30 us, 5.4 TB/s of 6.8 (with the rows held in registers 38.6 us,
-// read twice 49 us).
+// read twice 49 us); the narrower widths 19, 12 and 11 us. fp32: 62 us at the full
+// width, 4.4 TB/s (a page is 147 KB, one an SM, whose load waits for the conversion of
+// the one before), 25, 17 and 12 at the others.
 // ---------------------------------------------------------------------------
 constexpr int kAppThreads = 384;
 
