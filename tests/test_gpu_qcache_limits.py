@@ -60,7 +60,7 @@ def test_attend_references_that_move_with_every_chunk(M, kv, rope, H):
     row = np.repeat(list(range(12)) * 2, 2)
     q = np.zeros((bs, H, D))
     q[:, :2, -1] = 14 * 70 * np.log(2) / (1.75 * 1.3 / np.sqrt(D))
-    t = Laid(M, kv, codes, [2.0 ** -8] * 12, [row] * bs, [3072] * bs, [1] * bs, q)
+    t = Laid(M, kv, codes, [2.0 ** -8] * 12, [row] * bs, [3067] * bs, [1] * bs, q)
     o, lse = t.run(False)
     assert t.cache.check() == 0
     check_steered(t, o, lse)
@@ -86,7 +86,7 @@ def test_attend_zero_pages_behind_low_scores(M, kv, rope, bs, chunks):
         row[-1] = 3
     q = np.zeros((bs, H, D))
     q[:, :, -1] = np.linspace(76.0, 76.9, bs * H).reshape(bs, H) / (1.75 * 1.3 / np.sqrt(D))
-    t = Laid(M, kv, codes, [2.0 ** -8, 2.0 ** -8, 2.0 ** -60, 2.0 ** -7], [row] * bs, [128 * chunks] * bs, [1] * bs, q)
+    t = Laid(M, kv, codes, [2.0 ** -8, 2.0 ** -8, 2.0 ** -60, 2.0 ** -7], [row] * bs, [128 * chunks - 5] * bs, [1] * bs, q)
     o, lse = t.run(False)
     assert t.cache.check() == 0 and torch.isfinite(lse).all()
     check_steered(t, o, lse)
@@ -101,7 +101,7 @@ def test_attend_pieces_at_both_ends_of_the_page_scales(M, kv, rope):
     row = [0, 1] + [2] * 22 + [1, 1] + [2] * 22
     q = np.zeros((bs, H, D))
     q[:, :, -1] = np.linspace(46.5, 46.9, bs * H).reshape(bs, H) / (1.75 * 1.3 / np.sqrt(D))
-    t = Laid(M, kv, codes, [2.0 ** 60, 2.0 ** -8, 2.0 ** -8], [row] * bs, [3072] * bs, [1] * bs, q)
+    t = Laid(M, kv, codes, [2.0 ** 60, 2.0 ** -8, 2.0 ** -8], [row] * bs, [3067] * bs, [1] * bs, q)
     o, lse = t.run(False)
     assert t.cache.check() == 0
     check_steered(t, o, lse)
