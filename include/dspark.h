@@ -396,6 +396,68 @@ size_t dspark_qcache_workspace_bytes(const dspark_qcache_t *c, int max_heads);
 /* Synchronise the stream, return and clear the error word. */
 dspark_status dspark_qcache_check(void *ws, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit layers: products of E4M3 rows and E4M3 weights with a scale for each
+ * block of 128, for the projections around the latent cache (a prompt's rows as
+ * well as a single token's).
+ *
+ * Quantised rows: element [m, k] stands for codes[m, k] * scales[k / 128, m].
+ * Weights: element [n, k] stands for codes[n, k] * scales[n / 128, k / 128]. Scales
+ * are any fp32 numbers; those that the quantisers write are powers of two. An
+ * E4M3 NaN makes every output that it enters NaN. n and k are multiples of 16 up
+ * to DSPARK_QLINEAR_MAX_DIM; the last block of an edge may be shorter than 128.
+ * No handle is needed. The products' workspace is an error word (16-byte
+ * aligned, zero-filled once, DSPARK_QLINEAR_WS_BYTES), read with
+ * dspark_qcache_check(); concurrent calls may share one. The calls read no other
+ * GPU's memory: everything lies on the current device.
+ */
+#define DSPARK_QLINEAR_MAX_DIM (1 << 20)
+#define DSPARK_QLINEAR_MAX_ROWS (1 << 24)
+#define DSPARK_QLINEAR_WS_BYTES 1024
+
+typedef struct {
+    int rows, k;            /* rows 0..DSPARK_QLINEAR_MAX_ROWS */
+    void *codes;            /* device, E4M3 [rows, k], 16-byte aligned */
+    float *scales;          /* device, fp32 [ceil(k / 128), rows], 4-byte aligned */
+    int64_t scale_stride;   /* elements from one block's scales to the next's, >= rows */
+} dspark_qrows_t;
+
+typedef struct {
+    int n, k;               /* outputs, inputs */
+    void *codes;            /* device, E4M3 [n, k], 16-byte aligned */
+    float *scales;          /* device, fp32 [ceil(n / 128), ceil(k / 128)], 4-byte aligned */
+} dspark_qweight_t;
+
+/* (10) Quantise rows: of every row's block of 128 elements (the last may be
+ * shorter) the scale is the least power of two 2^e, e >= -100, with amax <= 448 * 2^e
+ * over its finite elements (2^-100 if there are none but zeros), and the codes
+ * are x / 2^e rounded to nearest even. NaN and infinities become the NaN code.
+ * x [rows, k], x_type DSPARK_ENTRY_BF16 or _FP32; x_stride counts elements (a
+ * multiple of 8 for bf16, 4 for fp32). x and the codes may not overlap. */
+dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_stride, const dspark_qrows_t *out, void *stream);
+
+/* (11) The same for weights [n, k] over blocks of 128 x 128. */
+dspark_status dspark_qlinear_quantise_weight(const void *w, int w_type, int64_t w_stride, const dspark_qweight_t *out,
+                                             void *stream);
+
+/* (12) y = x w^T (+ add): for every block of 128 k the products of the codes are
+ * summed in fp32 and enter an fp32 sum times sx * sw (one fp32 product of the two
+ * scales, which has to be a normal number). y [rows, n], y_type DSPARK_ENTRY_BF16 or
+ * _FP32; add, fp32 [rows, n] or null, is added before the one rounding and may be
+ * y itself (fp32, the same stride); otherwise y overlaps no input. Strides count
+ * elements (y: a multiple of 8 for bf16, 4 for fp32; add: of 4). Results do not
+ * depend on timing. Device errors: DSPARK_ERR_TIMEOUT. */
+dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweight_t *w, const float *add, int64_t add_stride,
+                                    void *y, int y_type, int64_t y_stride, void *ws, size_t ws_bytes, void *stream);
+
+/* (13) The first half of a gated feed-forward block: h = silu(x gate^T) * (x up^T),
+ * silu(g) = g / (1 + exp(-g)), quantised as rows (call 10) straight from the fp32
+ * sums; the second half is dspark_qlinear_matmul. gate and up have one shape; h is
+ * [rows, n] and overlaps no input. Values that are not finite become NaN codes.
+ * Device errors: DSPARK_ERR_TIMEOUT. */
+dspark_status dspark_qlinear_gated(const dspark_qrows_t *x, const dspark_qweight_t *gate, const dspark_qweight_t *up,
+                                   const dspark_qrows_t *h, void *ws, size_t ws_bytes, void *stream);
+
 /* Synchronise the stream, return and clear the device error word
  * (DSPARK_OK if no kernel recorded an error since the last check). With
  * ws == NULL the word read is the one of dspark_fuse_ctx_noalloc's fixed

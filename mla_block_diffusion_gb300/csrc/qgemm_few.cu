@@ -1,0 +1,284 @@
+// Products of few quantised rows (up to 64) with block-scaled weights (include/dspark.h, calls 12 and 13).
+//
+// The same sums as in qgemm.cu with outputs on the accumulator's 128 lanes and the
+// rows (padded to NT = 16, 32 or 64) as its columns: the weights stream past the
+// rows once. A CTA takes 128 outputs (gated: of gate and of up) and a share of the
+// blocks of k; the CTAs of a cluster share a tile's blocks, add their partial sums
+// in rank order through distributed shared memory, and each finishes some of the
+// rows, so nothing goes through global memory and a result does not depend on
+// timing. Bound: HBM (one byte a weight). The cluster is the largest of up to 8
+// CTAs that leaves all tiles in one wave of two CTAs an SM.
+#include <math.h>
+
+#include "per_device.h"
+#include "qlinear.h"
+
+namespace ds {
+
+constexpr int kQfWindow = 32;     // blocks of k whose factors lie in shared memory at a time
+constexpr int kQfMaxSplit = 8;
+
+template <int NT, bool GATED>
+struct QfCfg {
+    static constexpr int kMats = GATED ? 2 : 1;
+    static constexpr int kX = kMats * 128 * 128;                        // weights, then rows
+    static constexpr int kStage = kX + NT * 128;
+    static constexpr int kFactors = kMats * kQfWindow * NT * 4;
+    static constexpr int kStages = (112 * 1024 - 2048 - kFactors) / kStage;
+    static constexpr int kSlots = 256 / (kMats * NT) < 4 ? 256 / (kMats * NT) : 4;
+    static constexpr int kCols = kSlots * kMats * NT;
+    static constexpr int kThreads = 64 + 128 * kMats;
+    static constexpr int kPartial = kMats * NT * 128 * 4;
+    static_assert(kStages >= 2 && kPartial <= kStages * kStage, "shared memory");
+    static_assert(kCols >= 32 && (kCols & (kCols - 1)) == 0, "tensor memory");
+    struct Bars {
+        uint64_t full[kStages], empty[kStages], afull[kSlots], aempty[kSlots], done;
+        uint32_t tmem, issued;
+        volatile int abort;
+    };
+    static constexpr int kSmem = kStages * kStage + kFactors + (int)sizeof(Bars);
+    static_assert(kSmem <= 112 * 1024, "two CTAs an SM");
+};
+
+// 16 bytes of the same place in the shared memory of CTA `rank` of the cluster.
+DS_DEVINL float4 ld_peer_f4(const float *local, uint32_t rank) {
+    uint32_t a;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
+    qgemm_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
+                     const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int split) {
+    using C = QfCfg<NT, GATED>;
+    using Bars = typename C::Bars;
+    extern __shared__ __align__(1024) uint8_t qf_smem[];
+    float *sF = (float *)(qf_smem + C::kStages * C::kStage);
+    Bars &ms = *(Bars *)((uint8_t *)sF + C::kFactors);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *abort = &ms.abort;
+    const int rank = blockIdx.x % split, n0 = blockIdx.x / split * 128;
+    const int k0 = (int)((long long)rank * p.KB / split), k1 = (int)((long long)(rank + 1) * p.KB / split);
+    if (tid == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(&ms.full[s], 1);
+            mbar_init(&ms.empty[s], 1);
+        }
+        for (int s = 0; s < C::kSlots; ++s) {
+            mbar_init(&ms.afull[s], 1);
+            mbar_init(&ms.aempty[s], 4 * C::kMats);
+        }
+        mbar_init(&ms.done, 1);
+        ms.abort = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tm_x);
+        tma_prefetch_desc(&tm_w0);
+        if (GATED) tma_prefetch_desc(&tm_w1);
+    }
+    __syncthreads();
+    // Tensor memory is taken once the kernels before have ended, and the kernel behind is let in once it is taken: of
+    // two that share an SM, neither holds what the other waits for. The producer needs none and goes ahead.
+    pdl_wait();
+    if (warp == 1) {
+        tmem_alloc(&ms.tmem, C::kCols);
+        pdl_trigger();
+    }
+    uint32_t tmem = 0;
+    if (warp != 0) {
+        tc_fence_before();
+        named_bar_sync(7, C::kThreads - 32);
+        tc_fence_after();
+        tmem = ms.tmem;
+    }
+
+    if (warp == 0) {
+        if (ql_elect()) {
+            uint32_t u = 0;
+            for (int kb = k0; kb < k1; ++kb, ++u) {
+                const uint32_t s = u % C::kStages;
+                if (u >= C::kStages && !mbar_wait_bounded(&ms.empty[s], ((u / C::kStages) & 1) ^ 1, abort)) break;
+                uint8_t *to = qf_smem + s * C::kStage;
+                mbar_arrive_expect_tx(&ms.full[s], C::kStage);
+                // 16-bit elements: 64 a box row
+                tma_load_2d(to, &tm_w0, kb * 64, n0, &ms.full[s]);
+                if (GATED) tma_load_2d(to + 128 * 128, &tm_w1, kb * 64, n0, &ms.full[s]);
+                tma_load_2d(to + C::kX, &tm_x, kb * 64, 0, &ms.full[s]);
+            }
+            ms.issued = u;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (ql_elect()) {
+            const uint32_t lo = sdesc_lo(smem_u32(qf_smem));
+            constexpr uint32_t hi = sdesc_hi(1024, 2), id = idesc_e4m3_f32(128, NT);
+            const uint32_t n = k1 - k0;
+            for (uint32_t u = 0; u < n; ++u) {
+                const uint32_t s = u % C::kStages, a = u % C::kSlots;
+                if (!mbar_wait_bounded(&ms.full[s], (u / C::kStages) & 1, abort)) break;
+                if (u >= C::kSlots && !mbar_wait_bounded(&ms.aempty[a], ((u / C::kSlots) & 1) ^ 1, abort)) break;
+                tc_fence_after();
+                const uint32_t w = lo + s * (C::kStage >> 4), x = w + (C::kX >> 4);
+#pragma unroll
+                for (int i = 0; i < C::kMats; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_e4m3(tmem + (a * C::kMats + i) * NT, (uint64_t)hi << 32 | (w + i * 1024 + 2 * k), (uint64_t)hi << 32 | (x + 2 * k),
+                                 id, k > 0);
+                mma_commit(&ms.empty[s]);
+                mma_commit(&ms.afull[a]);
+            }
+            mma_commit(&ms.done);
+            mbar_drain(&ms.done, 0);
+        }
+        __syncwarp();
+    } else {
+        const int mat = (warp - 2) >> 2, q = warp & 3, me = tid - 64 - 128 * mat;
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + mat * NT;
+        float *fac = sF + mat * kQfWindow * NT;
+        const float *sw = (mat ? p.sw[1] : p.sw[0]) + (size_t)(n0 / kQlBlock) * p.KB;
+        unsigned long long acc[NT / 2];
+#pragma unroll
+        for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
+        const uint32_t n = k1 - k0;
+        for (uint32_t u = 0; u < n; ++u) {
+            const uint32_t w = u % kQfWindow, a = u % C::kSlots;
+            if (w == 0) {
+                named_bar_sync(1 + mat, 128);  // the window before has been used
+                const int blocks = min(kQfWindow, (int)(n - u));
+                for (int i = me; i < blocks * NT; i += 128) {
+                    const int b = k0 + (int)u + i / NT, m = i % NT;
+                    fac[i] = m < p.M ? __ldg(p.sx + (size_t)b * p.sx_stride + m) * __ldg(sw + b) : 0.f;
+                }
+                named_bar_sync(1 + mat, 128);
+            }
+            // every warp keeps to the barriers above, whatever a wait says
+            if (!ql_warp_wait(&ms.afull[a], (u / C::kSlots) & 1, abort)) continue;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                uint32_t v[16];
+                tmem_ld16_issue(tl + a * (C::kMats * NT) + 16 * c, v);
+                tmem_ld_wait_tied(v);
+                const ulonglong2 *f = (const ulonglong2 *)(fac + w * NT + 16 * c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const ulonglong2 g = f[i];
+                    fma2(acc[8 * c + 2 * i], v[4 * i], v[4 * i + 1], g.x);
+                    fma2(acc[8 * c + 2 * i + 1], v[4 * i + 2], v[4 * i + 3], g.y);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.aempty[a]);
+        }
+        // partial sums [matrix, row, output] in the stages' place: every product is done
+        float *part = (float *)qf_smem + mat * NT * 128 + 32 * q + lane;
+        if (!*abort) {
+#pragma unroll
+            for (int i = 0; i < NT / 2; ++i) {
+                const float2 v = unpack2(acc[i]);
+                part[2 * i * 128] = v.x;
+                part[(2 * i + 1) * 128] = v.y;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    // row m is finished by CTA m % split: a warp a row, four outputs a lane
+    for (int m = rank + split * warp; m < p.M; m += split * (C::kThreads / 32)) {
+        float4 v[C::kMats];
+#pragma unroll
+        for (int i = 0; i < C::kMats; ++i) {
+            const float *at = (const float *)qf_smem + (i * NT + m) * 128 + 4 * lane;
+            float4 s[kQfMaxSplit];
+#pragma unroll
+            for (int r = 0; r < kQfMaxSplit; ++r)
+                if (r < split) s[r] = ld_peer_f4(at, r);
+            v[i] = s[0];
+#pragma unroll
+            for (int r = 1; r < kQfMaxSplit; ++r)
+                if (r < split) {
+                    v[i].x += s[r].x;
+                    v[i].y += s[r].y;
+                    v[i].z += s[r].z;
+                    v[i].w += s[r].w;
+                }
+        }
+        const int n = n0 + 4 * lane;
+        if constexpr (GATED) {
+            float h[4] = {ql_gate(v[0].x, v[1].x), ql_gate(v[0].y, v[1].y), ql_gate(v[0].z, v[1].z), ql_gate(v[0].w, v[1].w)};
+            uint32_t mx = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a = __float_as_uint(h[i]) & 0x7fffffffu;
+                if (a < 0x7f800000u) mx = max(mx, a);
+                else h[i] = __uint_as_float(0x7fffffffu);
+            }
+            const int e = ql_exponent(__reduce_max_sync(~0u, mx));
+            const float inv = qc_pow2(-e);
+            if (n < p.N)
+                *(uint32_t *)(p.h + (size_t)m * p.N + n) = ql_e4m3x2(h[0] * inv, h[1] * inv) | ql_e4m3x2(h[2] * inv, h[3] * inv) << 16;
+            if (lane == 0) p.sh[(size_t)(n0 / kQlBlock) * p.sh_stride + m] = qc_pow2(e);
+        } else if (n < p.N) {
+            if (p.add) {
+                const float4 a = *(const float4 *)(p.add + (size_t)m * p.add_stride + n);
+                v[0].x += a.x;
+                v[0].y += a.y;
+                v[0].z += a.z;
+                v[0].w += a.w;
+            }
+            if (p.y_fp32) {
+                *(float4 *)((float *)p.y + (size_t)m * p.y_stride + n) = v[0];
+            } else {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(v[0].x, v[0].y), b = __floats2bfloat162_rn(v[0].z, v[0].w);
+                *(uint2 *)((__nv_bfloat16 *)p.y + (size_t)m * p.y_stride + n) = make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // no CTA leaves while another reads its sums
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kCols);
+    }
+    if (tid == 0 && ms.abort) {  // no copy outlives the CTA
+        for (uint32_t u = ms.issued > C::kStages ? ms.issued - C::kStages : 0; u < ms.issued; ++u)
+            mbar_drain(&ms.full[u % C::kStages], (u / C::kStages) & 1);
+        set_error(p.err, DSPARK_ERR_TIMEOUT);
+    }
+}
+
+template <int NT, bool GATED>
+static cudaError_t launch(const QlParams &p, const void *x_codes, const CUtensorMap &w0, const CUtensorMap &w1, int num_sms,
+                          cudaStream_t st, uint64_t k) {
+    using C = QfCfg<NT, GATED>;
+    static OncePerDevice once;
+    const cudaError_t e = once(
+        [] { return cudaFuncSetAttribute(qgemm_few_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
+    if (e != cudaSuccess) return e;
+    CUtensorMap x;
+    if (!encode_u16_map(&x, x_codes, p.M, k, 128, NT)) return cudaErrorInvalidValue;
+    const int tiles = (p.N + 127) / 128;
+    int split = 1;
+    while (split < kQfMaxSplit && split < p.KB && tiles * (split + 1) <= 2 * num_sms) ++split;
+    return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3(tiles * split), dim3(C::kThreads), (size_t)C::kSmem, st, split, x, w0, w1,
+                              p, split);
+}
+template <bool GATED>
+static cudaError_t pick(const QlParams &p, const void *x_codes, const CUtensorMap &w0, const CUtensorMap &w1, int num_sms,
+                        cudaStream_t st, uint64_t k) {
+    if (p.M <= 16) return launch<16, GATED>(p, x_codes, w0, w1, num_sms, st, k);
+    if (p.M <= 32) return launch<32, GATED>(p, x_codes, w0, w1, num_sms, st, k);
+    return launch<64, GATED>(p, x_codes, w0, w1, num_sms, st, k);
+}
+
+cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const CUtensorMap &w0, const CUtensorMap &w1,
+                             int num_sms, cudaStream_t st) {
+    return gated ? pick<true>(p, x.codes, w0, w1, num_sms, st, x.k) : pick<false>(p, x.codes, w0, w1, num_sms, st, x.k);
+}
+
+}  // namespace ds

@@ -1,0 +1,332 @@
+// 8-bit layers with a scale for each block of 128: host entry points and the
+// quantisers (include/dspark.h, calls 10 to 13).
+#include <math.h>
+#include <string.h>
+
+#include "qlinear.h"
+
+using namespace ds;
+
+namespace ds {
+
+// ---------------------------------------------------------------------------
+// Quantising rows: 16 lanes hold a block of 128 elements, eight each.
+//
+// e = the least exponent >= -100 with amax <= 448 * 2^e; codes are RN(x 2^-e),
+// one rounding since 2^-e is a power of two. Bound: HBM (2 or 4 bytes read and
+// one written per element). A CTA takes 8 rows x 2 PER blocks, each half-warp PER
+// blocks that it requests together; the scales of 8 rows are one full sector of
+// their [block, row] matrix.
+// ---------------------------------------------------------------------------
+constexpr int kQrThreads = 256, kQrRows = 8;
+
+template <typename T>
+struct Eight {
+    uint4 v[sizeof(T) / 2];
+    DS_DEVINL void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldg((const uint4 *)p + i);
+    }
+    DS_DEVINL void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+    }
+    DS_DEVINL void floats(float (&f)[8]) const {
+        const uint32_t *w = (const uint32_t *)v;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            f[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+};
+// Largest magnitude (bits) of the finite ones among eight; *bad: there is another.
+DS_DEVINL uint32_t amax8(const float (&f)[8], bool *bad) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+    if (m >= 0x7f800000u) {
+        *bad = true;
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+            if (u < 0x7f800000u) m = max(m, u);
+        }
+    }
+    return m;
+}
+DS_DEVINL uint2 codes8(const float (&f)[8], float inv, bool bad) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = f[2 * i], b = f[2 * i + 1];
+        if (bad) {
+            a = ql_inf_to_nan(a);
+            b = ql_inf_to_nan(b);
+        }
+        c[i] = ql_e4m3x2(a * inv, b * inv);
+    }
+    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+template <typename T, int PER>
+__global__ void __launch_bounds__(kQrThreads) quantise_rows_kernel(const T *__restrict__ x, long long x_stride, int M, int K,
+                                                                   uint8_t *__restrict__ codes, float *__restrict__ scales,
+                                                                   long long s_stride) {
+    const int tid = threadIdx.x, lane16 = tid & 15, half = tid >> 4;
+    const int across = ((K + kQlBlock - 1) / kQlBlock + 2 * PER - 1) / (2 * PER);  // CTAs side by side
+    const int row0 = (blockIdx.x / across) * kQrRows, first = (blockIdx.x % across) * (2 * PER);
+    const int r = row0 + (half & 7), b0 = first + (half >> 3);
+    __shared__ float s_scale[2 * PER][kQrRows];
+    pdl_trigger();
+    pdl_wait();
+    Eight<T> v[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int k = (b0 + 2 * i) * kQlBlock + 8 * lane16;
+        if (r < M && k < K) v[i].load(x + (long long)r * x_stride + k);
+        else v[i].zero();
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int k = (b0 + 2 * i) * kQlBlock + 8 * lane16;
+        float f[8];
+        v[i].floats(f);
+        bool bad = false;
+        uint32_t m = amax8(f, &bad);
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
+        const int e = ql_exponent(m);
+        if (r < M && k < K) *(uint2 *)(codes + (long long)r * K + k) = codes8(f, qc_pow2(-e), bad);
+        if (lane16 == 0) s_scale[(half >> 3) + 2 * i][half & 7] = qc_pow2(e);
+    }
+    __syncthreads();
+    if (tid < 2 * PER * kQrRows) {
+        const int b = first + tid / kQrRows, rr = row0 + tid % kQrRows;
+        if (rr < M && b * kQlBlock < K) scales[(long long)b * s_stride + rr] = s_scale[tid / kQrRows][tid % kQrRows];
+    }
+}
+
+// The same over blocks of 128 x 128, one CTA each; the block waits in registers for its maximum.
+template <typename T>
+__global__ void __launch_bounds__(kQrThreads) quantise_weight_kernel(const T *__restrict__ w, long long stride, int N, int K,
+                                                                     uint8_t *__restrict__ codes, float *__restrict__ scales) {
+    constexpr int kPer = kQlBlock / (kQrThreads / 16);  // rows of a half-warp
+    __shared__ uint32_t s_max;
+    const int tid = threadIdx.x, r0 = blockIdx.y * kQlBlock + (tid >> 4), k = blockIdx.x * kQlBlock + 8 * (tid & 15);
+    pdl_trigger();
+    if (tid == 0) s_max = 0;
+    pdl_wait();
+    __syncthreads();
+    Eight<T> v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int r = r0 + 16 * i;
+        if (r < N && k < K) v[i].load(w + (long long)r * stride + k);
+        else v[i].zero();
+    }
+    uint32_t m = 0;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        float f[8];
+        v[i].floats(f);
+        m = max(m, amax8(f, &bad));
+    }
+    m = __reduce_max_sync(~0u, m);
+    if ((tid & 31) == 0) atomicMax(&s_max, m);
+    __syncthreads();
+    const int e = ql_exponent(s_max);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int r = r0 + 16 * i;
+        float f[8];
+        v[i].floats(f);
+        if (r < N && k < K) *(uint2 *)(codes + (long long)r * K + k) = codes8(f, qc_pow2(-e), bad);
+    }
+    if (tid == 0) scales[(long long)blockIdx.y * gridDim.x + blockIdx.x] = qc_pow2(e);
+}
+
+template <typename T>
+static cudaError_t launch_rows(const void *x, long long stride, const dspark_qrows_t &o, int sms, cudaStream_t st) {
+    const int kb = (o.k + kQlBlock - 1) / kQlBlock, rb = (o.rows + kQrRows - 1) / kQrRows;
+    // four blocks a half-warp where that still leaves every SM a few CTAs, else one: more SMs share a short call
+    if ((long long)rb * kb >= 64ll * sms)
+        return launch_pdl(quantise_rows_kernel<T, 4>, dim3((kb + 7) / 8 * rb), dim3(kQrThreads), 0, st, (const T *)x, stride,
+                          o.rows, o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
+    return launch_pdl(quantise_rows_kernel<T, 1>, dim3((kb + 1) / 2 * rb), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
+                      o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
+}
+template <typename T>
+static cudaError_t launch_weight(const void *w, long long stride, const dspark_qweight_t &o, cudaStream_t st) {
+    const int kb = (o.k + kQlBlock - 1) / kQlBlock, nb = (o.n + kQlBlock - 1) / kQlBlock;
+    return launch_pdl(quantise_weight_kernel<T>, dim3(kb, nb), dim3(kQrThreads), 0, st, (const T *)w, stride, o.n, o.k,
+                      (uint8_t *)o.codes, o.scales);
+}
+
+}  // namespace ds
+
+namespace {
+
+bool ok16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+bool ok4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+bool ok_dim(int d) { return d >= 16 && d <= DSPARK_QLINEAR_MAX_DIM && d % 16 == 0; }
+
+int current_sms() {
+    static int sms[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms[dev];
+}
+
+dspark_status done(cudaError_t e) {
+    if (e == cudaSuccess) return DSPARK_OK;
+    (void)cudaGetLastError();
+    return DSPARK_ERR_CUDA;
+}
+
+dspark_status check_rows(const dspark_qrows_t *x) {
+    if (!x) return DSPARK_ERR_NULL;
+    if (x->rows < 0 || x->rows > DSPARK_QLINEAR_MAX_ROWS || !ok_dim(x->k) || x->scale_stride < x->rows) return DSPARK_ERR_SHAPE;
+    if (x->rows == 0) return DSPARK_OK;
+    if (!x->codes || !x->scales) return DSPARK_ERR_NULL;
+    return ok16(x->codes) && ok4(x->scales) ? DSPARK_OK : DSPARK_ERR_ALIGN;
+}
+dspark_status check_weight(const dspark_qweight_t *w) {
+    if (!w) return DSPARK_ERR_NULL;
+    if (!ok_dim(w->n) || !ok_dim(w->k)) return DSPARK_ERR_SHAPE;
+    if (!w->codes || !w->scales) return DSPARK_ERR_NULL;
+    return ok16(w->codes) && ok4(w->scales) ? DSPARK_OK : DSPARK_ERR_ALIGN;
+}
+dspark_status check_source(const void *x, int type, int64_t stride, int k) {
+    if (type != DSPARK_ENTRY_BF16 && type != DSPARK_ENTRY_FP32) return DSPARK_ERR_UNSUPPORTED;
+    if (stride < k) return DSPARK_ERR_SHAPE;
+    if (!x) return DSPARK_ERR_NULL;
+    return ok16(x) && stride % (type == DSPARK_ENTRY_BF16 ? 8 : 4) == 0 ? DSPARK_OK : DSPARK_ERR_ALIGN;
+}
+
+// Do [a, a + an) and [b, b + bn) share a byte?
+bool overlap(const void *a, unsigned long long an, const void *b, unsigned long long bn) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + bn && y < x + an;
+}
+
+unsigned long long source_bytes(int type, int64_t stride, int rows, int k) {
+    return ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4);
+}
+
+// Few rows: the weights stream past them, outputs on the tensor core's 128 lanes;
+// many: rows on the lanes.
+dspark_status product(const QlParams &p, bool gated, const dspark_qrows_t *x, const dspark_qweight_t *w0,
+                      const dspark_qweight_t *w1, cudaStream_t st) {
+    const int sms = current_sms();
+    if (sms < 1) return DSPARK_ERR_CUDA;
+    CUtensorMap mw0, mw1;
+    if (!encode_u16_map(&mw0, w0->codes, w0->n, w0->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
+    mw1 = mw0;
+    if (gated && !encode_u16_map(&mw1, w1->codes, w1->n, w1->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
+    if (p.M <= 64) return done(launch_qgemm_few(p, gated, *x, mw0, mw1, sms, st));
+    CUtensorMap mx;
+    if (!encode_u16_map(&mx, x->codes, x->rows, x->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
+    return done(launch_qgemm(p, gated, mx, mw0, mw1, sms, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_stride, const dspark_qrows_t *out, void *stream) {
+    dspark_status s = check_rows(out);
+    if (s != DSPARK_OK || out->rows == 0) return s;
+    s = check_source(x, x_type, x_stride, out->k);
+    if (s != DSPARK_OK) return s;
+    if (overlap(out->codes, (unsigned long long)out->rows * out->k, x, source_bytes(x_type, x_stride, out->rows, out->k)))
+        return DSPARK_ERR_SHAPE;
+    const int sms = current_sms();
+    if (sms < 1) return DSPARK_ERR_CUDA;
+    return done(x_type == DSPARK_ENTRY_BF16 ? launch_rows<__nv_bfloat16>(x, x_stride, *out, sms, (cudaStream_t)stream)
+                                            : launch_rows<float>(x, x_stride, *out, sms, (cudaStream_t)stream));
+}
+
+dspark_status dspark_qlinear_quantise_weight(const void *w, int w_type, int64_t w_stride, const dspark_qweight_t *out,
+                                             void *stream) {
+    dspark_status s = check_weight(out);
+    if (s != DSPARK_OK) return s;
+    s = check_source(w, w_type, w_stride, out->k);
+    if (s != DSPARK_OK) return s;
+    if (overlap(out->codes, (unsigned long long)out->n * out->k, w, source_bytes(w_type, w_stride, out->n, out->k)))
+        return DSPARK_ERR_SHAPE;
+    return done(w_type == DSPARK_ENTRY_BF16 ? launch_weight<__nv_bfloat16>(w, w_stride, *out, (cudaStream_t)stream)
+                                            : launch_weight<float>(w, w_stride, *out, (cudaStream_t)stream));
+}
+
+dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweight_t *w, const float *add, int64_t add_stride,
+                                    void *y, int y_type, int64_t y_stride, void *ws, size_t ws_bytes, void *stream) {
+    dspark_status s = check_rows(x);
+    if (s == DSPARK_OK) s = check_weight(w);
+    if (s != DSPARK_OK) return s;
+    if (y_type != DSPARK_ENTRY_BF16 && y_type != DSPARK_ENTRY_FP32) return DSPARK_ERR_UNSUPPORTED;
+    if (x->k != w->k || y_stride < w->n || (add && add_stride < w->n)) return DSPARK_ERR_SHAPE;
+    if (!ws || ws_bytes < DSPARK_QLINEAR_WS_BYTES) return DSPARK_ERR_WORKSPACE;
+    if (!ok16(ws)) return DSPARK_ERR_ALIGN;
+    if (x->rows == 0) return DSPARK_OK;
+    if (!y) return DSPARK_ERR_NULL;
+    if (!ok16(y) || !ok16(add) || y_stride % (y_type == DSPARK_ENTRY_BF16 ? 8 : 4) || (add && add_stride % 4)) return DSPARK_ERR_ALIGN;
+    const unsigned long long rows = (unsigned long long)x->rows;
+    const unsigned long long y_bytes = ((rows - 1) * (unsigned long long)y_stride + w->n) * (y_type == DSPARK_ENTRY_BF16 ? 2 : 4);
+    if (overlap(y, y_bytes, x->codes, rows * x->k)) return DSPARK_ERR_SHAPE;
+    // the residual may be y itself, element for element, and nothing else that overlaps it
+    if (add && !((const void *)add == y && y_type == DSPARK_ENTRY_FP32 && add_stride == y_stride) &&
+        overlap(y, y_bytes, add, ((rows - 1) * (unsigned long long)add_stride + w->n) * 4))
+        return DSPARK_ERR_SHAPE;
+    QlParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = x->rows;
+    p.N = w->n;
+    p.KB = (x->k + kQlBlock - 1) / kQlBlock;
+    p.sx = x->scales;
+    p.sx_stride = x->scale_stride;
+    p.sw[0] = p.sw[1] = w->scales;
+    p.add = add;
+    p.add_stride = add_stride;
+    p.y = y;
+    p.y_fp32 = y_type == DSPARK_ENTRY_FP32;
+    p.y_stride = y_stride;
+    p.err = (int *)ws;
+    return product(p, false, x, w, w, (cudaStream_t)stream);
+}
+
+dspark_status dspark_qlinear_gated(const dspark_qrows_t *x, const dspark_qweight_t *gate, const dspark_qweight_t *up,
+                                   const dspark_qrows_t *h, void *ws, size_t ws_bytes, void *stream) {
+    dspark_status s = check_rows(x);
+    if (s == DSPARK_OK) s = check_weight(gate);
+    if (s == DSPARK_OK) s = check_weight(up);
+    if (s == DSPARK_OK) s = check_rows(h);
+    if (s != DSPARK_OK) return s;
+    if (x->k != gate->k || x->k != up->k || gate->n != up->n || h->k != gate->n || h->rows != x->rows) return DSPARK_ERR_SHAPE;
+    if (!ws || ws_bytes < DSPARK_QLINEAR_WS_BYTES) return DSPARK_ERR_WORKSPACE;
+    if (!ok16(ws)) return DSPARK_ERR_ALIGN;
+    if (x->rows == 0) return DSPARK_OK;
+    const unsigned long long rows = (unsigned long long)x->rows;
+    const unsigned long long kb = (x->k + kQlBlock - 1) / kQlBlock, hb = (h->k + kQlBlock - 1) / kQlBlock;
+    const unsigned long long sx_bytes = ((kb - 1) * (unsigned long long)x->scale_stride + rows) * 4;
+    const unsigned long long sh_bytes = ((hb - 1) * (unsigned long long)h->scale_stride + rows) * 4;
+    if (overlap(h->codes, rows * h->k, x->codes, rows * x->k) || overlap(h->scales, sh_bytes, x->scales, sx_bytes))
+        return DSPARK_ERR_SHAPE;
+    QlParams p;
+    memset(&p, 0, sizeof(p));
+    p.M = x->rows;
+    p.N = gate->n;
+    p.KB = (int)kb;
+    p.sx = x->scales;
+    p.sx_stride = x->scale_stride;
+    p.sw[0] = gate->scales;
+    p.sw[1] = up->scales;
+    p.h = (uint8_t *)h->codes;
+    p.sh = h->scales;
+    p.sh_stride = h->scale_stride;
+    p.err = (int *)ws;
+    return product(p, true, x, gate, up, (cudaStream_t)stream);
+}
+
+}  // extern "C"

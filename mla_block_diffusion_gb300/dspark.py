@@ -24,7 +24,8 @@ STATUS = {0: "OK", 1: "ERR_NULL", 2: "ERR_ALIGN", 3: "ERR_SHAPE", 4: "ERR_UNSUPP
 EXPORTS = ("dspark_create", "dspark_destroy", "dspark_workspace_bytes", "dspark_fuse_ctx", "dspark_draft_block",
            "dspark_markov_rollout", "dspark_confidence", "dspark_verify", "dspark_check", "dspark_status_str",
            "dspark_fuse_ctx_noalloc", "dspark_kv_append", "dspark_qcache_plan", "dspark_qcache_append",
-           "dspark_qcache_attend", "dspark_qcache_workspace_bytes", "dspark_qcache_check")
+           "dspark_qcache_attend", "dspark_qcache_workspace_bytes", "dspark_qcache_check", "dspark_qlinear_quantise",
+           "dspark_qlinear_quantise_weight", "dspark_qlinear_matmul", "dspark_qlinear_gated")
 
 
 class Geom(C.Structure):
@@ -58,6 +59,14 @@ class KV(C.Structure):
 class Sample(C.Structure):
     _fields_ = [("draft_mode", C.c_int), ("verify_mode", C.c_int), ("temperature", C.c_float),
                 ("top_p", C.c_float), ("seed", C.c_uint64), ("step", C.c_uint32)]
+
+
+class QRowsStruct(C.Structure):
+    _fields_ = [("rows", C.c_int), ("k", C.c_int), ("codes", C.c_void_p), ("scales", C.c_void_p), ("scale_stride", C.c_int64)]
+
+
+class QWeightStruct(C.Structure):
+    _fields_ = [("n", C.c_int), ("k", C.c_int), ("codes", C.c_void_p), ("scales", C.c_void_p)]
 
 
 class QCacheStruct(C.Structure):
@@ -113,6 +122,12 @@ def lib():
         L.dspark_qcache_workspace_bytes.argtypes = [C.POINTER(QCacheStruct), i]
         L.dspark_qcache_workspace_bytes.restype = sz
         L.dspark_qcache_check.argtypes = [vp, vp]
+        L.dspark_qlinear_quantise.argtypes = [vp, i, C.c_int64, C.POINTER(QRowsStruct), vp]
+        L.dspark_qlinear_quantise_weight.argtypes = [vp, i, C.c_int64, C.POINTER(QWeightStruct), vp]
+        L.dspark_qlinear_matmul.argtypes = [C.POINTER(QRowsStruct), C.POINTER(QWeightStruct), vp, C.c_int64, vp, i, C.c_int64, vp,
+                                            sz, vp]
+        L.dspark_qlinear_gated.argtypes = [C.POINTER(QRowsStruct), C.POINTER(QWeightStruct), C.POINTER(QWeightStruct),
+                                           C.POINTER(QRowsStruct), vp, sz, vp]
         L.dspark_status_str.argtypes = [i]
         L.dspark_status_str.restype = C.c_char_p
         for f in EXPORTS:
@@ -423,3 +438,149 @@ class QCache:
         """Synchronise and return (and clear) the device error word."""
         self._device()
         return lib().dspark_qcache_check(_p(self.ws), _stream())
+
+
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_QLINEAR_WS = 1024
+
+
+def _qrows(name: str, codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QRowsStruct:
+    """Quantised rows: codes [rows, k], scales fp32 [ceil(k / 128), rows]."""
+    if codes.dim() != 2 or codes.dtype not in _CODES or codes.get_device() != dev or not codes.is_contiguous():
+        raise ValueError(f"{name}: codes are a contiguous uint8 or float8_e4m3fn tensor [rows, k] on cuda:{dev}")
+    rows, k = codes.shape
+    blocks = (k + 127) // 128
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or tuple(scales.shape) != (blocks, rows):
+        raise ValueError(f"{name}: scales are an fp32 tensor [{blocks}, {rows}] on cuda:{dev}")
+    stride, one = scales.stride()
+    if rows > 1 and one != 1 or blocks > 1 and stride < rows:
+        raise ValueError(f"{name}: the scales of a block are contiguous")
+    return QRowsStruct(rows, k, codes.data_ptr() or None, scales.data_ptr() or None, stride if blocks > 1 else rows)
+
+
+def _qsource(name: str, x: torch.Tensor, shape, dev: int):
+    """Type and row stride of a matrix to be quantised."""
+    if tuple(x.shape) != tuple(shape) or x.get_device() != dev:
+        raise ValueError(f"{name}: tensor {list(shape)} on cuda:{dev}")
+    kind = 0 if x.dtype is torch.bfloat16 else 1
+    if kind and x.dtype is not torch.float32:
+        raise ValueError(f"{name}: bf16 or fp32")
+    stride, one = x.stride()
+    if one != 1 and x.shape[1] > 1:
+        raise ValueError(f"{name}: the elements of a row are contiguous")
+    return kind, stride if x.shape[0] > 1 else x.shape[1]  # torch leaves the stride of one row open
+
+
+def quantise_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """x [rows, k] (bf16 or fp32, any row stride) into E4M3 codes [rows, k] and scales fp32 [ceil(k / 128), rows], one
+    power of two per row and 128 elements; k is a multiple of 16. Tensors lie on the current GPU; nothing waits."""
+    dev = torch._C._cuda_getDevice()
+    r = _qrows("quantise_rows", codes, scales, dev)
+    kind, stride = _qsource("x", x, codes.shape, dev)
+    st = lib().dspark_qlinear_quantise(x.data_ptr() or None, kind, stride, C.byref(r), _stream())
+    if st:
+        raise DSparkError("dspark_qlinear_quantise", st)
+
+
+def quantise_weight(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
+    """w [n, k] (bf16 or fp32, any row stride) into E4M3 codes [n, k] and scales fp32 [ceil(n / 128), ceil(k / 128)], one
+    power of two per block of 128 x 128; n and k are multiples of 16."""
+    dev = torch._C._cuda_getDevice()
+    a = _qweight(codes, scales, dev)
+    kind, stride = _qsource("w", w, codes.shape, dev)
+    st = lib().dspark_qlinear_quantise_weight(w.data_ptr() or None, kind, stride, C.byref(a), _stream())
+    if st:
+        raise DSparkError("dspark_qlinear_quantise_weight", st)
+
+
+def _qweight(codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QWeightStruct:
+    if codes.dim() != 2 or codes.dtype not in _CODES or codes.get_device() != dev or not codes.is_contiguous():
+        raise ValueError(f"codes: a contiguous uint8 or float8_e4m3fn tensor [n, k] on cuda:{dev}")
+    n, k = codes.shape
+    want = ((n + 127) // 128, (k + 127) // 128)
+    if (scales.dtype is not torch.float32 or scales.get_device() != dev or tuple(scales.shape) != want
+            or not scales.is_contiguous()):
+        raise ValueError(f"scales: a contiguous fp32 tensor {list(want)} on cuda:{dev}")
+    return QWeightStruct(n, k, codes.data_ptr() or None, scales.data_ptr() or None)
+
+
+class QLinear:
+    """A weight matrix in E4M3 with one fp32 scale per block of 128 x 128.
+
+    ``codes`` uint8 or float8_e4m3fn [n, k] (n and k multiples of 16), ``scales`` fp32 [ceil(n / 128), ceil(k / 128)];
+    both belong to the caller and are read at each call. They and every call's tensors lie on one GPU, the current one
+    at each call. Calls run on the current stream and do not wait. ``check()`` reads the error word that the kernels
+    set; a zero-filled ``workspace`` (uint8, 1024 bytes) may be given and shared.
+    """
+
+    def __init__(self, codes: torch.Tensor, scales: torch.Tensor, workspace: Optional[torch.Tensor] = None):
+        self.dev = codes.get_device()
+        if self.dev < 0:
+            raise ValueError("codes: a CUDA tensor")
+        self.w = _qweight(codes, scales, self.dev)
+        if not 16 <= self.w.n <= 1 << 20 or not 16 <= self.w.k <= 1 << 20 or self.w.n % 16 or self.w.k % 16:
+            raise ValueError("codes: n and k are multiples of 16 up to 2^20")
+        self.ref = C.byref(self.w)
+        self._keep = (codes, scales)  # the struct holds raw device pointers
+        if workspace is None:
+            workspace = torch.zeros(_QLINEAR_WS, dtype=torch.uint8, device=codes.device)
+        if workspace.dtype is not torch.uint8 or workspace.get_device() != self.dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{self.dev}, zero-filled before its first use")
+        self.ws, self.ws_ptr, self.ws_bytes = workspace, C.c_void_p(workspace.data_ptr()), workspace.numel()
+
+    def _device(self) -> int:
+        dev = torch._C._cuda_getDevice()
+        if dev != self.dev:
+            raise ValueError(f"the weights lie on cuda:{self.dev}, the current device is cuda:{dev}")
+        return dev
+
+    def matmul(self, codes: torch.Tensor, scales: torch.Tensor, y: torch.Tensor, add: Optional[torch.Tensor] = None):
+        """y = x w^T (+ add) for the quantised rows x (``codes`` [rows, k], ``scales`` [ceil(k / 128), rows]): y bf16 or
+        fp32 [rows, n], add fp32 [rows, n] (may be y), any row strides."""
+        dev = self._device()
+        r = _qrows("x", codes, scales, dev)
+        n = self.w.n
+        if r.k != self.w.k:
+            raise ValueError(f"x: codes [rows, {self.w.k}]")
+        kind, stride = _qsource("y", y, (r.rows, n), dev)
+        pa, add_stride = None, n
+        if add is not None:
+            if _qsource("add", add, (r.rows, n), dev)[0] != 1:
+                raise ValueError("add: fp32")
+            pa, add_stride = add.data_ptr() or None, add.stride(0) if r.rows > 1 else n
+        st = lib().dspark_qlinear_matmul(C.byref(r), self.ref, pa, add_stride, y.data_ptr() or None, kind, stride, self.ws_ptr,
+                                         self.ws_bytes, _stream())
+        if st:
+            raise DSparkError("dspark_qlinear_matmul", st)
+
+    def check(self) -> int:
+        """Synchronise and return (and clear) the device error word."""
+        self._device()
+        return lib().dspark_qcache_check(_p(self.ws), _stream())
+
+
+class QGated:
+    """The first half of a gated feed-forward block: silu(x gate^T) * (x up^T), quantised as rows in the same kernel.
+
+    ``gate`` and ``up`` are QLinear matrices of one shape; the second half is the down projection's ``matmul``."""
+
+    def __init__(self, gate: QLinear, up: QLinear):
+        if (gate.w.n, gate.w.k, gate.dev) != (up.w.n, up.w.k, up.dev):
+            raise ValueError("gate and up: one shape, one device")
+        self.gate, self.up = gate, up
+
+    def forward(self, codes: torch.Tensor, scales: torch.Tensor, h_codes: torch.Tensor, h_scales: torch.Tensor):
+        """Quantised rows x (``codes`` [rows, k], ``scales`` [ceil(k / 128), rows]) into quantised rows h (``h_codes``
+        [rows, n], ``h_scales`` [ceil(n / 128), rows])."""
+        g = self.gate
+        dev = g._device()
+        x, h = _qrows("x", codes, scales, dev), _qrows("h", h_codes, h_scales, dev)
+        if x.k != g.w.k or h.k != g.w.n or h.rows != x.rows:
+            raise ValueError(f"x: codes [rows, {g.w.k}], h: codes [rows, {g.w.n}]")
+        st = lib().dspark_qlinear_gated(C.byref(x), g.ref, self.up.ref, C.byref(h), g.ws_ptr, g.ws_bytes, _stream())
+        if st:
+            raise DSparkError("dspark_qlinear_gated", st)
+
+    def check(self) -> int:
+        """Synchronise and return (and clear) the device error word (the gate's)."""
+        return self.gate.check()
