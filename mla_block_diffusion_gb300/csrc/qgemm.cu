@@ -2,14 +2,15 @@
 //
 //   y[m, n] = sum_b sx[b, m] sw[n / 128, b] sum_{k in block b} cx[m, k] cw[n, k]
 //
-// A tile is 128 rows x 256 outputs: 256 columns of one matrix, or 128 of the
-// gate's and the same 128 of up's, so that the epilogue holds both factors of
-// silu(g) u. Rows are the accumulator's lanes. E4M3 codes go to the tensor core as
-// they are stored (kind::f8f6f4); a block of 128 k is four MMAs into one of two
-// accumulators of 256 columns, from which the epilogue warps add it, times
-// sx sw, to fp32 registers: scales are any fp32 numbers, and no sum is longer than
-// 128 terms before it is one of fp32 FMAs. A thread holds 64 + 64 columns of one row,
-// so that a block costs it two factors.
+// A pair of CTAs (cta_group::2) holds a tile of 256 rows x 256 outputs of one matrix (128
+// where wider tiles would leave SMs without one), or 128 of the gate's and the same 128 of up's, so that
+// the epilogue holds both factors of silu(g) u. Rows are the accumulator's lanes, 128
+// a CTA; each CTA loads its rows and half of the outputs' codes. E4M3 codes go to the
+// tensor core as they are stored (kind::f8f6f4); a block of 128 k is four MMAs into one of two
+// accumulators, from which eight warps add it, times sx sw, to fp32 registers: scales
+// are any fp32 numbers, and no sum is longer than 128 terms before it is one of fp32
+// FMAs. The accumulator's columns are the first CTA's 64 of the first half, its 64 of
+// the second, then the other CTA's, so that a warp's 128 columns have two factors.
 #include <math.h>
 
 #include "per_device.h"
@@ -17,42 +18,116 @@
 
 namespace ds {
 
-constexpr int kQgThreads = 384;                    // 4 warps that issue, 8 that sum; registers: 168 x 384 = 88 x 128 + 208 x 256
-constexpr int kQgRegsIssue = 88, kQgRegsSum = 208;
+constexpr int kQgSum0 = 4;                         // warps: loads, products, scales, none; then those that sum
+constexpr int kQgSums = 8, kQgWide = 512 / kQgSums;  // columns of either half that a warp sums
+constexpr int kQgThreads = 32 * (kQgSum0 + kQgSums);  // registers: 168 x 384 = 56 x 128 + 224 x 256
+constexpr int kQgRegsIssue = 56, kQgRegsSum = 224;
 constexpr int kQgBox = 128 * 128;                  // bytes: 128 rows or outputs x 128 k
-constexpr int kQgStage = 3 * kQgBox;               // rows, two boxes of outputs
-constexpr int kQgStages = 4;
-constexpr int kQgOut = 8 * 4096;                   // staged output: 4 KB a summing warp
+constexpr int kQgStages = 5;
+constexpr int kQgSlots = 2;                        // accumulators of 256 columns
+constexpr int kQgOut = kQgSums * 4096;             // staged output: 4 KB a summing warp
+constexpr int kQgGroup = 8;                        // blocks of k whose scales arrive together
 
 struct QgBars {
-    uint64_t full[kQgStages], empty[kQgStages], afull[2], aempty[2], done;
+    uint64_t full[kQgStages], empty[kQgStages], afull[kQgSlots], aempty[kQgSlots], done;  // full, aempty: the pair's, in its first CTA
+    uint64_t sfull[2], sempty[2];                  // scales
+    uint64_t group[4];                             // gated: the four warps of 32 rows
     uint32_t tmem;
     volatile int abort;
     uint32_t issued;                               // stages that the producer has requested
-    uint32_t amax[2][2][128];                      // gated, tiles in turn: a row's largest magnitude by column half
+    alignas(16) float x[2][kQgGroup][128];         // scales: rows'
+    alignas(16) float2 w[2][kQgGroup];             // the two halves'
+    int8_t e[2][kQgSums / 4][128];                           // gated, tiles in turn: a row's scale exponent by column group
 };
-constexpr int kQgSmem = kQgStages * kQgStage + kQgOut + (int)sizeof(QgBars);
+constexpr int kQgSmem = kQgStages * 2 * kQgBox + kQgOut + (int)sizeof(QgBars);
 static_assert(kQgSmem <= 232448, "shared memory");
 
-template <bool GATED>
+// The pair's forms of what common.cuh and e4m3.cuh have for one CTA.
+DS_DEVINL uint32_t first_of_pair(const void *local) {  // the same place in the first CTA's shared memory
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(local)));
+    return a;
+}
+DS_DEVINL void tma_load_2d_pair(void *dst, const CUtensorMap *m, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+DS_DEVINL void tmem_alloc_pair(uint32_t *slot, uint32_t cols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+DS_DEVINL void tmem_dealloc_pair(uint32_t addr, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+DS_DEVINL void mma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive on this barrier of both CTAs once the MMAs issued before are done.
+DS_DEVINL void mma_commit_pair(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+// Without memory ordering at the pair's scope (that is a memory barrier, 1000 clocks a block): what the arrival
+// publishes are reads of tensor memory, ordered by tcgen05.wait and the tcgen05 fences.
+DS_DEVINL void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 columns of the warp's lanes and the wait for them in one statement: apart, with the registers tied to the wait, each
+// costs a move, and the block's sums take as many issue slots as its products take clocks.
+DS_DEVINL void tmem_ld32_now(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
+}
+
+// Four bytes into shared memory; the barrier's arrival when all that this thread has requested is there.
+DS_DEVINL void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+DS_DEVINL void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// HALVES: columns of the tile / 128; gated: 2, the gate's and up's
+template <bool GATED, int HALVES>
 __global__ void __launch_bounds__(kQgThreads, 1)
     qgemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                  const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int tiles_m, int tiles) {
+    constexpr int kBoxW = 64 * 128, kStage = kQgBox + HALVES * kBoxW;  // a CTA's rows, its 64 of each half's outputs
+    constexpr int kStep = GATED ? 128 : 128 * HALVES;
+    static_assert(!GATED || HALVES == 2, "gate and up");
     extern __shared__ __align__(1024) uint8_t qg_smem[];
-    uint8_t *sOut = qg_smem + kQgStages * kQgStage;
+    uint8_t *sOut = qg_smem + kQgStages * 2 * kQgBox;
     QgBars &ms = *(QgBars *)(sOut + kQgOut);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort = &ms.abort;
-    const int KB = p.KB;
+    const int KB = p.KB, rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (tid == 0) {
         for (int s = 0; s < kQgStages; ++s) {
             mbar_init(&ms.full[s], 1);
             mbar_init(&ms.empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < kQgSlots; ++s) {
             mbar_init(&ms.afull[s], 1);
-            mbar_init(&ms.aempty[s], 8);
+            mbar_init(&ms.aempty[s], 2 * kQgSums);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ms.sfull[s], 32);
+            mbar_init(&ms.sempty[s], kQgSums);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&ms.group[i], kQgSums / 4);
         mbar_init(&ms.done, 1);
         ms.abort = 0;
         fence_mbar_init();
@@ -60,12 +135,12 @@ __global__ void __launch_bounds__(kQgThreads, 1)
         tma_prefetch_desc(&tm_w0);
         if (GATED) tma_prefetch_desc(&tm_w1);
     }
-    __syncthreads();
+    cluster_sync();
     // Tensor memory is taken once the kernels before have ended, and the kernel behind is let in once it is taken: of
     // two that share an SM, neither holds what the other waits for. The producer needs none and goes ahead.
     pdl_wait();
     if (warp == 1) {
-        tmem_alloc(&ms.tmem, 512);
+        tmem_alloc_pair(&ms.tmem, 512);
         pdl_trigger();
     }
     uint32_t tmem = 0;
@@ -76,124 +151,154 @@ __global__ void __launch_bounds__(kQgThreads, 1)
         tmem = ms.tmem;
     }
 
-    if (warp < 4) {
+    if (warp < kQgSum0) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQgRegsIssue));
         if (warp == 0) {
             if (ql_elect()) {
                 uint32_t u = 0;
                 bool ok = true;
-                for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
-                    const int m0 = t % tiles_m * 128, n0 = t / tiles_m * (GATED ? 128 : 256);
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    const int m0 = t % tiles_m * 256 + 128 * rank, n0 = t / tiles_m * kStep + 64 * rank;
                     for (int kb = 0; kb < KB; ++kb, ++u) {
                         const uint32_t s = u % kQgStages, par = (u / kQgStages) & 1;
                         if (u >= kQgStages && !mbar_wait_bounded(&ms.empty[s], par ^ 1, abort)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *to = qg_smem + s * kQgStage;
-                        mbar_arrive_expect_tx(&ms.full[s], kQgStage);
+                        uint8_t *to = qg_smem + s * kStage;
+                        const uint32_t bar = first_of_pair(&ms.full[s]);
+                        if (rank == 0) mbar_arrive_expect_tx(&ms.full[s], 2 * kStage);
                         // 16-bit elements: 64 a box row
-                        tma_load_2d(to, &tm_x, kb * 64, m0, &ms.full[s]);
-                        tma_load_2d(to + kQgBox, &tm_w0, kb * 64, n0, &ms.full[s]);
-                        if (GATED) tma_load_2d(to + 2 * kQgBox, &tm_w1, kb * 64, n0, &ms.full[s]);
-                        else tma_load_2d(to + 2 * kQgBox, &tm_w0, kb * 64, n0 + 128, &ms.full[s]);
+                        tma_load_2d_pair(to, &tm_x, kb * 64, m0, bar);
+                        tma_load_2d_pair(to + kQgBox, &tm_w0, kb * 64, n0, bar);
+                        if (HALVES == 2) tma_load_2d_pair(to + kQgBox + kBoxW, GATED ? &tm_w1 : &tm_w0, kb * 64, n0 + (GATED ? 0 : 128), bar);
                     }
                 }
                 ms.issued = u;
             }
             __syncwarp();
         } else if (warp == 1) {
-            if (ql_elect()) {
+            if (rank == 0 && ql_elect()) {
                 const uint32_t lo = sdesc_lo(smem_u32(qg_smem));
-                constexpr uint32_t hi = sdesc_hi(1024, 2), id = idesc_e4m3_f32(128, 256);
+                constexpr uint32_t hi = sdesc_hi(1024, 2), id = idesc_e4m3_f32(256, 128 * HALVES);
                 uint32_t u = 0;
                 bool ok = true;
-                for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x)
+                for (int t = pair; t < tiles && ok; t += pairs)
                     for (int kb = 0; kb < KB; ++kb, ++u) {
                         const uint32_t s = u % kQgStages;
-                        ok = mbar_wait_bounded(&ms.full[s], (u / kQgStages) & 1, abort) &&
-                             (u < 2 || mbar_wait_bounded(&ms.aempty[u & 1], ((u >> 1) & 1) ^ 1, abort));
+                        ok = mbar_wait_bounded(&ms.full[s], (u / kQgStages) & 1, abort);
+                        const uint32_t a = lo + s * (kStage >> 4), b = a + (kQgBox >> 4);
+                        ok = ok && (u < kQgSlots || mbar_wait_bounded(&ms.aempty[u % kQgSlots], ((u / kQgSlots) & 1) ^ 1, abort));
                         if (!ok) break;
                         tc_fence_after();
-                        const uint32_t a = lo + s * (kQgStage >> 4), b = a + (kQgBox >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            mma_e4m3(tmem + 256 * (u & 1), (uint64_t)hi << 32 | (a + 2 * k), (uint64_t)hi << 32 | (b + 2 * k), id, k > 0);
-                        mma_commit(&ms.empty[s]);
-                        mma_commit(&ms.afull[u & 1]);
+                            mma_e4m3_pair(tmem + 256 * (u % kQgSlots), (uint64_t)hi << 32 | (a + 2 * k), (uint64_t)hi << 32 | (b + 2 * k), id, k > 0);
+                        mma_commit_pair(&ms.afull[u % kQgSlots]);
+                        mma_commit_pair(&ms.empty[s]);
                     }
-                mma_commit(&ms.done);
+                mma_commit_pair(&ms.done);
                 mbar_drain(&ms.done, 0);
             }
             __syncwarp();
+        } else if (warp == 2) {
+            // scales, a group of blocks ahead: a load's latency would otherwise stand in every block of the summing warps
+            const int nb = (p.N + kQlBlock - 1) / kQlBlock;
+            uint32_t g = 0;
+            bool ok = true;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                const int m0 = t % tiles_m * 256 + 128 * rank, b0 = t / tiles_m * kStep / kQlBlock;
+                const float *s0 = p.sw[0] + (size_t)b0 * KB;
+                const float *s1 = GATED ? p.sw[1] + (size_t)b0 * KB : s0 + (b0 + 1 < nb ? KB : 0);
+                const float *s = lane & 1 ? s1 : s0;
+                for (int kb = 0; kb < KB; kb += kQgGroup, ++g) {
+                    const uint32_t at = g & 1;
+                    ok = g < 2 || ql_warp_wait(&ms.sempty[at], ((g >> 1) & 1) ^ 1, abort);
+                    if (!ok) break;
+                    const int n = min(kQgGroup, KB - kb);
+                    for (int j = 0; j < n; ++j) {
+                        const float *x = p.sx + (size_t)(kb + j) * p.sx_stride;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cp_async4(&ms.x[at][j][lane + 32 * i], x + min(m0 + lane + 32 * i, p.M - 1));
+                    }
+                    if ((lane >> 1) < n) cp_async4((float *)&ms.w[at][lane >> 1] + (lane & 1), s + kb + (lane >> 1));
+                    cp_async_arrive(&ms.sfull[at]);
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQgRegsSum));
-        const int q = warp & 3, h = (warp - 4) >> 2;  // lanes 32 q .., columns 64 h .. of either half
-        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * h;
-        uint8_t *out = sOut + (warp - 4) * 4096;
-        uint32_t u = 0, count = 0;
+        const int q = warp & 3, h = (warp - kQgSum0) >> 2;  // lanes 32 q .., columns kQgWide h .. of each half
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + 64 * HALVES * h;
+        uint8_t *out = sOut + (warp - kQgSum0) * 4096;
+        uint32_t u = 0, g = 0, count = 0;
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++count) {
-            const int m0 = t % tiles_m * 128 + 32 * q, n0 = t / tiles_m * (GATED ? 128 : 256), row = m0 + lane;
-            const int nb = (p.N + kQlBlock - 1) / kQlBlock, b0 = n0 / kQlBlock;
-            const float *sx = p.sx + (row < p.M ? row : p.M - 1);
-            const float *s0 = p.sw[0] + (size_t)b0 * KB;
-            const float *s1 = GATED ? p.sw[1] + (size_t)b0 * KB : s0 + (b0 + 1 < nb ? KB : 0);
-            unsigned long long acc[64];  // columns 64 h .. of the first half, then of the second
+        for (int t = pair; t < tiles && ok; t += pairs, ++count) {
+            const int m0 = t % tiles_m * 256 + 128 * rank + 32 * q, n0 = t / tiles_m * kStep, row = m0 + lane;
+            float acc[kQgWide * HALVES];  // columns kQgWide h .. of the first half, then of the second
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
-            // scales two blocks ahead
-            float x0 = __ldg(sx), x1 = KB > 1 ? __ldg(sx + p.sx_stride) : 0.f;
-            float a0 = __ldg(s0), a1 = KB > 1 ? __ldg(s0 + 1) : 0.f, c0 = __ldg(s1), c1 = KB > 1 ? __ldg(s1 + 1) : 0.f;
+            for (int i = 0; i < kQgWide * HALVES; ++i) acc[i] = 0.f;
+            if (!GATED && p.add && row < p.M) {
+                // the tile's share of `add` on its way into L2 while the products are formed
+#pragma unroll
+                for (int c = 0; c < HALVES; ++c) {
+                    const int n = n0 + 128 * c + kQgWide * h;
+                    if (n < p.N) prefetch_l2_bulk(p.add + (size_t)row * p.add_stride + n, 4 * min(kQgWide, p.N - n));
+                }
+            }
             for (int kb = 0; kb < KB; ++kb, ++u) {
-                const unsigned long long f0 = pack2(x0 * a0), f1 = pack2(x0 * c0);
-                x0 = x1;
-                a0 = a1;
-                c0 = c1;
-                if (kb + 2 < KB) {
-                    x1 = __ldg(sx + (size_t)(kb + 2) * p.sx_stride);
-                    a1 = __ldg(s0 + kb + 2);
-                    c1 = __ldg(s1 + kb + 2);
+                const int j = kb % kQgGroup;
+                if (j == 0) {
+                    ok = ql_warp_wait(&ms.sfull[g & 1], (g >> 1) & 1, abort);
+                    if (!ok) break;
+                }
+                const float x = ms.x[g & 1][j][32 * q + lane];
+                const float2 w = ms.w[g & 1][j];
+                const float f0 = x * w.x, f1 = x * w.y;
+                if (j == kQgGroup - 1 || kb == KB - 1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.sempty[g & 1]);
+                    ++g;
                 }
                 ok = ql_warp_wait(&ms.afull[u & 1], (u >> 1) & 1, abort);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = tl + 256 * (u & 1);
-                uint32_t v[2][16];
-                tmem_ld16_issue(at, v[0]);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_ld_wait_tied(v[c & 1]);
-                    if (c < 7) tmem_ld16_issue(at + (c + 1 & 3) * 16 + (c + 1 >> 2) * 128, v[~c & 1]);
+                for (int c = 0; c < 2 * HALVES; ++c) {
+                    float v[32];
+                    tmem_ld32_now(at + 32 * c, v);
+                    if (c + 1 == 2 * HALVES) {  // read: its products may be replaced
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(first_of_pair(&ms.aempty[u & 1]));
+                    }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], c < 4 ? f0 : f1);
+                    for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(v[i], c < 2 ? f0 : f1, acc[32 * c + i]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ms.aempty[u & 1]);
             }
             if (!ok) break;
             if constexpr (GATED) {
-                float v[64];
+                float v[kQgWide];
                 uint32_t mx = 0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const float2 g = unpack2(acc[i]), w = unpack2(acc[32 + i]);
-                    v[2 * i] = ql_gate(g.x, w.x);
-                    v[2 * i + 1] = ql_gate(g.y, w.y);
-                    const uint32_t a = __float_as_uint(v[2 * i]) & 0x7fffffffu, b = __float_as_uint(v[2 * i + 1]) & 0x7fffffffu;
+                for (int i = 0; i < kQgWide; ++i) {
+                    v[i] = ql_gate(acc[i], acc[kQgWide * (HALVES - 1) + i]);
+                    const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
                     if (a < 0x7f800000u) mx = max(mx, a);
-                    else v[2 * i] = __uint_as_float(0x7fffffffu);
-                    if (b < 0x7f800000u) mx = max(mx, b);
-                    else v[2 * i + 1] = __uint_as_float(0x7fffffffu);
+                    else v[i] = __uint_as_float(0x7fffffffu);
                 }
-                ms.amax[count & 1][h][32 * q + lane] = mx;
-                named_bar_sync(1 + q, 64);  // the two warps of these rows
-                mx = max(mx, ms.amax[count & 1][h ^ 1][32 * q + lane]);
-                const int e = ql_exponent(mx);
+                int e = ql_exponent(mx);  // (of the largest: the largest of the groups')
+                ms.e[count & 1][h][32 * q + lane] = (int8_t)e;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ms.group[q]);
+                ok = ql_warp_wait(&ms.group[q], count & 1, abort);
+                if (!ok) break;
+#pragma unroll
+                for (int i = 0; i < kQgSums / 4; ++i) e = max(e, (int)ms.e[count & 1][i][32 * q + lane]);
                 const float inv = qc_pow2(-e);
-                if (h == 0 && row < p.M) p.sh[(size_t)b0 * p.sh_stride + row] = qc_pow2(e);
+                if (h == 0 && row < p.M) p.sh[(size_t)(n0 / kQlBlock) * p.sh_stride + row] = qc_pow2(e);
                 // 64 bytes a row, 16-byte pieces swizzled; then four lanes a row
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -214,37 +319,52 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                 }
                 __syncwarp();
             } else {
-                // 32 columns at a time through shared memory: 128 bytes a row, 16-byte pieces swizzled
+                // 32 columns at a time through shared memory: 128 bytes a row, 16-byte pieces swizzled; then eight lanes a
+                // row, whose share of `add` is requested two steps ahead
+                constexpr int kPer = kQgWide / 32;
+                const int r0 = lane >> 3, left = p.M - m0;
+                auto column = [&](int c) { return n0 + 128 * (c / kPer) + kQgWide * h + 32 * (c % kPer) + 4 * (lane & 7); };
+                float4 a[2][8];
+                auto fetch = [&](int c) {
+                    const int n = column(c);
+                    const float *at = p.add + (size_t)(m0 + r0) * p.add_stride + n;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                    for (int i = 0; i < 8; ++i)
+                        a[c & 1][i] = 4 * i + r0 < left && n < p.N ? *(const float4 *)(at + (size_t)(4 * i) * p.add_stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+                };
+                if (p.add) {
+                    fetch(0);
+                    if (kPer * HALVES > 1) fetch(1);
+                }
+#pragma unroll
+                for (int c = 0; c < kPer * HALVES; ++c) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float2 a = unpack2(acc[16 * c + 2 * i]), b = unpack2(acc[16 * c + 2 * i + 1]);
-                        *(float4 *)(out + lane * 128 + ((i ^ lane) & 7) * 16) = make_float4(a.x, a.y, b.x, b.y);
+                        const float *v = acc + 32 * c + 4 * i;
+                        *(float4 *)(out + lane * 128 + ((i ^ lane) & 7) * 16) = make_float4(v[0], v[1], v[2], v[3]);
                     }
                     __syncwarp();
-                    const int n = n0 + 128 * (c >> 1) + 64 * h + 32 * (c & 1) + 4 * (lane & 7);
+                    const int n = column(c);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3), m = m0 + r;
-                        float4 v = *(const float4 *)(out + r * 128 + ((lane ^ r) & 7) * 16);
-                        if (m < p.M && n < p.N) {
-                            if (p.add) {
-                                const float4 a = *(const float4 *)(p.add + (size_t)m * p.add_stride + n);
-                                v.x += a.x;
-                                v.y += a.y;
-                                v.z += a.z;
-                                v.w += a.w;
-                            }
+                        float4 v = *(const float4 *)(out + (4 * i + r0) * 128 + ((lane ^ (4 * i + r0)) & 7) * 16);
+                        if (p.add) {
+                            v.x += a[c & 1][i].x;
+                            v.y += a[c & 1][i].y;
+                            v.z += a[c & 1][i].z;
+                            v.w += a[c & 1][i].w;
+                        }
+                        if (4 * i + r0 < left && n < p.N) {
+                            const size_t to = (size_t)(m0 + 4 * i + r0) * p.y_stride + n;
                             if (p.y_fp32) {
-                                *(float4 *)((float *)p.y + (size_t)m * p.y_stride + n) = v;
+                                *(float4 *)((float *)p.y + to) = v;
                             } else {
-                                const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-                                *(uint2 *)((__nv_bfloat16 *)p.y + (size_t)m * p.y_stride + n) =
-                                    make_uint2(*(const uint32_t *)&a, *(const uint32_t *)&b);
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+                                *(uint2 *)((__nv_bfloat16 *)p.y + to) = make_uint2(*(const uint32_t *)&lo, *(const uint32_t *)&hi);
                             }
                         }
                     }
+                    if (p.add && c + 2 < kPer * HALVES) fetch(c + 2);
                     __syncwarp();
                 }
             }
@@ -252,34 +372,48 @@ __global__ void __launch_bounds__(kQgThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        tmem_dealloc(tmem, 512);
-    }
-    if (tid == 0 && ms.abort) {  // no copy outlives the CTA
-        for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; u < ms.issued; ++u)
+    if (tid == 0) mbar_drain(&ms.done, 0);  // in either CTA: no arrival is on its way either
+    if (tid == 0 && ms.abort) {  // no copy outlives the pair
+        for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; rank == 0 && u < ms.issued; ++u)
             mbar_drain(&ms.full[u % kQgStages], (u / kQgStages) & 1);
         set_error(p.err, DSPARK_ERR_TIMEOUT);
     }
+    __syncwarp();
+    cluster_sync();  // the pair's products and barriers are in either CTA's memory
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
 }
 
-template <bool GATED>
-static cudaError_t launch(const QlParams &p, const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1, int num_sms,
+template <bool GATED, int HALVES>
+static cudaError_t launch(const QlParams &p, const CUtensorMap &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int pairs,
                           cudaStream_t st) {
     static OncePerDevice once;
-    const cudaError_t e =
-        once([] { return cudaFuncSetAttribute(qgemm_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem); });
+    const cudaError_t e = once(
+        [] { return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem); });
     if (e != cudaSuccess) return e;
-    const int tiles_m = (p.M + 127) / 128, tiles_n = (p.N + (GATED ? 127 : 255)) / (GATED ? 128 : 256);
+    CUtensorMap m0, m1;
+    if (!encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 64)) return cudaErrorInvalidValue;
+    m1 = m0;
+    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, 64)) return cudaErrorInvalidValue;
+    const int step = GATED ? 128 : 128 * HALVES, tiles_m = (p.M + 255) / 256, tiles_n = (p.N + step - 1) / step;
     const long long tiles = (long long)tiles_m * tiles_n;
     if (tiles >= 1ll << 30) return cudaErrorInvalidValue;
-    return launch_pdl(qgemm_kernel<GATED>, dim3((unsigned)(tiles < num_sms ? tiles : num_sms)), dim3(kQgThreads), (size_t)kQgSmem, st,
-                      x, w0, w1, p, tiles_m, (int)tiles);
+    return launch_pdl_cluster(qgemm_kernel<GATED, HALVES>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), dim3(kQgThreads),
+                              (size_t)kQgSmem, st, 2, x, m0, m1, p, tiles_m, (int)tiles);
 }
 
-cudaError_t launch_qgemm(const QlParams &p, bool gated, const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
+cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
                          int num_sms, cudaStream_t st) {
-    return gated ? launch<true>(p, x, w0, w1, num_sms, st) : launch<false>(p, x, w0, w1, num_sms, st);
+    CUtensorMap mx;
+    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, 128)) return cudaErrorInvalidValue;
+    const int pairs = num_sms / 2;
+    if (gated) return launch<true, 2>(p, mx, w0, w1, pairs, st);
+    // waves of tiles, in units of half a tile's time
+    const long long tm = (p.M + 255) / 256, wide = (tm * ((p.N + 255) / 256) + pairs - 1) / pairs * 2,
+                    half = (tm * ((p.N + 127) / 128) + pairs - 1) / pairs;
+    return half < wide ? launch<false, 1>(p, mx, w0, w0, pairs, st) : launch<false, 2>(p, mx, w0, w0, pairs, st);
 }
 
 }  // namespace ds

@@ -253,32 +253,35 @@ __global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
 }
 
 template <int NT, bool GATED>
-static cudaError_t launch(const QlParams &p, const void *x_codes, const CUtensorMap &w0, const CUtensorMap &w1, int num_sms,
-                          cudaStream_t st, uint64_t k) {
+static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int num_sms,
+                          cudaStream_t st) {
     using C = QfCfg<NT, GATED>;
     static OncePerDevice once;
     const cudaError_t e = once(
         [] { return cudaFuncSetAttribute(qgemm_few_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (e != cudaSuccess) return e;
-    CUtensorMap x;
-    if (!encode_u16_map(&x, x_codes, p.M, k, 128, NT)) return cudaErrorInvalidValue;
+    CUtensorMap mx, m0, m1;
+    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, NT) || !encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 128))
+        return cudaErrorInvalidValue;
+    m1 = m0;
+    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, 128)) return cudaErrorInvalidValue;
     const int tiles = (p.N + 127) / 128;
     int split = 1;
     while (split < kQfMaxSplit && split < p.KB && tiles * (split + 1) <= 2 * num_sms) ++split;
-    return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3(tiles * split), dim3(C::kThreads), (size_t)C::kSmem, st, split, x, w0, w1,
-                              p, split);
+    return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3(tiles * split), dim3(C::kThreads), (size_t)C::kSmem, st, split, mx, m0,
+                              m1, p, split);
 }
 template <bool GATED>
-static cudaError_t pick(const QlParams &p, const void *x_codes, const CUtensorMap &w0, const CUtensorMap &w1, int num_sms,
-                        cudaStream_t st, uint64_t k) {
-    if (p.M <= 16) return launch<16, GATED>(p, x_codes, w0, w1, num_sms, st, k);
-    if (p.M <= 32) return launch<32, GATED>(p, x_codes, w0, w1, num_sms, st, k);
-    return launch<64, GATED>(p, x_codes, w0, w1, num_sms, st, k);
+static cudaError_t pick(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int num_sms,
+                        cudaStream_t st) {
+    if (p.M <= 16) return launch<16, GATED>(p, x, w0, w1, num_sms, st);
+    if (p.M <= 32) return launch<32, GATED>(p, x, w0, w1, num_sms, st);
+    return launch<64, GATED>(p, x, w0, w1, num_sms, st);
 }
 
-cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const CUtensorMap &w0, const CUtensorMap &w1,
-                             int num_sms, cudaStream_t st) {
-    return gated ? pick<true>(p, x.codes, w0, w1, num_sms, st, x.k) : pick<false>(p, x.codes, w0, w1, num_sms, st, x.k);
+cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0,
+                             const dspark_qweight_t &w1, int num_sms, cudaStream_t st) {
+    return gated ? pick<true>(p, x, w0, w1, num_sms, st) : pick<false>(p, x, w0, w1, num_sms, st);
 }
 
 }  // namespace ds

@@ -221,14 +221,7 @@ dspark_status product(const QlParams &p, bool gated, const dspark_qrows_t *x, co
                       const dspark_qweight_t *w1, cudaStream_t st) {
     const int sms = current_sms();
     if (sms < 1) return DSPARK_ERR_CUDA;
-    CUtensorMap mw0, mw1;
-    if (!encode_u16_map(&mw0, w0->codes, w0->n, w0->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
-    mw1 = mw0;
-    if (gated && !encode_u16_map(&mw1, w1->codes, w1->n, w1->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
-    if (p.M <= 64) return done(launch_qgemm_few(p, gated, *x, mw0, mw1, sms, st));
-    CUtensorMap mx;
-    if (!encode_u16_map(&mx, x->codes, x->rows, x->k, 128, kQlBlock)) return DSPARK_ERR_CUDA;
-    return done(launch_qgemm(p, gated, mx, mw0, mw1, sms, st));
+    return done(p.M <= 64 ? launch_qgemm_few(p, gated, *x, *w0, *w1, sms, st) : launch_qgemm(p, gated, *x, *w0, *w1, sms, st));
 }
 
 }  // namespace

@@ -69,9 +69,9 @@ DS_DEVINL float2 unpack2(unsigned long long d) {
     return f;
 }
 
-cudaError_t launch_qgemm(const QlParams &p, bool gated, const CUtensorMap &x, const CUtensorMap &w0, const CUtensorMap &w1,
+cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
                          int num_sms, cudaStream_t st);
-cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const CUtensorMap &w0, const CUtensorMap &w1,
-                             int num_sms, cudaStream_t st);
+cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0,
+                             const dspark_qweight_t &w1, int num_sms, cudaStream_t st);
 
 }  // namespace ds

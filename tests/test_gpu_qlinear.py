@@ -134,6 +134,18 @@ def test_matmul(m, n, k, out):
     assert (off <= bound).all(), (off / bound).max()
 
 
+@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (65, 19472, 144), (1000, 9744, 16)])
+@pytest.mark.parametrize("out", ["bf16", "add"])
+def test_matmul_of_many_tiles(m, n, k, out):
+    """Tiles of the full width, several a CTA."""
+    test_matmul(m, n, k, out)
+
+
+@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (1300, 4112, 144)])
+def test_gated_of_many_tiles(m, n, k):
+    test_gated(m, n, k)
+
+
 @pytest.mark.parametrize("m", ROWS)
 @pytest.mark.parametrize("n,k", SHAPES)
 def test_gated(m, n, k):
