@@ -101,7 +101,7 @@ DS_DEVINL void cp_async_arrive(uint64_t *bar) {
 }
 
 // HALVES: columns of the tile / 128; gated: 2, the gate's and up's
-template <bool GATED, int HALVES>
+template <bool GATED, int HALVES, bool ADD>
 __global__ void __launch_bounds__(kQgThreads, 1)
     qgemm_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
                  const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int tiles_m, int tiles) {
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
             float acc[kQgWide * HALVES];  // columns kQgWide h .. of the first half, then of the second
 #pragma unroll
             for (int i = 0; i < kQgWide * HALVES; ++i) acc[i] = 0.f;
-            if (!GATED && p.add && row < p.M) {
+            if (ADD && row < p.M) {
                 // the tile's share of `add` on its way into L2 while the products are formed
 #pragma unroll
                 for (int c = 0; c < HALVES; ++c) {
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                     for (int i = 0; i < 8; ++i)
                         a[c & 1][i] = 4 * i + r0 < left && n < p.N ? *(const float4 *)(at + (size_t)(4 * i) * p.add_stride) : make_float4(0.f, 0.f, 0.f, 0.f);
                 };
-                if (p.add) {
+                if (ADD) {
                     fetch(0);
                     if (kPer * HALVES > 1) fetch(1);
                 }
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         float4 v = *(const float4 *)(out + (4 * i + r0) * 128 + ((lane ^ (4 * i + r0)) & 7) * 16);
-                        if (p.add) {
+                        if (ADD) {
                             v.x += a[c & 1][i].x;
                             v.y += a[c & 1][i].y;
                             v.z += a[c & 1][i].z;
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                             }
                         }
                     }
-                    if (p.add && c + 2 < kPer * HALVES) fetch(c + 2);
+                    if (ADD && c + 2 < kPer * HALVES) fetch(c + 2);
                     __syncwarp();
                 }
             }
@@ -386,12 +386,12 @@ __global__ void __launch_bounds__(kQgThreads, 1)
     }
 }
 
-template <bool GATED, int HALVES>
+template <bool GATED, int HALVES, bool ADD>
 static cudaError_t launch(const QlParams &p, const CUtensorMap &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int pairs,
                           cudaStream_t st) {
     static OncePerDevice once;
     const cudaError_t e = once(
-        [] { return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem); });
+        [] { return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem); });
     if (e != cudaSuccess) return e;
     CUtensorMap m0, m1;
     if (!encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 64)) return cudaErrorInvalidValue;
@@ -400,7 +400,7 @@ static cudaError_t launch(const QlParams &p, const CUtensorMap &x, const dspark_
     const int step = GATED ? 128 : 128 * HALVES, tiles_m = (p.M + 255) / 256, tiles_n = (p.N + step - 1) / step;
     const long long tiles = (long long)tiles_m * tiles_n;
     if (tiles >= 1ll << 30) return cudaErrorInvalidValue;
-    return launch_pdl_cluster(qgemm_kernel<GATED, HALVES>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), dim3(kQgThreads),
+    return launch_pdl_cluster(qgemm_kernel<GATED, HALVES, ADD>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), dim3(kQgThreads),
                               (size_t)kQgSmem, st, 2, x, m0, m1, p, tiles_m, (int)tiles);
 }
 
@@ -409,11 +409,13 @@ cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x,
     CUtensorMap mx;
     if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, 128)) return cudaErrorInvalidValue;
     const int pairs = num_sms / 2;
-    if (gated) return launch<true, 2>(p, mx, w0, w1, pairs, st);
+    if (gated) return launch<true, 2, false>(p, mx, w0, w1, pairs, st);
     // waves of tiles, in units of half a tile's time
     const long long tm = (p.M + 255) / 256, wide = (tm * ((p.N + 255) / 256) + pairs - 1) / pairs * 2,
                     half = (tm * ((p.N + 127) / 128) + pairs - 1) / pairs;
-    return half < wide ? launch<false, 1>(p, mx, w0, w0, pairs, st) : launch<false, 2>(p, mx, w0, w0, pairs, st);
+    if (half < wide)
+        return p.add ? launch<false, 1, true>(p, mx, w0, w0, pairs, st) : launch<false, 1, false>(p, mx, w0, w0, pairs, st);
+    return p.add ? launch<false, 2, true>(p, mx, w0, w0, pairs, st) : launch<false, 2, false>(p, mx, w0, w0, pairs, st);
 }
 
 }  // namespace ds

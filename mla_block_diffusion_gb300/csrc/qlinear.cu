@@ -20,56 +20,57 @@ namespace ds {
 // ---------------------------------------------------------------------------
 constexpr int kQrThreads = 256, kQrRows = 8;
 
+// Eight consecutive elements, as they lie in memory.
 template <typename T>
 struct Eight {
-    uint4 v[sizeof(T) / 2];
+    static constexpr bool kWide = sizeof(T) == 4;
+    uint4 v[kWide ? 2 : 1];
     DS_DEVINL void load(const T *p) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = __ldg((const uint4 *)p + i);
+        v[0] = __ldg((const uint4 *)p);
+        if (kWide) v[kWide] = __ldg((const uint4 *)p + 1);
     }
     DS_DEVINL void zero() {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        v[0] = make_uint4(0, 0, 0, 0);
+        if (kWide) v[kWide] = v[0];
     }
-    DS_DEVINL void floats(float (&f)[8]) const {
+    DS_DEVINL float at(int i) const {
         const uint32_t *w = (const uint32_t *)v;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = __uint_as_float(sizeof(T) == 4 ? w[i] : (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+        return __uint_as_float(kWide ? w[i] : (i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
-};
-// Largest magnitude (bits) of the finite ones among eight; *bad: there is another.
-DS_DEVINL uint32_t amax8(const float (&f)[8], bool *bad) {
-    uint32_t m = 0;
+    // Largest magnitude, as the bits of an fp32 number (an infinity or NaN is above every number).
+    DS_DEVINL uint32_t amax() const {
+        const uint32_t *w = (const uint32_t *)v;
+        if (kWide) {
+            uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-    if (m >= 0x7f800000u) {
-        *bad = true;
-        m = 0;
-#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7fffffffu);
+            return m;
+        }
+        const uint32_t m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu), __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    DS_DEVINL uint32_t amax_finite() const {
+        uint32_t m = 0;
         for (int i = 0; i < 8; ++i) {
-            const uint32_t u = __float_as_uint(f[i]) & 0x7fffffffu;
+            const uint32_t u = __float_as_uint(at(i)) & 0x7fffffffu;
             if (u < 0x7f800000u) m = max(m, u);
         }
+        return m;
     }
-    return m;
-}
-DS_DEVINL uint2 codes8(const float (&f)[8], float inv, bool bad) {
-    uint32_t c[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a = f[2 * i], b = f[2 * i + 1];
-        if (bad) {
-            a = ql_inf_to_nan(a);
-            b = ql_inf_to_nan(b);
-        }
-        c[i] = ql_e4m3x2(a * inv, b * inv);
+    DS_DEVINL uint2 codes(float inv) const {
+        return make_uint2(ql_e4m3x2(at(0) * inv, at(1) * inv) | ql_e4m3x2(at(2) * inv, at(3) * inv) << 16,
+                          ql_e4m3x2(at(4) * inv, at(5) * inv) | ql_e4m3x2(at(6) * inv, at(7) * inv) << 16);
     }
-    return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-}
+    DS_DEVINL uint2 codes_nan(float inv) const {  // some are not finite
+        uint32_t c[4];
+        for (int i = 0; i < 4; ++i) c[i] = ql_e4m3x2(ql_inf_to_nan(at(2 * i)) * inv, ql_inf_to_nan(at(2 * i + 1)) * inv);
+        return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+    }
+};
+constexpr uint32_t kQlInf = 0x7f800000u;
 
 template <typename T, int PER>
-__global__ void __launch_bounds__(kQrThreads) quantise_rows_kernel(const T *__restrict__ x, long long x_stride, int M, int K,
+__global__ void __launch_bounds__(kQrThreads, sizeof(T) == 2 ? 8 : 5) quantise_rows_kernel(const T *__restrict__ x, long long x_stride, int M, int K,
                                                                    uint8_t *__restrict__ codes, float *__restrict__ scales,
                                                                    long long s_stride) {
     const int tid = threadIdx.x, lane16 = tid & 15, half = tid >> 4;
@@ -89,14 +90,13 @@ __global__ void __launch_bounds__(kQrThreads) quantise_rows_kernel(const T *__re
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int k = (b0 + 2 * i) * kQlBlock + 8 * lane16;
-        float f[8];
-        v[i].floats(f);
-        bool bad = false;
-        uint32_t m = amax8(f, &bad);
+        uint32_t m = v[i].amax();
+        const bool bad = __any_sync(~0u, m >= kQlInf);
+        if (bad) m = v[i].amax_finite();
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
         const int e = ql_exponent(m);
-        if (r < M && k < K) *(uint2 *)(codes + (long long)r * K + k) = codes8(f, qc_pow2(-e), bad);
+        if (r < M && k < K) *(uint2 *)(codes + (long long)r * K + k) = bad ? v[i].codes_nan(qc_pow2(-e)) : v[i].codes(qc_pow2(-e));
         if (lane16 == 0) s_scale[(half >> 3) + 2 * i][half & 7] = qc_pow2(e);
     }
     __syncthreads();
@@ -107,43 +107,45 @@ __global__ void __launch_bounds__(kQrThreads) quantise_rows_kernel(const T *__re
 }
 
 // The same over blocks of 128 x 128, one CTA each; the block waits in registers for its maximum.
+constexpr int kQwThreads = 512;
 template <typename T>
-__global__ void __launch_bounds__(kQrThreads) quantise_weight_kernel(const T *__restrict__ w, long long stride, int N, int K,
-                                                                     uint8_t *__restrict__ codes, float *__restrict__ scales) {
-    constexpr int kPer = kQlBlock / (kQrThreads / 16);  // rows of a half-warp
+__global__ void __launch_bounds__(kQwThreads, sizeof(T) == 2 ? 3 : 2)
+    quantise_weight_kernel(const T *__restrict__ w, long long stride, int N, int K, uint8_t *__restrict__ codes, float *__restrict__ scales) {
+    constexpr int kPer = kQlBlock / (kQwThreads / 16), kStep = kQlBlock / kPer;  // rows of a half-warp
     __shared__ uint32_t s_max;
-    const int tid = threadIdx.x, r0 = blockIdx.y * kQlBlock + (tid >> 4), k = blockIdx.x * kQlBlock + 8 * (tid & 15);
+    const int tid = threadIdx.x, across = (K + kQlBlock - 1) / kQlBlock;
+    const int r0 = blockIdx.x / across * kQlBlock + (tid >> 4), k = blockIdx.x % across * kQlBlock + 8 * (tid & 15);
     pdl_trigger();
     if (tid == 0) s_max = 0;
     pdl_wait();
-    __syncthreads();
     Eight<T> v[kPer];
+    const T *at = w + (long long)r0 * stride + k;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int r = r0 + 16 * i;
-        if (r < N && k < K) v[i].load(w + (long long)r * stride + k);
+        if (r0 + kStep * i < N && k < K) v[i].load(at + (long long)(kStep * i) * stride);
         else v[i].zero();
     }
+    __syncthreads();
     uint32_t m = 0;
-    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        float f[8];
-        v[i].floats(f);
-        m = max(m, amax8(f, &bad));
+    for (int i = 0; i < kPer; ++i) m = max(m, v[i].amax());
+    const bool bad = m >= kQlInf;
+    if (bad) {
+        m = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) m = max(m, v[i].amax_finite());
     }
     m = __reduce_max_sync(~0u, m);
     if ((tid & 31) == 0) atomicMax(&s_max, m);
     __syncthreads();
     const int e = ql_exponent(s_max);
+    uint8_t *to = codes + (long long)r0 * K + k;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int r = r0 + 16 * i;
-        float f[8];
-        v[i].floats(f);
-        if (r < N && k < K) *(uint2 *)(codes + (long long)r * K + k) = codes8(f, qc_pow2(-e), bad);
+        if (r0 + kStep * i < N && k < K)
+            *(uint2 *)(to + (long long)(kStep * i) * K) = bad ? v[i].codes_nan(qc_pow2(-e)) : v[i].codes(qc_pow2(-e));
     }
-    if (tid == 0) scales[(long long)blockIdx.y * gridDim.x + blockIdx.x] = qc_pow2(e);
+    if (tid == 0) scales[blockIdx.x] = qc_pow2(e);
 }
 
 template <typename T>
@@ -159,7 +161,7 @@ static cudaError_t launch_rows(const void *x, long long stride, const dspark_qro
 template <typename T>
 static cudaError_t launch_weight(const void *w, long long stride, const dspark_qweight_t &o, cudaStream_t st) {
     const int kb = (o.k + kQlBlock - 1) / kQlBlock, nb = (o.n + kQlBlock - 1) / kQlBlock;
-    return launch_pdl(quantise_weight_kernel<T>, dim3(kb, nb), dim3(kQrThreads), 0, st, (const T *)w, stride, o.n, o.k,
+    return launch_pdl(quantise_weight_kernel<T>, dim3(kb * nb), dim3(kQwThreads), 0, st, (const T *)w, stride, o.n, o.k,
                       (uint8_t *)o.codes, o.scales);
 }
 
