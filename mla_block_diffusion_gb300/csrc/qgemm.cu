@@ -82,16 +82,6 @@ DS_DEVINL void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// 32 columns of the warp's lanes and the wait for them in one statement: apart, with the registers tied to the wait, each
-// costs a move, and the block's sums take as many issue slots as its products take clocks.
-DS_DEVINL void tmem_ld32_now(uint32_t addr, float (&v)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
-        : "r"(addr)
-        : "memory");
-}
-
 // Four bytes into shared memory; the barrier's arrival when all that this thread has requested is there.
 DS_DEVINL void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -135,6 +125,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
         tma_prefetch_desc(&tm_w0);
         if (GATED) tma_prefetch_desc(&tm_w1);
     }
+    __syncthreads();  // (the cluster's barrier wants whole warps)
     cluster_sync();
     // Tensor memory is taken once the kernels before have ended, and the kernel behind is let in once it is taken: of
     // two that share an SM, neither holds what the other waits for. The producer needs none and goes ahead.
@@ -372,11 +363,19 @@ __global__ void __launch_bounds__(kQgThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (tid == 0) mbar_drain(&ms.done, 0);  // in either CTA: no arrival is on its way either
-    if (tid == 0 && ms.abort) {  // no copy outlives the pair
-        for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; rank == 0 && u < ms.issued; ++u)
-            mbar_drain(&ms.full[u % kQgStages], (u / kQgStages) & 1);
-        set_error(p.err, DSPARK_ERR_TIMEOUT);
+    if (tid == 0) {
+        // Every arrival that the products' commits, or the other CTA's warps, send to this CTA has come: one that is still on
+        // its way when the CTA has left would land in memory that is no longer its own.
+        mbar_drain(&ms.done, 0);
+        for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; !ms.abort && u < ms.issued; ++u)
+            mbar_drain(&ms.empty[u % kQgStages], (u / kQgStages) & 1);
+        for (uint32_t u = ms.issued > kQgSlots ? ms.issued - kQgSlots : 0; rank == 0 && !ms.abort && u < ms.issued; ++u)
+            mbar_drain(&ms.aempty[u % kQgSlots], (u / kQgSlots) & 1);  // and every one of the other CTA's
+        if (ms.abort) {  // no copy outlives the pair
+            for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; rank == 0 && u < ms.issued; ++u)
+                mbar_drain(&ms.full[u % kQgStages], (u / kQgStages) & 1);
+            set_error(p.err, DSPARK_ERR_TIMEOUT);
+        }
     }
     __syncwarp();
     cluster_sync();  // the pair's products and barriers are in either CTA's memory
@@ -387,35 +386,45 @@ __global__ void __launch_bounds__(kQgThreads, 1)
 }
 
 template <bool GATED, int HALVES, bool ADD>
-static cudaError_t launch(const QlParams &p, const CUtensorMap &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int pairs,
-                          cudaStream_t st) {
+static QlPlan plan(const QlParams &p) {
     static OncePerDevice once;
-    const cudaError_t e = once(
-        [] { return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem); });
-    if (e != cudaSuccess) return e;
-    CUtensorMap m0, m1;
-    if (!encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 64)) return cudaErrorInvalidValue;
-    m1 = m0;
-    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, 64)) return cudaErrorInvalidValue;
-    const int step = GATED ? 128 : 128 * HALVES, tiles_m = (p.M + 255) / 256, tiles_n = (p.N + step - 1) / step;
-    const long long tiles = (long long)tiles_m * tiles_n;
-    if (tiles >= 1ll << 30) return cudaErrorInvalidValue;
-    return launch_pdl_cluster(qgemm_kernel<GATED, HALVES, ADD>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), dim3(kQgThreads),
-                              (size_t)kQgSmem, st, 2, x, m0, m1, p, tiles_m, (int)tiles);
+    static ClusterRoom<decltype(&qgemm_kernel<GATED, HALVES, ADD>)> room;
+    constexpr int kStep = GATED ? 128 : 128 * HALVES;
+    QlPlan r = {HALVES, (long long)((p.M + 255) / 256) * ((p.N + kStep - 1) / kStep), 1, 0.f, cudaSuccess};
+    r.error = once([] {
+        return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem);
+    });
+    if (r.error != cudaSuccess) return r;
+    r.room = room(qgemm_kernel<GATED, HALVES, ADD>, 2, kQgThreads, kQgSmem);
+    r.time = 4.f + (float)((r.tiles + r.room - 1) / r.room) * (1.f + p.KB * (HALVES == 2 ? 0.47f : 0.26f));
+    return r;
 }
 
+template <bool GATED, int HALVES, bool ADD>
+static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
+                          const QlPlan &plan, cudaStream_t st) {
+    CUtensorMap mx, m0, m1;
+    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, 128) || !encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 64))
+        return cudaErrorInvalidValue;
+    m1 = m0;
+    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, 64)) return cudaErrorInvalidValue;
+    if (plan.tiles >= 1ll << 30) return cudaErrorInvalidValue;
+    const int pairs = (int)(plan.tiles < plan.room ? plan.tiles : plan.room);
+    return launch_pdl_cluster(qgemm_kernel<GATED, HALVES, ADD>, dim3(2 * pairs), dim3(kQgThreads), (size_t)kQgSmem, st, 2, mx, m0, m1, p,
+                              (p.M + 255) / 256, (int)plan.tiles);
+}
+
+QlPlan plan_qgemm(const QlParams &p, bool gated) {
+    if (gated) return plan<true, 2, false>(p);
+    const QlPlan wide = p.add ? plan<false, 2, true>(p) : plan<false, 2, false>(p);
+    const QlPlan half = p.add ? plan<false, 1, true>(p) : plan<false, 1, false>(p);
+    return half.time < wide.time ? half : wide;
+}
 cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
-                         int num_sms, cudaStream_t st) {
-    CUtensorMap mx;
-    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, 128)) return cudaErrorInvalidValue;
-    const int pairs = num_sms / 2;
-    if (gated) return launch<true, 2, false>(p, mx, w0, w1, pairs, st);
-    // waves of tiles, in units of half a tile's time
-    const long long tm = (p.M + 255) / 256, wide = (tm * ((p.N + 255) / 256) + pairs - 1) / pairs * 2,
-                    half = (tm * ((p.N + 127) / 128) + pairs - 1) / pairs;
-    if (half < wide)
-        return p.add ? launch<false, 1, true>(p, mx, w0, w0, pairs, st) : launch<false, 1, false>(p, mx, w0, w0, pairs, st);
-    return p.add ? launch<false, 2, true>(p, mx, w0, w0, pairs, st) : launch<false, 2, false>(p, mx, w0, w0, pairs, st);
+                         const QlPlan &plan, cudaStream_t st) {
+    if (gated) return launch<true, 2, false>(p, x, w0, w1, plan, st);
+    if (plan.split == 1) return p.add ? launch<false, 1, true>(p, x, w0, w1, plan, st) : launch<false, 1, false>(p, x, w0, w1, plan, st);
+    return p.add ? launch<false, 2, true>(p, x, w0, w1, plan, st) : launch<false, 2, false>(p, x, w0, w1, plan, st);
 }
 
 }  // namespace ds

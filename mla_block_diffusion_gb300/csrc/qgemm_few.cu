@@ -1,13 +1,14 @@
-// Products of few quantised rows (up to 64) with block-scaled weights (include/dspark.h, calls 12 and 13).
+// Products of few quantised rows with block-scaled weights (include/dspark.h, calls 12 and 13).
 //
 // The same sums as in qgemm.cu with outputs on the accumulator's 128 lanes and the
-// rows (padded to NT = 16, 32 or 64) as its columns: the weights stream past the
-// rows once. A CTA takes 128 outputs (gated: of gate and of up) and a share of the
-// blocks of k; the CTAs of a cluster share a tile's blocks, add their partial sums
-// in rank order through distributed shared memory, and each finishes some of the
-// rows, so nothing goes through global memory and a result does not depend on
-// timing. Bound: HBM (one byte a weight). The cluster is the largest of up to 8
-// CTAs that leaves all tiles in one wave of two CTAs an SM.
+// rows (padded to NT = 16, 32 or 64, more rows in tiles of 64) as its columns: the
+// weights stream past the rows. A CTA takes 128 outputs (gated: 64 of gate and the same 64 of up) and a
+// share of the blocks of k; the CTAs of a cluster share a tile's blocks (gated: and the
+// two halves of 128 outputs, which have a scale in common), add their partial sums in
+// rank order through distributed shared memory, and each finishes some of the rows, so
+// nothing goes through global memory and a result does not depend on timing. Bound: HBM
+// (one byte a weight). The cluster is the largest of up to 8 CTAs that leaves all tiles in
+// one wave of two CTAs an SM.
 #include <math.h>
 
 #include "per_device.h"
@@ -16,27 +17,25 @@
 namespace ds {
 
 constexpr int kQfWindow = 32;     // blocks of k whose factors lie in shared memory at a time
-constexpr int kQfMaxSplit = 8;
+constexpr int kQfMaxCluster = 8;
 
-template <int NT, bool GATED>
+template <int NT>
 struct QfCfg {
-    static constexpr int kMats = GATED ? 2 : 1;
-    static constexpr int kX = kMats * 128 * 128;                        // weights, then rows
+    static constexpr int kX = 128 * 128;                                // weights, then rows
     static constexpr int kStage = kX + NT * 128;
-    static constexpr int kFactors = kMats * kQfWindow * NT * 4;
-    static constexpr int kStages = (112 * 1024 - 2048 - kFactors) / kStage;
-    static constexpr int kSlots = 256 / (kMats * NT) < 4 ? 256 / (kMats * NT) : 4;
-    static constexpr int kCols = kSlots * kMats * NT;
-    static constexpr int kThreads = 64 + 128 * kMats;
-    static constexpr int kPartial = kMats * NT * 128 * 4;
-    static_assert(kStages >= 2 && kPartial <= kStages * kStage, "shared memory");
-    static_assert(kCols >= 32 && (kCols & (kCols - 1)) == 0, "tensor memory");
+    static constexpr int kFactors = kQfWindow * NT * 4;
+    static constexpr int kMats = 2;                                     // factors of gate and of up lie apart
+    static constexpr int kStages = (112 * 1024 - 2048 - kMats * kFactors) / kStage;
+    static constexpr int kSlots = 4, kCols = kSlots * NT;
+    static constexpr int kThreads = 64 + 128;
+    static_assert(kStages >= 3 && NT * 128 * 4 <= kStages * kStage, "shared memory");
+    static_assert(kCols >= 32 && kCols <= 256 && (kCols & (kCols - 1)) == 0, "tensor memory: two CTAs an SM");
     struct Bars {
         uint64_t full[kStages], empty[kStages], afull[kSlots], aempty[kSlots], done;
         uint32_t tmem, issued;
         volatile int abort;
     };
-    static constexpr int kSmem = kStages * kStage + kFactors + (int)sizeof(Bars);
+    static constexpr int kSmem = kStages * kStage + kMats * kFactors + (int)sizeof(Bars);
     static_assert(kSmem <= 112 * 1024, "two CTAs an SM");
 };
 
@@ -50,17 +49,20 @@ DS_DEVINL float4 ld_peer_f4(const float *local, uint32_t rank) {
 }
 
 template <int NT, bool GATED>
-__global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
+__global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
     qgemm_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
-                     const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int split) {
-    using C = QfCfg<NT, GATED>;
+                     const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int split, int tiles_m) {
+    using C = QfCfg<NT>;
     using Bars = typename C::Bars;
     extern __shared__ __align__(1024) uint8_t qf_smem[];
-    float *sF = (float *)(qf_smem + C::kStages * C::kStage);
-    Bars &ms = *(Bars *)((uint8_t *)sF + C::kFactors);
+    float *sF = (float *)(qf_smem + C::kStages * C::kStage);  // [gate, up][block][row]
+    Bars &ms = *(Bars *)((uint8_t *)sF + C::kMats * C::kFactors);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *abort = &ms.abort;
-    const int rank = blockIdx.x % split, n0 = blockIdx.x / split * 128;
+    // gated: ranks 0 .. split - 1 hold the first half of the 128 outputs, split .. 2 split - 1 the second
+    const int cluster = GATED ? 2 * split : split, peer = blockIdx.x % cluster, tile = blockIdx.x / cluster;
+    const int rank = GATED ? peer % split : peer, half = GATED ? peer / split : 0;
+    const int m0 = tile % tiles_m * NT, n0 = tile / tiles_m * 128, rows = min(NT, p.M - m0);
     const int k0 = (int)((long long)rank * p.KB / split), k1 = (int)((long long)(rank + 1) * p.KB / split);
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
         }
         for (int s = 0; s < C::kSlots; ++s) {
             mbar_init(&ms.afull[s], 1);
-            mbar_init(&ms.aempty[s], 4 * C::kMats);
+            mbar_init(&ms.aempty[s], 4);
         }
         mbar_init(&ms.done, 1);
         ms.abort = 0;
@@ -103,9 +105,9 @@ __global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
                 uint8_t *to = qf_smem + s * C::kStage;
                 mbar_arrive_expect_tx(&ms.full[s], C::kStage);
                 // 16-bit elements: 64 a box row
-                tma_load_2d(to, &tm_w0, kb * 64, n0, &ms.full[s]);
-                if (GATED) tma_load_2d(to + 128 * 128, &tm_w1, kb * 64, n0, &ms.full[s]);
-                tma_load_2d(to + C::kX, &tm_x, kb * 64, 0, &ms.full[s]);
+                tma_load_2d(to, &tm_w0, kb * 64, n0 + 64 * half, &ms.full[s]);
+                if (GATED) tma_load_2d(to + 64 * 128, &tm_w1, kb * 64, n0 + 64 * half, &ms.full[s]);
+                tma_load_2d(to + C::kX, &tm_x, kb * 64, m0, &ms.full[s]);
             }
             ms.issued = u;
         }
@@ -122,91 +124,100 @@ __global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
                 tc_fence_after();
                 const uint32_t w = lo + s * (C::kStage >> 4), x = w + (C::kX >> 4);
 #pragma unroll
-                for (int i = 0; i < C::kMats; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_e4m3(tmem + (a * C::kMats + i) * NT, (uint64_t)hi << 32 | (w + i * 1024 + 2 * k), (uint64_t)hi << 32 | (x + 2 * k),
-                                 id, k > 0);
+                for (int k = 0; k < 4; ++k)
+                    mma_e4m3(tmem + a * NT, (uint64_t)hi << 32 | (w + 2 * k), (uint64_t)hi << 32 | (x + 2 * k), id, k > 0);
                 mma_commit(&ms.empty[s]);
                 mma_commit(&ms.afull[a]);
             }
             mma_commit(&ms.done);
             mbar_drain(&ms.done, 0);
+            for (uint32_t u = n > C::kStages ? n - C::kStages : 0; !*abort && u < n; ++u)  // and what the last stages' commits send
+                mbar_drain(&ms.empty[u % C::kStages], (u / C::kStages) & 1);
         }
         __syncwarp();
     } else {
-        const int mat = (warp - 2) >> 2, q = warp & 3, me = tid - 64 - 128 * mat;
-        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16) + mat * NT;
-        float *fac = sF + mat * kQfWindow * NT;
-        const float *sw = (mat ? p.sw[1] : p.sw[0]) + (size_t)(n0 / kQlBlock) * p.KB;
-        unsigned long long acc[NT / 2];
+        const int q = warp & 3, me = tid - 64, mat = GATED && q >= 2;  // lanes 64 ..: up's outputs
+        const uint32_t tl = tmem + ((uint32_t)(32 * q) << 16);
+        const float *fac = sF + mat * (kQfWindow * NT);
+        const size_t block = (size_t)(n0 / kQlBlock) * p.KB;
+        float acc[NT];
 #pragma unroll
-        for (int i = 0; i < NT / 2; ++i) acc[i] = 0;
+        for (int i = 0; i < NT; ++i) acc[i] = 0.f;
         const uint32_t n = k1 - k0;
         for (uint32_t u = 0; u < n; ++u) {
             const uint32_t w = u % kQfWindow, a = u % C::kSlots;
             if (w == 0) {
-                named_bar_sync(1 + mat, 128);  // the window before has been used
+                named_bar_sync(1, 128);  // the window before has been used
                 const int blocks = min(kQfWindow, (int)(n - u));
                 for (int i = me; i < blocks * NT; i += 128) {
                     const int b = k0 + (int)u + i / NT, m = i % NT;
-                    fac[i] = m < p.M ? __ldg(p.sx + (size_t)b * p.sx_stride + m) * __ldg(sw + b) : 0.f;
+                    const float x = m < rows ? __ldg(p.sx + (size_t)b * p.sx_stride + m0 + m) : 0.f;
+                    sF[i] = x * __ldg(p.sw[0] + block + b);
+                    if (GATED) sF[kQfWindow * NT + i] = x * __ldg(p.sw[1] + block + b);
                 }
-                named_bar_sync(1 + mat, 128);
+                named_bar_sync(1, 128);
             }
             // every warp keeps to the barriers above, whatever a wait says
             if (!ql_warp_wait(&ms.afull[a], (u / C::kSlots) & 1, abort)) continue;
             tc_fence_after();
+            constexpr int kLoad = NT < 32 ? NT : 32;
 #pragma unroll
-            for (int c = 0; c < NT / 16; ++c) {
-                uint32_t v[16];
-                tmem_ld16_issue(tl + a * (C::kMats * NT) + 16 * c, v);
-                tmem_ld_wait_tied(v);
-                const ulonglong2 *f = (const ulonglong2 *)(fac + w * NT + 16 * c);
+            for (int c = 0; c < NT; c += kLoad) {
+                float v[kLoad];
+                if constexpr (NT < 32) tmem_ld16_now(tl + a * NT + c, v);
+                else tmem_ld32_now(tl + a * NT + c, v);
+                if (c + kLoad == NT) {  // read: its products may be replaced
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ms.aempty[a]);
+                }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const ulonglong2 g = f[i];
-                    fma2(acc[8 * c + 2 * i], v[4 * i], v[4 * i + 1], g.x);
-                    fma2(acc[8 * c + 2 * i + 1], v[4 * i + 2], v[4 * i + 3], g.y);
+                for (int i = 0; i < kLoad; i += 4) {
+                    const float4 f = *(const float4 *)(fac + w * NT + c + i);
+                    acc[c + i] = __fmaf_rn(v[i], f.x, acc[c + i]);
+                    acc[c + i + 1] = __fmaf_rn(v[i + 1], f.y, acc[c + i + 1]);
+                    acc[c + i + 2] = __fmaf_rn(v[i + 2], f.z, acc[c + i + 2]);
+                    acc[c + i + 3] = __fmaf_rn(v[i + 3], f.w, acc[c + i + 3]);
                 }
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.aempty[a]);
         }
-        // partial sums [matrix, row, output] in the stages' place: every product is done
-        float *part = (float *)qf_smem + mat * NT * 128 + 32 * q + lane;
+        // partial sums [row, output] in the stages' place: every product is done
+        float *part = (float *)qf_smem + 32 * q + lane;
         if (!*abort) {
 #pragma unroll
-            for (int i = 0; i < NT / 2; ++i) {
-                const float2 v = unpack2(acc[i]);
-                part[2 * i * 128] = v.x;
-                part[(2 * i + 1) * 128] = v.y;
-            }
+            for (int i = 0; i < NT; ++i) part[i * 128] = acc[i];
         }
     }
     tc_fence_before();
     __syncwarp();
     cluster_sync();
-    // row m is finished by CTA m % split: a warp a row, four outputs a lane
-    for (int m = rank + split * warp; m < p.M; m += split * (C::kThreads / 32)) {
-        float4 v[C::kMats];
+    // row i of the tile is finished by CTA i % cluster: a warp a row, four outputs a lane
+    for (int row = peer + cluster * warp; row < rows; row += cluster * (C::kThreads / 32)) {
+        const int m = m0 + row;
+        // partial sums of four outputs, in the place `at` of CTAs first .. first + split - 1
+        auto gather = [&](const float *at, int first) {
+            float4 s[kQfMaxCluster];
 #pragma unroll
-        for (int i = 0; i < C::kMats; ++i) {
-            const float *at = (const float *)qf_smem + (i * NT + m) * 128 + 4 * lane;
-            float4 s[kQfMaxSplit];
+            for (int r = 0; r < kQfMaxCluster; ++r)
+                if (r < split) s[r] = ld_peer_f4(at, first + r);
+            float4 v = s[0];
 #pragma unroll
-            for (int r = 0; r < kQfMaxSplit; ++r)
-                if (r < split) s[r] = ld_peer_f4(at, r);
-            v[i] = s[0];
-#pragma unroll
-            for (int r = 1; r < kQfMaxSplit; ++r)
+            for (int r = 1; r < kQfMaxCluster; ++r)
                 if (r < split) {
-                    v[i].x += s[r].x;
-                    v[i].y += s[r].y;
-                    v[i].z += s[r].z;
-                    v[i].w += s[r].w;
+                    v.x += s[r].x;
+                    v.y += s[r].y;
+                    v.z += s[r].z;
+                    v.w += s[r].w;
                 }
+            return v;
+        };
+        float4 v[C::kMats];
+        if (GATED) {  // outputs 4 lane ..: of half lane / 16, gate's at 4 (lane % 16), up's 64 behind
+            const float *at = (const float *)qf_smem + row * 128 + 4 * (lane & 15);
+            v[0] = gather(at, lane >> 4 ? split : 0);
+            v[1] = gather(at + 64, lane >> 4 ? split : 0);
+        } else {
+            v[0] = gather((const float *)qf_smem + row * 128 + 4 * lane, 0);
         }
         const int n = n0 + 4 * lane;
         if constexpr (GATED) {
@@ -253,35 +264,53 @@ __global__ void __launch_bounds__(QfCfg<NT, GATED>::kThreads, 2)
 }
 
 template <int NT, bool GATED>
-static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int num_sms,
-                          cudaStream_t st) {
-    using C = QfCfg<NT, GATED>;
+static QlPlan plan(const QlParams &p) {
+    using C = QfCfg<NT>;
     static OncePerDevice once;
-    const cudaError_t e = once(
+    static ClusterRoom<decltype(&qgemm_few_kernel<NT, GATED>)> room;
+    QlPlan r = {1, (long long)((p.N + 127) / 128) * ((p.M + NT - 1) / NT), 1, 0.f, cudaSuccess};
+    r.error = once(
         [] { return cudaFuncSetAttribute(qgemm_few_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
-    if (e != cudaSuccess) return e;
-    CUtensorMap mx, m0, m1;
-    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, NT) || !encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, 128))
-        return cudaErrorInvalidValue;
-    m1 = m0;
-    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, 128)) return cudaErrorInvalidValue;
-    const int tiles = (p.N + 127) / 128;
-    int split = 1;
-    while (split < kQfMaxSplit && split < p.KB && tiles * (split + 1) <= 2 * num_sms) ++split;
-    return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3(tiles * split), dim3(C::kThreads), (size_t)C::kSmem, st, split, mx, m0,
-                              m1, p, split);
-}
-template <bool GATED>
-static cudaError_t pick(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1, int num_sms,
-                        cudaStream_t st) {
-    if (p.M <= 16) return launch<16, GATED>(p, x, w0, w1, num_sms, st);
-    if (p.M <= 32) return launch<32, GATED>(p, x, w0, w1, num_sms, st);
-    return launch<64, GATED>(p, x, w0, w1, num_sms, st);
+    if (r.error != cudaSuccess) return r;
+    constexpr int kHalves = GATED ? 2 : 1;
+    // the largest cluster that leaves all tiles on the device at once
+    for (int s = 1; s * kHalves <= kQfMaxCluster && s <= p.KB; ++s) {
+        const int n = room(qgemm_few_kernel<NT, GATED>, s * kHalves, C::kThreads, C::kSmem);
+        if (s > 1 && r.tiles > n) continue;
+        r.split = s;
+        r.room = n;
+    }
+    const long long waves = (r.tiles + r.room - 1) / r.room, ctas = r.tiles * r.split * kHalves;
+    r.time = 4.f + (float)(waves * ((p.KB + r.split - 1) / r.split)) * (ctas <= 152 ? 0.37f : 0.56f);
+    return r;
 }
 
+template <int NT, bool GATED>
+static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
+                          const QlPlan &plan, cudaStream_t st) {
+    using C = QfCfg<NT>;
+    CUtensorMap mx, m0, m1;
+    constexpr int kBox = GATED ? 64 : 128;
+    if (!encode_u16_map(&mx, x.codes, x.rows, x.k, 128, NT) || !encode_u16_map(&m0, w0.codes, w0.n, w0.k, 128, kBox))
+        return cudaErrorInvalidValue;
+    m1 = m0;
+    if (GATED && !encode_u16_map(&m1, w1.codes, w1.n, w1.k, 128, kBox)) return cudaErrorInvalidValue;
+    const int cluster = plan.split * (GATED ? 2 : 1);
+    if (plan.tiles * cluster >= 1ll << 30) return cudaErrorInvalidValue;
+    return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3((unsigned)(plan.tiles * cluster)), dim3(C::kThreads), (size_t)C::kSmem, st,
+                              cluster, mx, m0, m1, p, plan.split, (p.M + NT - 1) / NT);
+}
+
+QlPlan plan_qgemm_few(const QlParams &p, bool gated) {
+    if (p.M <= 16) return gated ? plan<16, true>(p) : plan<16, false>(p);
+    if (p.M <= 32) return gated ? plan<32, true>(p) : plan<32, false>(p);
+    return gated ? plan<64, true>(p) : plan<64, false>(p);
+}
 cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0,
-                             const dspark_qweight_t &w1, int num_sms, cudaStream_t st) {
-    return gated ? pick<true>(p, x, w0, w1, num_sms, st) : pick<false>(p, x, w0, w1, num_sms, st);
+                             const dspark_qweight_t &w1, const QlPlan &plan, cudaStream_t st) {
+    if (p.M <= 16) return gated ? launch<16, true>(p, x, w0, w1, plan, st) : launch<16, false>(p, x, w0, w1, plan, st);
+    if (p.M <= 32) return gated ? launch<32, true>(p, x, w0, w1, plan, st) : launch<32, false>(p, x, w0, w1, plan, st);
+    return gated ? launch<64, true>(p, x, w0, w1, plan, st) : launch<64, false>(p, x, w0, w1, plan, st);
 }
 
 }  // namespace ds

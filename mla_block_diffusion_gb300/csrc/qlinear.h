@@ -1,6 +1,8 @@
 // Internal declarations of the 8-bit layers (qlinear.cu, qgemm.cu, qgemm_few.cu).
 #pragma once
 
+#include <atomic>
+
 #include "e4m3.cuh"
 #include "internal.h"
 #include "qcache.h"
@@ -13,7 +15,7 @@ constexpr int kQlEmin = -100;     // the least exponent of a scale that the quan
 // A product of quantised rows and one weight matrix, or (gated) two of the same shape.
 struct QlParams {
     int M, N, KB;                 // rows, outputs (of one matrix), blocks of k
-    const float *sx;              // [KB, M], row stride sx_stride
+    const float *sx;              // [KB, M], sx_stride from one block to the next
     long long sx_stride;
     const float *sw[2];           // [ceil(N / 128), KB]; gated: gate, up; else both the same
     // matmul
@@ -54,24 +56,67 @@ DS_DEVINL bool ql_elect() {
 DS_DEVINL bool ql_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
 }
-// acc (a pair of floats) += (a, b) * f
-DS_DEVINL void fma2(unsigned long long &acc, uint32_t a, uint32_t b, unsigned long long f) {
-    asm("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}" : "+l"(acc) : "r"(a), "r"(b), "l"(f));
+// 32 columns of the warp's lanes and the wait for them in one statement: apart, with the registers tied to the wait, each
+// costs a move, and the block's sums take as many issue slots as its products take clocks.
+DS_DEVINL void tmem_ld32_now(uint32_t addr, float (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
 }
-DS_DEVINL unsigned long long pack2(float f) {
-    unsigned long long d;
-    asm("mov.b64 %0, {%1, %1};" : "=l"(d) : "f"(f));
-    return d;
-}
-DS_DEVINL float2 unpack2(unsigned long long d) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(d));
-    return f;
+DS_DEVINL void tmem_ld16_now(uint32_t addr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
 }
 
+// Clusters of `cluster` CTAs that fit on the current device at once; asked once per kernel, size and device.
+template <typename Kernel>
+class ClusterRoom {
+    static constexpr int kDevices = 64, kMost = 8;
+    std::atomic<int> known_[kDevices][kMost + 1] = {};
+
+  public:
+    int operator()(Kernel kern, int cluster, int threads, int smem) {
+        int dev = 0, n = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+        const bool kept = dev >= 0 && dev < kDevices && cluster <= kMost;
+        if (kept && (n = known_[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(cluster);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+            (void)cudaGetLastError();
+            n = 1;
+        }
+        if (kept) known_[dev][cluster].store(n, std::memory_order_relaxed);
+        return n;
+    }
+};
+
+// How either kernel would divide a call and about how long that takes, in us.
+struct QlPlan {
+    int split;           // few: CTAs that share a tile's blocks of k; many: 1 or 2 halves of 128 outputs a tile
+    long long tiles;
+    int room;            // clusters on the device at once
+    float time;
+    cudaError_t error;
+};
+QlPlan plan_qgemm(const QlParams &p, bool gated);
+QlPlan plan_qgemm_few(const QlParams &p, bool gated);
 cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
-                         int num_sms, cudaStream_t st);
+                         const QlPlan &plan, cudaStream_t st);
 cudaError_t launch_qgemm_few(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0,
-                             const dspark_qweight_t &w1, int num_sms, cudaStream_t st);
+                             const dspark_qweight_t &w1, const QlPlan &plan, cudaStream_t st);
 
 }  // namespace ds
