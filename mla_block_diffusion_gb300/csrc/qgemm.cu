@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                         mma_commit_pair(&ms.empty[s]);
                     }
                 mma_commit_pair(&ms.done);
-                mbar_drain(&ms.done, 0);
+                ql_drain(&ms.done, 0);
             }
             __syncwarp();
         } else if (warp == 2) {
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                 if (j == kQgGroup - 1 || kb == KB - 1) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.sempty[g & 1]);
+                    __syncwarp();
                     ++g;
                 }
                 ok = ql_warp_wait(&ms.afull[u & 1], (u >> 1) & 1, abort);
@@ -264,6 +265,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(first_of_pair(&ms.aempty[u & 1]));
+                        __syncwarp();
                     }
 #pragma unroll
                     for (int i = 0; i < 32; ++i) acc[32 * c + i] = __fmaf_rn(v[i], c < 2 ? f0 : f1, acc[32 * c + i]);
@@ -366,14 +368,14 @@ __global__ void __launch_bounds__(kQgThreads, 1)
     if (tid == 0) {
         // Every arrival that the products' commits, or the other CTA's warps, send to this CTA has come: one that is still on
         // its way when the CTA has left would land in memory that is no longer its own.
-        mbar_drain(&ms.done, 0);
+        ql_drain(&ms.done, 0);
         for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; !ms.abort && u < ms.issued; ++u)
-            mbar_drain(&ms.empty[u % kQgStages], (u / kQgStages) & 1);
+            ql_drain(&ms.empty[u % kQgStages], (u / kQgStages) & 1);
         for (uint32_t u = ms.issued > kQgSlots ? ms.issued - kQgSlots : 0; rank == 0 && !ms.abort && u < ms.issued; ++u)
-            mbar_drain(&ms.aempty[u % kQgSlots], (u / kQgSlots) & 1);  // and every one of the other CTA's
+            ql_drain(&ms.aempty[u % kQgSlots], (u / kQgSlots) & 1);  // and every one of the other CTA's
         if (ms.abort) {  // no copy outlives the pair
             for (uint32_t u = ms.issued > kQgStages ? ms.issued - kQgStages : 0; rank == 0 && u < ms.issued; ++u)
-                mbar_drain(&ms.full[u % kQgStages], (u / kQgStages) & 1);
+                ql_drain(&ms.full[u % kQgStages], (u / kQgStages) & 1);
             set_error(p.err, DSPARK_ERR_TIMEOUT);
         }
     }

@@ -1,14 +1,14 @@
-// Products of few quantised rows with block-scaled weights (include/dspark.h, calls 12 and 13).
+// Products of few quantised rows (up to 64) with block-scaled weights (include/dspark.h, calls 12 and 13).
 //
 // The same sums as in qgemm.cu with outputs on the accumulator's 128 lanes and the
-// rows (padded to NT = 16, 32 or 64, more rows in tiles of 64) as its columns: the
-// weights stream past the rows. A CTA takes 128 outputs (gated: 64 of gate and the same 64 of up) and a
-// share of the blocks of k; the CTAs of a cluster share a tile's blocks (gated: and the
-// two halves of 128 outputs, which have a scale in common), add their partial sums in
-// rank order through distributed shared memory, and each finishes some of the rows, so
-// nothing goes through global memory and a result does not depend on timing. Bound: HBM
-// (one byte a weight). The cluster is the largest of up to 8 CTAs that leaves all tiles in
-// one wave of two CTAs an SM.
+// rows (padded to NT = 16, 32 or 64) as its columns: the weights stream past the rows
+// once, one CTA an SM, through a ring of 200 KB. A CTA takes 128 outputs (gated: 64 of gate and
+// the same 64 of up) and a share of the blocks of k; the CTAs of a cluster share a tile's
+// blocks (gated: and the two halves of 128 outputs, which have a scale in common), add
+// their partial sums in rank order through distributed shared memory, and each finishes
+// some of the rows, so nothing goes through global memory and a result does not depend on
+// timing. Bound: HBM (one byte a weight). The cluster is the largest of up to 8 CTAs that
+// leaves all tiles on the device at once.
 #include <math.h>
 
 #include "per_device.h"
@@ -16,7 +16,7 @@
 
 namespace ds {
 
-constexpr int kQfWindow = 32;     // blocks of k whose factors lie in shared memory at a time
+constexpr int kQfWindow = 16;     // blocks of k whose factors lie in shared memory at a time
 constexpr int kQfMaxCluster = 8;
 
 template <int NT>
@@ -25,18 +25,18 @@ struct QfCfg {
     static constexpr int kStage = kX + NT * 128;
     static constexpr int kFactors = kQfWindow * NT * 4;
     static constexpr int kMats = 2;                                     // factors of gate and of up lie apart
-    static constexpr int kStages = (112 * 1024 - 2048 - kMats * kFactors) / kStage;
-    static constexpr int kSlots = 4, kCols = kSlots * NT;
+    static constexpr int kStages = (208 * 1024 - kMats * kFactors) / kStage;
+    static constexpr int kSlots = 8, kCols = kSlots * NT;
     static constexpr int kThreads = 64 + 128;
     static_assert(kStages >= 3 && NT * 128 * 4 <= kStages * kStage, "shared memory");
-    static_assert(kCols >= 32 && kCols <= 256 && (kCols & (kCols - 1)) == 0, "tensor memory: two CTAs an SM");
+    static_assert(kCols >= 32 && kCols <= 512 && (kCols & (kCols - 1)) == 0, "tensor memory");
     struct Bars {
         uint64_t full[kStages], empty[kStages], afull[kSlots], aempty[kSlots], done;
         uint32_t tmem, issued;
         volatile int abort;
     };
     static constexpr int kSmem = kStages * kStage + kMats * kFactors + (int)sizeof(Bars);
-    static_assert(kSmem <= 112 * 1024, "two CTAs an SM");
+    static_assert(kSmem <= 232448 && kSmem > 116 * 1024, "shared memory: one CTA an SM");
 };
 
 // 16 bytes of the same place in the shared memory of CTA `rank` of the cluster.
@@ -49,9 +49,9 @@ DS_DEVINL float4 ld_peer_f4(const float *local, uint32_t rank) {
 }
 
 template <int NT, bool GATED>
-__global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
+__global__ void __launch_bounds__(QfCfg<NT>::kThreads, 1)
     qgemm_few_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w0,
-                     const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int split, int tiles_m) {
+                     const __grid_constant__ CUtensorMap tm_w1, const QlParams p, int split) {
     using C = QfCfg<NT>;
     using Bars = typename C::Bars;
     extern __shared__ __align__(1024) uint8_t qf_smem[];
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
     // gated: ranks 0 .. split - 1 hold the first half of the 128 outputs, split .. 2 split - 1 the second
     const int cluster = GATED ? 2 * split : split, peer = blockIdx.x % cluster, tile = blockIdx.x / cluster;
     const int rank = GATED ? peer % split : peer, half = GATED ? peer / split : 0;
-    const int m0 = tile % tiles_m * NT, n0 = tile / tiles_m * 128, rows = min(NT, p.M - m0);
+    const int n0 = tile * 128, rows = p.M;
     const int k0 = (int)((long long)rank * p.KB / split), k1 = (int)((long long)(rank + 1) * p.KB / split);
     if (tid == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
                 // 16-bit elements: 64 a box row
                 tma_load_2d(to, &tm_w0, kb * 64, n0 + 64 * half, &ms.full[s]);
                 if (GATED) tma_load_2d(to + 64 * 128, &tm_w1, kb * 64, n0 + 64 * half, &ms.full[s]);
-                tma_load_2d(to + C::kX, &tm_x, kb * 64, m0, &ms.full[s]);
+                tma_load_2d(to + C::kX, &tm_x, kb * 64, 0, &ms.full[s]);
             }
             ms.issued = u;
         }
@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
                 mma_commit(&ms.afull[a]);
             }
             mma_commit(&ms.done);
-            mbar_drain(&ms.done, 0);
+            ql_drain(&ms.done, 0);
             for (uint32_t u = n > C::kStages ? n - C::kStages : 0; !*abort && u < n; ++u)  // and what the last stages' commits send
-                mbar_drain(&ms.empty[u % C::kStages], (u / C::kStages) & 1);
+                ql_drain(&ms.empty[u % C::kStages], (u / C::kStages) & 1);
         }
         __syncwarp();
     } else {
@@ -147,14 +147,16 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
         for (uint32_t u = 0; u < n; ++u) {
             const uint32_t w = u % kQfWindow, a = u % C::kSlots;
             if (w == 0) {
+                __syncwarp();
                 named_bar_sync(1, 128);  // the window before has been used
                 const int blocks = min(kQfWindow, (int)(n - u));
                 for (int i = me; i < blocks * NT; i += 128) {
                     const int b = k0 + (int)u + i / NT, m = i % NT;
-                    const float x = m < rows ? __ldg(p.sx + (size_t)b * p.sx_stride + m0 + m) : 0.f;
+                    const float x = m < rows ? __ldg(p.sx + (size_t)b * p.sx_stride + m) : 0.f;
                     sF[i] = x * __ldg(p.sw[0] + block + b);
                     if (GATED) sF[kQfWindow * NT + i] = x * __ldg(p.sw[1] + block + b);
                 }
+                __syncwarp();
                 named_bar_sync(1, 128);
             }
             // every warp keeps to the barriers above, whatever a wait says
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ms.aempty[a]);
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int i = 0; i < kLoad; i += 4) {
@@ -193,7 +196,7 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
     cluster_sync();
     // row i of the tile is finished by CTA i % cluster: a warp a row, four outputs a lane
     for (int row = peer + cluster * warp; row < rows; row += cluster * (C::kThreads / 32)) {
-        const int m = m0 + row;
+        const int m = row;
         // partial sums of four outputs, in the place `at` of CTAs first .. first + split - 1
         auto gather = [&](const float *at, int first) {
             float4 s[kQfMaxCluster];
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(QfCfg<NT>::kThreads, 2)
     }
     if (tid == 0 && ms.abort) {  // no copy outlives the CTA
         for (uint32_t u = ms.issued > C::kStages ? ms.issued - C::kStages : 0; u < ms.issued; ++u)
-            mbar_drain(&ms.full[u % C::kStages], (u / C::kStages) & 1);
+            ql_drain(&ms.full[u % C::kStages], (u / C::kStages) & 1);
         set_error(p.err, DSPARK_ERR_TIMEOUT);
     }
 }
@@ -268,20 +271,17 @@ static QlPlan plan(const QlParams &p) {
     using C = QfCfg<NT>;
     static OncePerDevice once;
     static ClusterRoom<decltype(&qgemm_few_kernel<NT, GATED>)> room;
-    QlPlan r = {1, (long long)((p.N + 127) / 128) * ((p.M + NT - 1) / NT), 1, 0.f, cudaSuccess};
+    QlPlan r = {1, (p.N + 127) / 128, 1, 0.f, cudaSuccess};
     r.error = once(
         [] { return cudaFuncSetAttribute(qgemm_few_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem); });
     if (r.error != cudaSuccess) return r;
     constexpr int kHalves = GATED ? 2 : 1;
-    // the largest cluster that leaves all tiles on the device at once
     for (int s = 1; s * kHalves <= kQfMaxCluster && s <= p.KB; ++s) {
         const int n = room(qgemm_few_kernel<NT, GATED>, s * kHalves, C::kThreads, C::kSmem);
         if (s > 1 && r.tiles > n) continue;
         r.split = s;
         r.room = n;
     }
-    const long long waves = (r.tiles + r.room - 1) / r.room, ctas = r.tiles * r.split * kHalves;
-    r.time = 4.f + (float)(waves * ((p.KB + r.split - 1) / r.split)) * (ctas <= 152 ? 0.37f : 0.56f);
     return r;
 }
 
@@ -298,7 +298,7 @@ static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspa
     const int cluster = plan.split * (GATED ? 2 : 1);
     if (plan.tiles * cluster >= 1ll << 30) return cudaErrorInvalidValue;
     return launch_pdl_cluster(qgemm_few_kernel<NT, GATED>, dim3((unsigned)(plan.tiles * cluster)), dim3(C::kThreads), (size_t)C::kSmem, st,
-                              cluster, mx, m0, m1, p, plan.split, (p.M + NT - 1) / NT);
+                              cluster, mx, m0, m1, p, plan.split);
 }
 
 QlPlan plan_qgemm_few(const QlParams &p, bool gated) {

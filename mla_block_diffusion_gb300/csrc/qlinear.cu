@@ -217,19 +217,13 @@ unsigned long long source_bytes(int type, int64_t stride, int rows, int k) {
     return ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4);
 }
 
-// The kernel that is done sooner by either one's estimate: a few us for the call, and for every wave of tiles the blocks
-// of k that a cluster goes through one after another (qgemm_few: 0.37 us a block with a CTA an SM, 0.56 with two; qgemm: 0.47 for
-// 256 outputs, 0.26 for 128, and 1 a tile). Up to 64 rows qgemm_few always was (64 rows: 12288 outputs x 576 7.9 against 7.4 us, 14336 x
-// 7168 24.7 against 28.1, 576 x 14336 9.0 against 31.0); above, 7168 x 14336 of 128 rows 35.3 against 35.6 us, of 256 64.3 against 35.6,
-// 576 x 14336 of 256 rows 11.8 against 30.7, 2112 x 7168 of 320 14.9 against 18.8, of 512 19.7 against 18.8.
+// Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes (64 rows: 12288 outputs x 576
+// 7.9 against 7.4 us, 14336 x 7168 24.7 against 28.1, 576 x 14336 9.0 against 31.0).
 dspark_status product(const QlParams &p, bool gated, const dspark_qrows_t *x, const dspark_qweight_t *w0,
                       const dspark_qweight_t *w1, cudaStream_t st) {
-    const QlPlan few = plan_qgemm_few(p, gated);
-    if (few.error != cudaSuccess) return done(few.error);
-    if (p.M <= 64) return done(launch_qgemm_few(p, gated, *x, *w0, *w1, few, st));
-    const QlPlan many = plan_qgemm(p, gated);
-    if (many.error != cudaSuccess) return done(many.error);
-    return done(few.time < many.time ? launch_qgemm_few(p, gated, *x, *w0, *w1, few, st) : launch_qgemm(p, gated, *x, *w0, *w1, many, st));
+    const QlPlan plan = p.M <= 64 ? plan_qgemm_few(p, gated) : plan_qgemm(p, gated);
+    if (plan.error != cudaSuccess) return done(plan.error);
+    return done(p.M <= 64 ? launch_qgemm_few(p, gated, *x, *w0, *w1, plan, st) : launch_qgemm(p, gated, *x, *w0, *w1, plan, st));
 }
 
 }  // namespace

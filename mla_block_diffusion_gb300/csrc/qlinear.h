@@ -47,14 +47,33 @@ DS_DEVINL float ql_gate(float g, float u) { return __fdividef(g, 1.f + __expf(-g
 // An infinity as NaN, for the codes: E4M3 has no infinity, and what a row with one stands for is not finite.
 DS_DEVINL float ql_inf_to_nan(float x) { return fabsf(x) == INFINITY ? __uint_as_float(0x7fffffffu) : x; }
 
+// mbar_drain for what has nearly always come: reading the timer first would cost more than the look.
+DS_DEVINL void ql_drain(uint64_t *bar, uint32_t parity) {
+    if (!mbar_try_wait(bar, parity)) mbar_drain(bar, parity);
+}
 // One lane of the warp; a branch on it is known to hold a single thread.
 DS_DEVINL bool ql_elect() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
+// A whole warp waits, and stays whole: every turn of the loop ends in a vote, on which all lanes leave it together. What
+// follows reads tensor memory, which takes the 32 lanes at once whatever lanes execute it: after a wait that lets lanes
+// go one by one, a warp that happened to be split there had registers overwritten, and went on with wild addresses.
 DS_DEVINL bool ql_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort));
+    unsigned long long t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+        if ((i & 255u) == 255u) {
+            const unsigned long long t = __shfl_sync(~0u, globaltimer(), 0);
+            if (t0 == 0) t0 = t;
+            if (__any_sync(~0u, *abort != 0)) return false;
+            if (t - t0 > kWaitLimitNs) {
+                *abort = 1;
+                return false;
+            }
+        }
+    }
 }
 // 32 columns of the warp's lanes and the wait for them in one statement: apart, with the registers tied to the wait, each
 // costs a move, and the block's sums take as many issue slots as its products take clocks.
@@ -85,6 +104,7 @@ class ClusterRoom {
         if (cudaGetDevice(&dev) != cudaSuccess) return 0;
         const bool kept = dev >= 0 && dev < kDevices && cluster <= kMost;
         if (kept && (n = known_[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
+        carveout_max((const void *)kern);  // as every launch has it
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;

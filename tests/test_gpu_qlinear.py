@@ -134,16 +134,48 @@ def test_matmul(m, n, k, out):
     assert (off <= bound).all(), (off / bound).max()
 
 
-@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (65, 19472, 144), (1000, 9744, 16)])
+@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (65, 19472, 144), (1000, 9744, 16), (64, 20496, 4112), (320, 2112, 7168)])
 @pytest.mark.parametrize("out", ["bf16", "add"])
 def test_matmul_of_many_tiles(m, n, k, out):
     """Tiles of the full width, several a CTA."""
     test_matmul(m, n, k, out)
 
 
-@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (1300, 4112, 144)])
+@pytest.mark.parametrize("m,n,k", [(300, 9744, 272), (1300, 4112, 144), (64, 20496, 4112), (3, 20496, 4112), (30, 12304, 2576)])
 def test_gated_of_many_tiles(m, n, k):
     test_gated(m, n, k)
+
+
+@pytest.mark.parametrize("m,n", [(16, 20496), (60, 2112), (320, 2112), (150, 576)])
+def test_calls_in_a_row_give_the_same(m, n):
+    """Results do not depend on timing: calls that overlap in their prologues, eager and replayed, bit for bit."""
+    rng = np.random.default_rng(m)
+    k = 2576
+    x, sx = (dev(a) for a in rows_of(rng, m, k))
+    ws = [M.QLinear(*(dev(a) for a in weight_of(rng, n, k))) for _ in range(4)]
+    ys = torch.empty(4, m, n, device="cuda")
+    hs = [(torch.empty(m, n, dtype=torch.uint8, device="cuda"), torch.empty(-(-n // 128), m, device="cuda")) for _ in range(4)]
+
+    def calls():
+        for i in range(4):
+            ws[i].matmul(x, sx, ys[i])
+            M.QGated(ws[i], ws[(i + 1) % 4]).forward(x, sx, *hs[i])
+
+    def results():
+        return [ys.clone()] + [t.clone() for h in hs for t in h]
+    calls()
+    first = results()
+    for _ in range(10):
+        calls()
+    assert all(torch.equal(a, b) for a, b in zip(first, results()))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    ys.zero_()
+    for _ in range(10):
+        g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(first, results()))
+    assert all(w.check() == 0 for w in ws)
 
 
 @pytest.mark.parametrize("m", ROWS)
