@@ -82,14 +82,6 @@ DS_DEVINL void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// Four bytes into shared memory; the barrier's arrival when all that this thread has requested is there.
-DS_DEVINL void cp_async4(void *dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-DS_DEVINL void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 // HALVES: columns of the tile / 128; gated: 2, the gate's and up's
 template <bool GATED, int HALVES, bool ADD>
 __global__ void __launch_bounds__(kQgThreads, 1)

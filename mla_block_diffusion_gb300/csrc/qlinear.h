@@ -92,6 +92,14 @@ DS_DEVINL void tmem_ld16_now(uint32_t addr, float (&v)[16]) {
         : "memory");
 }
 
+// Four bytes into shared memory; the barrier's arrival when all that this thread has requested is there.
+DS_DEVINL void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+DS_DEVINL void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Clusters of `cluster` CTAs that fit on the current device at once; asked once per kernel, size and device.
 template <typename Kernel>
 class ClusterRoom {
