@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                     const float *at = p.add + (size_t)(m0 + r0) * p.add_stride + n;
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        a[c & 1][i] = 4 * i + r0 < left && n < p.N ? *(const float4 *)(at + (size_t)(4 * i) * p.add_stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        a[c & 1][i] = 4 * i + r0 < left && n < p.N ? __ldcs((const float4 *)(at + (size_t)(4 * i) * p.add_stride)) : make_float4(0.f, 0.f, 0.f, 0.f);
                 };
                 if (ADD) {
                     fetch(0);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                         if (4 * i + r0 < left && n < p.N) {
                             const size_t to = (size_t)(m0 + 4 * i + r0) * p.y_stride + n;
                             if (p.y_fp32) {
-                                *(float4 *)((float *)p.y + to) = v;
+                                __stcs((float4 *)((float *)p.y + to), v);
                             } else {
                                 const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
                                 *(uint2 *)((__nv_bfloat16 *)p.y + to) = make_uint2(*(const uint32_t *)&lo, *(const uint32_t *)&hi);

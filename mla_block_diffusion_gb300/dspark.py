@@ -446,11 +446,12 @@ _QLINEAR_WS = 1024
 
 def _qrows(name: str, codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QRowsStruct:
     """Quantised rows: codes [rows, k], scales fp32 [ceil(k / 128), rows]."""
-    if codes.dim() != 2 or codes.dtype not in _CODES or codes.get_device() != dev or not codes.is_contiguous():
+    shape = codes.shape
+    if len(shape) != 2 or codes.dtype not in _CODES or codes.get_device() != dev or not codes.is_contiguous():
         raise ValueError(f"{name}: codes are a contiguous uint8 or float8_e4m3fn tensor [rows, k] on cuda:{dev}")
-    rows, k = codes.shape
+    rows, k = shape
     blocks = (k + 127) // 128
-    if scales.dtype is not torch.float32 or scales.get_device() != dev or tuple(scales.shape) != (blocks, rows):
+    if scales.dtype is not torch.float32 or scales.get_device() != dev or scales.shape != (blocks, rows):
         raise ValueError(f"{name}: scales are an fp32 tensor [{blocks}, {rows}] on cuda:{dev}")
     stride, one = scales.stride()
     if rows > 1 and one != 1 or blocks > 1 and stride < rows:
@@ -459,16 +460,17 @@ def _qrows(name: str, codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QR
 
 
 def _qsource(name: str, x: torch.Tensor, shape, dev: int):
-    """Type and row stride of a matrix to be quantised."""
-    if tuple(x.shape) != tuple(shape) or x.get_device() != dev:
+    """Type and row stride of a matrix to be quantised, or of a product's result."""
+    if x.shape != shape or x.get_device() != dev:
         raise ValueError(f"{name}: tensor {list(shape)} on cuda:{dev}")
-    kind = 0 if x.dtype is torch.bfloat16 else 1
-    if kind and x.dtype is not torch.float32:
+    dtype = x.dtype
+    kind = 0 if dtype is torch.bfloat16 else 1
+    if kind and dtype is not torch.float32:
         raise ValueError(f"{name}: bf16 or fp32")
     stride, one = x.stride()
-    if one != 1 and x.shape[1] > 1:
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the elements of a row are contiguous")
-    return kind, stride if x.shape[0] > 1 else x.shape[1]  # torch leaves the stride of one row open
+    return kind, stride if shape[0] > 1 else shape[1]  # torch leaves the stride of one row open
 
 
 def quantise_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
