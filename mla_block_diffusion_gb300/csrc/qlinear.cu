@@ -74,30 +74,51 @@ __global__ void __launch_bounds__(kQrThreads, sizeof(T) == 2 ? 8 : 5) quantise_r
                                                                    uint8_t *__restrict__ codes, float *__restrict__ scales,
                                                                    long long s_stride) {
     const int tid = threadIdx.x, lane16 = tid & 15, half = tid >> 4;
-    const int across = ((K + kQlBlock - 1) / kQlBlock + 2 * PER - 1) / (2 * PER);  // CTAs side by side
-    const int row0 = (blockIdx.x / across) * kQrRows, first = (blockIdx.x % across) * (2 * PER);
-    const int r = row0 + (half & 7), b0 = first + (half >> 3);
+    const int row0 = blockIdx.x * kQrRows, first = blockIdx.y * (2 * PER);
+    const int r = row0 + (half & 7), k = (first + (half >> 3)) * kQlBlock + 8 * lane16;
+    const int left = r < M ? K - k : 0;  // elements from this thread's first to the row's end
     __shared__ float s_scale[2 * PER][kQrRows];
     pdl_trigger();
     pdl_wait();
+    const T *from = x + (long long)r * x_stride + k;
+    uint8_t *to = codes + (long long)r * K + k;
     Eight<T> v[PER];
+    uint32_t m[PER], all = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int k = (b0 + 2 * i) * kQlBlock + 8 * lane16;
-        if (r < M && k < K) v[i].load(x + (long long)r * x_stride + k);
+        if (2 * i * kQlBlock < left) v[i].load(from + 2 * i * kQlBlock);
         else v[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int k = (b0 + 2 * i) * kQlBlock + 8 * lane16;
-        uint32_t m = v[i].amax();
-        const bool bad = __any_sync(~0u, m >= kQlInf);
-        if (bad) m = v[i].amax_finite();
+        m[i] = v[i].amax();
+        all = max(all, m[i]);
+    }
+    const bool bad = __any_sync(~0u, all >= kQlInf);  // some are not finite
+    if (bad) {
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) m = max(m, __shfl_xor_sync(~0u, m, d));
-        const int e = ql_exponent(m);
-        if (r < M && k < K) *(uint2 *)(codes + (long long)r * K + k) = bad ? v[i].codes_nan(qc_pow2(-e)) : v[i].codes(qc_pow2(-e));
-        if (lane16 == 0) s_scale[(half >> 3) + 2 * i][half & 7] = qc_pow2(e);
+        for (int i = 0; i < PER; ++i) m[i] = v[i].amax_finite();
+    }
+    const uint32_t peers = 0xffffu << (tid & 16);
+    float scale[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int e = ql_exponent(__reduce_max_sync(peers, m[i]));
+        scale[i] = qc_pow2(e);
+        m[i] = (uint32_t)(127 - e) << 23;  // 2^-e
+    }
+    if (!bad) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (2 * i * kQlBlock < left) *(uint2 *)(to + 2 * i * kQlBlock) = v[i].codes(__uint_as_float(m[i]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (2 * i * kQlBlock < left) *(uint2 *)(to + 2 * i * kQlBlock) = v[i].codes_nan(__uint_as_float(m[i]));
+    }
+    if (lane16 == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s_scale[(half >> 3) + 2 * i][half & 7] = scale[i];
     }
     __syncthreads();
     if (tid < 2 * PER * kQrRows) {
@@ -153,9 +174,9 @@ static cudaError_t launch_rows(const void *x, long long stride, const dspark_qro
     const int kb = (o.k + kQlBlock - 1) / kQlBlock, rb = (o.rows + kQrRows - 1) / kQrRows;
     // four blocks a half-warp where that still leaves every SM a few CTAs, else one: more SMs share a short call
     if ((long long)rb * kb >= 64ll * sms)
-        return launch_pdl(quantise_rows_kernel<T, 4>, dim3((kb + 7) / 8 * rb), dim3(kQrThreads), 0, st, (const T *)x, stride,
+        return launch_pdl(quantise_rows_kernel<T, 4>, dim3(rb, (kb + 7) / 8), dim3(kQrThreads), 0, st, (const T *)x, stride,
                           o.rows, o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
-    return launch_pdl(quantise_rows_kernel<T, 1>, dim3((kb + 1) / 2 * rb), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
+    return launch_pdl(quantise_rows_kernel<T, 1>, dim3(rb, (kb + 1) / 2), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
                       o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
 }
 template <typename T>
