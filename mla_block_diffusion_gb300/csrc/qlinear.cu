@@ -172,9 +172,11 @@ __global__ void __launch_bounds__(kQwThreads, sizeof(T) == 2 ? 3 : 2)
 template <typename T>
 static cudaError_t launch_rows(const void *x, long long stride, const dspark_qrows_t &o, int sms, cudaStream_t st) {
     const int kb = (o.k + kQlBlock - 1) / kQlBlock, rb = (o.rows + kQrRows - 1) / kQrRows;
-    // four blocks a half-warp where that still leaves every SM a few CTAs, else one: more SMs share a short call
-    if ((long long)rb * kb >= 64ll * sms)
-        return launch_pdl(quantise_rows_kernel<T, 4>, dim3(rb, (kb + 7) / 8), dim3(kQrThreads), 0, st, (const T *)x, stride,
+    // Two blocks a half-warp for long calls of bf16, whose loads are half as long, else one. us, one against two, rows of
+    // 7168: bf16, 7 rows 1.4 and 1.6, 512 3.1 and 2.9, 1024 5.0 and 4.0, 4000 18.6 and 15.2 (four 15.9); fp32, 1024 7.3
+    // and 8.0, 4000 26.6 and 28.6.
+    if (sizeof(T) == 2 && (long long)rb * kb >= 20ll * sms)
+        return launch_pdl(quantise_rows_kernel<T, 2>, dim3(rb, (kb + 3) / 4), dim3(kQrThreads), 0, st, (const T *)x, stride,
                           o.rows, o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
     return launch_pdl(quantise_rows_kernel<T, 1>, dim3(rb, (kb + 1) / 2), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
                       o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
@@ -238,8 +240,9 @@ unsigned long long source_bytes(int type, int64_t stride, int rows, int k) {
     return ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4);
 }
 
-// Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes (64 rows: 12288 outputs x 576
-// 7.9 against 7.4 us, 14336 x 7168 24.7 against 28.1, 576 x 14336 9.0 against 31.0).
+// Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes. 64 rows, one against the
+// other, us: 12288 outputs x 576 inputs 5.4 and 9.3, 1808 x 720 6.1 and 7.1, 1024 x 512 4.9 and 6.3, 576 x 14336 9.2 and 33.1,
+// 14336 x 7168 21.2 and 30.2.
 dspark_status product(const QlParams &p, bool gated, const dspark_qrows_t *x, const dspark_qweight_t *w0,
                       const dspark_qweight_t *w1, cudaStream_t st) {
     const QlPlan plan = p.M <= 64 ? plan_qgemm_few(p, gated) : plan_qgemm(p, gated);
