@@ -21,7 +21,7 @@ namespace ds {
 constexpr int kQgSum0 = 4;                         // warps: loads, products, scales, none; then those that sum
 constexpr int kQgSums = 8, kQgWide = 512 / kQgSums;  // columns of either half that a warp sums
 constexpr int kQgThreads = 32 * (kQgSum0 + kQgSums);  // registers: 168 x 384 = 56 x 128 + 224 x 256
-constexpr int kQgRegsIssue = 56, kQgRegsSum = 224;
+constexpr int kQgRegsIssue = 56, kQgRegsSum = 224, kQgRegs = 168;
 constexpr int kQgBox = 128 * 128;                  // bytes: 128 rows or outputs x 128 k
 constexpr int kQgStages = 5;
 constexpr int kQgSlots = 2;                        // accumulators of 256 columns
@@ -37,7 +37,7 @@ struct QgBars {
     uint32_t issued;                               // stages that the producer has requested
     alignas(16) float x[2][kQgGroup][128];         // scales: rows'
     alignas(16) float2 w[2][kQgGroup];             // the two halves'
-    int8_t e[2][kQgSums / 4][128];                           // gated, tiles in turn: a row's scale exponent by column group
+    int8_t e[2][kQgSums / 4][128];                 // gated, tiles in turn: a row's scale exponent by column group
 };
 constexpr int kQgSmem = kQgStages * 2 * kQgBox + kQgOut + (int)sizeof(QgBars);
 static_assert(kQgSmem <= 232448, "shared memory");
@@ -76,7 +76,7 @@ DS_DEVINL void mma_commit_pair(uint64_t *bar) {
                  "h"((uint16_t)3)
                  : "memory");
 }
-// Without memory ordering at the pair's scope (that is a memory barrier, 1000 clocks a block): what the arrival
+// Without memory ordering at the pair's scope (that is a memory barrier in every block): what the arrival
 // publishes are reads of tensor memory, ordered by tcgen05.wait and the tcgen05 fences.
 DS_DEVINL void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -210,6 +210,8 @@ __global__ void __launch_bounds__(kQgThreads, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
+        __syncwarp();
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQgRegs));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQgRegsSum));
         const int q = warp & 3, h = (warp - kQgSum0) >> 2;  // lanes 32 q .., columns kQgWide h .. of each half
@@ -354,6 +356,9 @@ __global__ void __launch_bounds__(kQgThreads, 1)
                 }
             }
         }
+        // all warps leave with their share of the launch again
+        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQgRegs));
     }
     tc_fence_before();
     __syncthreads();
@@ -390,6 +395,8 @@ static QlPlan plan(const QlParams &p) {
     });
     if (r.error != cudaSuccess) return r;
     r.room = room(qgemm_kernel<GATED, HALVES, ADD>, 2, kQgThreads, kQgSmem);
+    // us a block of k, from whole calls. Tiles of 256 against 128 outputs: 2112 x 7168, 256 rows 28.8 and 20.2, 4000 rows 54.9
+    // and 65.7; 7168 x 14336, 512 rows 51.6 and 66.4; 12288 x 1536, 512 rows 20.3 and 18.2
     r.time = 4.f + (float)((r.tiles + r.room - 1) / r.room) * (1.f + p.KB * (HALVES == 2 ? 0.47f : 0.26f));
     return r;
 }

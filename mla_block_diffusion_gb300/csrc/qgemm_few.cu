@@ -9,7 +9,7 @@
 // global memory and a result does not depend on timing.
 //
 // Bound: HBM (one byte a weight), if a block of 128 k does not hold up the ring. Its sums
-// are a dependent chain (commit, wake, read, multiply, release) of some 400 to 800 clocks, so
+// are a dependent chain (commit, wake, read, multiply, release), so
 // four groups of four warps take blocks in turn (gated: two groups for each matrix), each
 // with accumulators of its own in tensor memory and sums of its own in registers, which are
 // added in order at the end.
@@ -22,7 +22,7 @@ namespace ds {
 
 constexpr int kQfSum0 = 4, kQfGroups = 4;                   // warps: loads, products, scales, none; then four groups of four that sum
 constexpr int kQfThreads = 32 * (kQfSum0 + 4 * kQfGroups);  // registers: 96 x 640 >= 56 x 128 + 104 x 512
-constexpr int kQfRegsIssue = 56, kQfRegsSum = 104;
+constexpr int kQfRegsIssue = 56, kQfRegsSum = 104, kQfRegs = 96;
 constexpr int kQfMaxStages = 12;
 constexpr int kQfMaxSplit = 8;                              // CTAs of a cluster
 constexpr int kQfWindow = 8, kQfWindows = 4;                // blocks of k whose scales arrive together, and such windows in shared memory
@@ -172,6 +172,8 @@ __global__ void __launch_bounds__(kQfThreads, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
+        __syncwarp();
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQfRegs));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQfRegsSum));
         const int q = warp & 3, group = (warp - kQfSum0) >> 2, mat = group / C::kTurns, turn = group % C::kTurns;
@@ -223,6 +225,9 @@ __global__ void __launch_bounds__(kQfThreads, 1)
 #pragma unroll
             for (int i = 0; i < NT; ++i) part[i * 128] = acc[i];
         }
+        // all warps finish the tile together, each with its share of the launch again
+        __syncwarp();
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQfRegs));
     }
     tc_fence_before();
     __syncthreads();
@@ -309,8 +314,11 @@ static QlPlan plan(const QlParams &p) {
         return cudaFuncSetAttribute(qgemm_few_kernel<NT, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (r.error != cudaSuccess) return r;
-    // the largest cluster that leaves all tiles on the device at once
-    for (int s = 2; s <= kQfMaxSplit && s <= p.KB; ++s)
+    // The largest cluster that leaves all tiles on the device at once and every CTA three blocks; none below 12 blocks, where
+    // the clusters' sum costs more than it saves. us, whole and in clusters, 1 and 64 rows: 1024 outputs x 512 inputs 3.2 and
+    // 4.9 against 3.8 and 6.2; x 1024 3.9 and 5.8 against (of two) 4.2 and 6.8; x 1536 4.7 and 6.6 against (of four) 3.9
+    // and 6.5; 576 x 14336 25.0 and 29.5 against (of eight) 6.6 and 9.2.
+    for (int s = 2; s <= kQfMaxSplit && p.KB >= 12 && s <= p.KB / 3; ++s)
         if (r.tiles <= room(qgemm_few_kernel<NT, GATED>, s, kQfThreads, C::kSmem)) r.split = s;
     return r;
 }

@@ -58,8 +58,7 @@ DS_DEVINL bool ql_elect() {
     return p != 0;
 }
 // A whole warp waits, and stays whole: every turn of the loop ends in a vote, on which all lanes leave it together. What
-// follows reads tensor memory, which takes the 32 lanes at once whatever lanes execute it: after a wait that lets lanes
-// go one by one, a warp that happened to be split there had registers overwritten, and went on with wild addresses.
+// follows reads tensor memory, whose instructions want all 32 lanes converged.
 DS_DEVINL bool ql_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
     unsigned long long t0 = 0;
     for (uint32_t i = 0;; ++i) {
@@ -76,7 +75,7 @@ DS_DEVINL bool ql_warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
     }
 }
 // 32 columns of the warp's lanes and the wait for them in one statement: apart, with the registers tied to the wait, each
-// costs a move, and the block's sums take as many issue slots as its products take clocks.
+// may cost a move.
 DS_DEVINL void tmem_ld32_now(uint32_t addr, float (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
@@ -132,12 +131,12 @@ class ClusterRoom {
     }
 };
 
-// How either kernel would divide a call and about how long that takes, in us.
+// How either kernel would divide a call.
 struct QlPlan {
     int split;           // few: CTAs that share a tile's blocks of k; many: 1 or 2 halves of 128 outputs a tile
     long long tiles;
-    int room;            // clusters on the device at once
-    float time;
+    int room;            // many: pairs on the device at once
+    float time;          // many: about how long, in us
     cudaError_t error;
 };
 QlPlan plan_qgemm(const QlParams &p, bool gated);
