@@ -13,6 +13,8 @@
 // four groups of four warps take blocks in turn (gated: two groups for each matrix), each
 // with accumulators of its own in tensor memory and sums of its own in registers, which are
 // added in order at the end.
+// Measured (graphs, weights in turn): one row, 35840 x 7168 42.5 us (6.0 TB/s), gated 7168 x 2 14336 34.5 (6.0 TB/s),
+// 7168 x 2112 7.4; 64 rows 47.1, 38.3 and 10.0.
 #include <math.h>
 
 #include "per_device.h"

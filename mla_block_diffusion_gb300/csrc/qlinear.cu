@@ -16,7 +16,7 @@ namespace ds {
 // one rounding since 2^-e is a power of two. Bound: HBM (2 or 4 bytes read and
 // one written per element). A CTA takes 8 rows x 2 PER blocks, each half-warp PER
 // blocks that it requests together; the scales of 8 rows are one full sector of
-// their [block, row] matrix.
+// their [block, row] matrix. Measured: 4000 x 7168 bf16 15.2 us in a graph, 16.9 through Python (5.1 TB/s), fp32 26.6.
 // ---------------------------------------------------------------------------
 constexpr int kQrThreads = 256, kQrRows = 8;
 
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(kQrThreads, sizeof(T) == 2 ? 8 : 5) quantise_r
 }
 
 // The same over blocks of 128 x 128, one CTA each; the block waits in registers for its maximum.
+// Bound: HBM; 7168 x 14336 bf16 55.8 us, 5.5 TB/s.
 constexpr int kQwThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kQwThreads, sizeof(T) == 2 ? 3 : 2)
