@@ -433,7 +433,8 @@ typedef struct {
  * over its finite elements (2^-100 if there are none but zeros), and the codes
  * are x / 2^e rounded to nearest even. NaN and infinities become the NaN code.
  * x [rows, k], x_type DSPARK_ENTRY_BF16 or _FP32; x_stride counts elements (a
- * multiple of 8 for bf16, 4 for fp32). x and the codes may not overlap. */
+ * multiple of 8 for bf16, 4 for fp32). x, the codes and the scales may not overlap. Here and
+ * below strides are at most 2^36. */
 dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_stride, const dspark_qrows_t *out, void *stream);
 
 /* (11) The same for weights [n, k] over blocks of 128 x 128. */

@@ -194,6 +194,8 @@ static cudaError_t launch_weight(const void *w, long long stride, const dspark_q
 namespace {
 
 bool ok16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
+// 2^24 rows of them, 4 bytes each, count within 64 bits; no memory holds two.
+constexpr int64_t kMaxStride = 1ll << 36;
 bool ok4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool ok_dim(int d) { return d >= 16 && d <= DSPARK_QLINEAR_MAX_DIM && d % 16 == 0; }
 
@@ -213,7 +215,7 @@ dspark_status done(cudaError_t e) {
 
 dspark_status check_rows(const dspark_qrows_t *x) {
     if (!x) return DSPARK_ERR_NULL;
-    if (x->rows < 0 || x->rows > DSPARK_QLINEAR_MAX_ROWS || !ok_dim(x->k) || x->scale_stride < x->rows) return DSPARK_ERR_SHAPE;
+    if (x->rows < 0 || x->rows > DSPARK_QLINEAR_MAX_ROWS || !ok_dim(x->k) || x->scale_stride < x->rows || x->scale_stride > kMaxStride) return DSPARK_ERR_SHAPE;
     if (x->rows == 0) return DSPARK_OK;
     if (!x->codes || !x->scales) return DSPARK_ERR_NULL;
     return ok16(x->codes) && ok4(x->scales) ? DSPARK_OK : DSPARK_ERR_ALIGN;
@@ -226,19 +228,31 @@ dspark_status check_weight(const dspark_qweight_t *w) {
 }
 dspark_status check_source(const void *x, int type, int64_t stride, int k) {
     if (type != DSPARK_ENTRY_BF16 && type != DSPARK_ENTRY_FP32) return DSPARK_ERR_UNSUPPORTED;
-    if (stride < k) return DSPARK_ERR_SHAPE;
+    if (stride < k || stride > kMaxStride) return DSPARK_ERR_SHAPE;
     if (!x) return DSPARK_ERR_NULL;
     return ok16(x) && stride % (type == DSPARK_ENTRY_BF16 ? 8 : 4) == 0 ? DSPARK_OK : DSPARK_ERR_ALIGN;
 }
 
-// Do [a, a + an) and [b, b + bn) share a byte?
-bool overlap(const void *a, unsigned long long an, const void *b, unsigned long long bn) {
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + bn && y < x + an;
+struct Range {
+    const void *at;
+    unsigned long long bytes;
+};
+bool overlap(const Range &a, const Range &b) {
+    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+    return x < y + b.bytes && y < x + a.bytes;
+}
+Range codes_of(const dspark_qrows_t &x) { return {x.codes, (unsigned long long)x.rows * x.k}; }
+Range codes_of(const dspark_qweight_t &w) { return {w.codes, (unsigned long long)w.n * w.k}; }
+unsigned long long blocks(int d) { return (d + kQlBlock - 1) / kQlBlock; }
+Range scales_of(const dspark_qrows_t &x) { return {x.scales, ((blocks(x.k) - 1) * (unsigned long long)x.scale_stride + x.rows) * 4}; }
+Range scales_of(const dspark_qweight_t &w) { return {w.scales, blocks(w.n) * blocks(w.k) * 4}; }
+template <typename T>
+bool overlaps(const Range &a, const T &x) {  // either part of x
+    return overlap(a, codes_of(x)) || overlap(a, scales_of(x));
 }
 
-unsigned long long source_bytes(int type, int64_t stride, int rows, int k) {
-    return ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4);
+Range source(const void *at, int type, int64_t stride, int rows, int k) {
+    return {at, ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4)};
 }
 
 // Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes. 64 rows, one against the
@@ -260,8 +274,7 @@ dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_strid
     if (s != DSPARK_OK || out->rows == 0) return s;
     s = check_source(x, x_type, x_stride, out->k);
     if (s != DSPARK_OK) return s;
-    if (overlap(out->codes, (unsigned long long)out->rows * out->k, x, source_bytes(x_type, x_stride, out->rows, out->k)))
-        return DSPARK_ERR_SHAPE;
+    if (overlaps(source(x, x_type, x_stride, out->rows, out->k), *out) || overlap(codes_of(*out), scales_of(*out))) return DSPARK_ERR_SHAPE;
     const int sms = current_sms();
     if (sms < 1) return DSPARK_ERR_CUDA;
     return done(x_type == DSPARK_ENTRY_BF16 ? launch_rows<__nv_bfloat16>(x, x_stride, *out, sms, (cudaStream_t)stream)
@@ -274,8 +287,7 @@ dspark_status dspark_qlinear_quantise_weight(const void *w, int w_type, int64_t 
     if (s != DSPARK_OK) return s;
     s = check_source(w, w_type, w_stride, out->k);
     if (s != DSPARK_OK) return s;
-    if (overlap(out->codes, (unsigned long long)out->n * out->k, w, source_bytes(w_type, w_stride, out->n, out->k)))
-        return DSPARK_ERR_SHAPE;
+    if (overlaps(source(w, w_type, w_stride, out->n, out->k), *out) || overlap(codes_of(*out), scales_of(*out))) return DSPARK_ERR_SHAPE;
     return done(w_type == DSPARK_ENTRY_BF16 ? launch_weight<__nv_bfloat16>(w, w_stride, *out, (cudaStream_t)stream)
                                             : launch_weight<float>(w, w_stride, *out, (cudaStream_t)stream));
 }
@@ -286,24 +298,24 @@ dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweigh
     if (s == DSPARK_OK) s = check_weight(w);
     if (s != DSPARK_OK) return s;
     if (y_type != DSPARK_ENTRY_BF16 && y_type != DSPARK_ENTRY_FP32) return DSPARK_ERR_UNSUPPORTED;
-    if (x->k != w->k || y_stride < w->n || (add && add_stride < w->n)) return DSPARK_ERR_SHAPE;
+    if (x->k != w->k || y_stride < w->n || y_stride > kMaxStride || (add && (add_stride < w->n || add_stride > kMaxStride)))
+        return DSPARK_ERR_SHAPE;
     if (!ws || ws_bytes < DSPARK_QLINEAR_WS_BYTES) return DSPARK_ERR_WORKSPACE;
     if (!ok16(ws)) return DSPARK_ERR_ALIGN;
     if (x->rows == 0) return DSPARK_OK;
     if (!y) return DSPARK_ERR_NULL;
     if (!ok16(y) || !ok16(add) || y_stride % (y_type == DSPARK_ENTRY_BF16 ? 8 : 4) || (add && add_stride % 4)) return DSPARK_ERR_ALIGN;
-    const unsigned long long rows = (unsigned long long)x->rows;
-    const unsigned long long y_bytes = ((rows - 1) * (unsigned long long)y_stride + w->n) * (y_type == DSPARK_ENTRY_BF16 ? 2 : 4);
-    if (overlap(y, y_bytes, x->codes, rows * x->k)) return DSPARK_ERR_SHAPE;
+    const Range out = source(y, y_type, y_stride, x->rows, w->n);
+    if (overlaps(out, *x) || overlaps(out, *w)) return DSPARK_ERR_SHAPE;
     // the residual may be y itself, element for element, and nothing else that overlaps it
     if (add && !((const void *)add == y && y_type == DSPARK_ENTRY_FP32 && add_stride == y_stride) &&
-        overlap(y, y_bytes, add, ((rows - 1) * (unsigned long long)add_stride + w->n) * 4))
+        overlap(out, source(add, DSPARK_ENTRY_FP32, add_stride, x->rows, w->n)))
         return DSPARK_ERR_SHAPE;
     QlParams p;
     memset(&p, 0, sizeof(p));
     p.M = x->rows;
     p.N = w->n;
-    p.KB = (x->k + kQlBlock - 1) / kQlBlock;
+    p.KB = (int)blocks(x->k);
     p.sx = x->scales;
     p.sx_stride = x->scale_stride;
     p.sw[0] = p.sw[1] = w->scales;
@@ -327,17 +339,15 @@ dspark_status dspark_qlinear_gated(const dspark_qrows_t *x, const dspark_qweight
     if (!ws || ws_bytes < DSPARK_QLINEAR_WS_BYTES) return DSPARK_ERR_WORKSPACE;
     if (!ok16(ws)) return DSPARK_ERR_ALIGN;
     if (x->rows == 0) return DSPARK_OK;
-    const unsigned long long rows = (unsigned long long)x->rows;
-    const unsigned long long kb = (x->k + kQlBlock - 1) / kQlBlock, hb = (h->k + kQlBlock - 1) / kQlBlock;
-    const unsigned long long sx_bytes = ((kb - 1) * (unsigned long long)x->scale_stride + rows) * 4;
-    const unsigned long long sh_bytes = ((hb - 1) * (unsigned long long)h->scale_stride + rows) * 4;
-    if (overlap(h->codes, rows * h->k, x->codes, rows * x->k) || overlap(h->scales, sh_bytes, x->scales, sx_bytes))
+    const Range hc = codes_of(*h), hs = scales_of(*h);
+    if (overlap(hc, hs) || overlaps(hc, *x) || overlaps(hs, *x) || overlaps(hc, *gate) || overlaps(hs, *gate) || overlaps(hc, *up) ||
+        overlaps(hs, *up))
         return DSPARK_ERR_SHAPE;
     QlParams p;
     memset(&p, 0, sizeof(p));
     p.M = x->rows;
     p.N = gate->n;
-    p.KB = (int)kb;
+    p.KB = (int)blocks(x->k);
     p.sx = x->scales;
     p.sx_stride = x->scale_stride;
     p.sw[0] = gate->scales;

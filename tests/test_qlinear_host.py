@@ -265,3 +265,32 @@ def test_binding_refuses_another_device(reach):
     with pytest.raises(ValueError):
         M.quantise_rows(Stand(7, 512, dtype=BF), Stand(7, 512), Stand(4, 7, dtype=F32))
     assert lib.calls == 0
+
+
+WIDE = 1 << 41  # elements from one row to the next: byte counts of such a matrix do not fit 64 bits at 2^24 rows
+
+
+def test_results_overlap_nothing(L):
+    end = 7 * 512 - 16  # the last 16 bytes of the rows' codes
+    # quantisers: scales over the source, over the codes
+    assert L.dspark_qlinear_quantise(P(1), BF16, 512, C.byref(rows()), None) == SHAPE
+    assert L.dspark_qlinear_quantise(P(9), BF16, 512, C.byref(rows(scales=P(0) + end)), None) == SHAPE
+    assert L.dspark_qlinear_quantise_weight(P(3), BF16, 512, C.byref(weight()), None) == SHAPE
+    assert L.dspark_qlinear_quantise_weight(P(9), BF16, 512, C.byref(weight(scales=P(2) + 64)), None) == SHAPE
+    # products: over the rows' scales, the weights' codes and scales
+    for y in (P(1), P(2), P(2) + 272 * 512 - 16, P(3)):
+        assert matmul(L, y=y) == SHAPE
+    # gated: h's codes or scales over any input, or over each other
+    for at in (P(0), P(1), P(2), P(3), P(8), P(2) + 272 * 512 - 16):
+        assert gated(L, h=rows(k=272, codes=at, scales=P(11))) == SHAPE
+        assert gated(L, h=rows(k=272, codes=P(10), scales=at)) == SHAPE
+    assert gated(L, h=rows(k=272, codes=P(10), scales=P(10) + 64)) == SHAPE
+
+
+def test_strides_beyond_any_memory(L):
+    assert matmul(L, stride=WIDE) == SHAPE
+    assert matmul(L, add=P(7), add_stride=WIDE) == SHAPE
+    assert matmul(L, r=rows(scale_stride=WIDE)) == SHAPE
+    assert L.dspark_qlinear_quantise(P(9), BF16, WIDE, C.byref(rows()), None) == SHAPE
+    assert L.dspark_qlinear_quantise_weight(P(9), FP32, WIDE, C.byref(weight()), None) == SHAPE
+    assert gated(L, h=rows(k=272, codes=P(10), scales=P(11), scale_stride=WIDE)) == SHAPE
