@@ -212,3 +212,65 @@ def test_gated(m, n, k):
     got = O.rows_values(host(hc[:m]), scales)
     # half a step: 2^-4 of the value, and 2^-10 scales below the normal numbers
     assert (np.abs(got - want) <= off + np.maximum((np.abs(want) + off) * 2.0 ** -4, s * 2.0 ** -10)).all()
+
+
+# 11 blocks of k stay whole; 12 and more are shared by clusters, not evenly where they are no multiple, the last block short
+SHARED = [(16, 1408), (144, 1424), (144, 1536), (272, 1552), (1040, 2064), (2112, 3600), (576, 14336)]
+
+
+@pytest.mark.parametrize("m", [1, 2, 16, 31, 64])
+@pytest.mark.parametrize("n,k", SHARED)
+@pytest.mark.parametrize("out", ["bf16", "add"])
+def test_matmul_of_shared_blocks(m, n, k, out):
+    test_matmul(m, n, k, out)
+
+
+@pytest.mark.parametrize("m", [1, 17, 64])
+@pytest.mark.parametrize("n,k", SHARED)
+def test_gated_of_shared_blocks(m, n, k):
+    test_gated(m, n, k)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,k", [(430, 7168), (435, 7184), (3001, 1040), (6001, 528)])
+def test_quantise_rows_of_long_calls(m, k, dtype):
+    """Either number of blocks a half-warp, around the border between them; blocks that are no multiple of it."""
+    test_quantise_rows(m, k, dtype)
+
+
+@pytest.mark.parametrize("m", [5, 64, 300])
+def test_two_streams_and_two_graphs_of_one_workspace(m):
+    """Calls on two streams, and two graphs replayed at once, that share an error word and weights."""
+    rng = np.random.default_rng(m)
+    n, k = 1040, 2064
+    x, sx = (dev(a) for a in rows_of(rng, m, k))
+    a = M.QLinear(*(dev(v) for v in weight_of(rng, n, k)))
+    b = M.QLinear(*(dev(v) for v in weight_of(rng, n, k)), workspace=a.ws)
+    want = [torch.empty(m, n, device="cuda") for _ in range(2)]
+    a.matmul(x, sx, want[0])
+    b.matmul(x, sx, want[1])
+    torch.cuda.synchronize()
+    ys = [torch.zeros(m, n, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lin, y, s in zip((a, b), ys, streams):
+            with torch.cuda.stream(s):
+                lin.matmul(x, sx, y)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in zip(ys, want))
+    graphs = []
+    for lin, y in zip((a, b), ys):
+        y.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            lin.matmul(x, sx, y)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in zip(ys, want))
+    assert a.check() == 0

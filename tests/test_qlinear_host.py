@@ -68,7 +68,7 @@ BAD_WEIGHT = [(dict(n=0), SHAPE), (dict(n=264), SHAPE), (dict(n=-16), SHAPE), (d
 @pytest.mark.parametrize("kw,status", BAD_ROWS + [(dict(x=None), NULL), (dict(x=P(9) + 2), ALIGN), (dict(kind=2), UNSUPPORTED),
                                                   (dict(kind=-1), UNSUPPORTED), (dict(stride=511), SHAPE), (dict(stride=516), ALIGN),
                                                   (dict(kind=FP32, stride=514), ALIGN), (dict(x=P(0)), SHAPE),
-                                                  (dict(x=P(0) + 3072 - 16), SHAPE)])
+                                                  (dict(x=P(0) + 7 * 512 - 16), SHAPE)])
 def test_quantise_refusals(L, kw, status):
     a = dict(x=P(9), kind=BF16, stride=512)
     a |= {k: v for k, v in kw.items() if k in a}
