@@ -405,7 +405,8 @@ dspark_status dspark_qcache_check(void *ws, void *stream);
  * Weights: element [n, k] stands for codes[n, k] * scales[n / 128, k / 128]. Scales
  * are any fp32 numbers; those that the quantisers write are powers of two. An
  * E4M3 NaN makes every output that it enters NaN. n and k are multiples of 16 up
- * to DSPARK_QLINEAR_MAX_DIM; the last block of an edge may be shorter than 128.
+ * to DSPARK_QLINEAR_MAX_DIM (dspark_qlinear_quantise_matrix: any n); the last block
+ * of an edge may be shorter than 128.
  * No handle is needed. The products' workspace is an error word (16-byte
  * aligned, zero-filled once, DSPARK_QLINEAR_WS_BYTES), read with
  * dspark_qcache_check(); concurrent calls may share one. The calls read no other
@@ -440,6 +441,12 @@ dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_strid
 /* (11) The same for weights [n, k] over blocks of 128 x 128. */
 dspark_status dspark_qlinear_quantise_weight(const void *w, int w_type, int64_t w_stride, const dspark_qweight_t *out,
                                              void *stream);
+
+/* The same for a matrix of any number of rows, n = 1..DSPARK_QLINEAR_MAX_DIM: codes [n, k],
+ * scales [ceil(n / 128), ceil(k / 128)], as in dspark_qweight_t. The products take n in multiples
+ * of 16 only: rows of zero codes behind the last one make such a matrix of any other. */
+dspark_status dspark_qlinear_quantise_matrix(const void *w, int w_type, int64_t w_stride, int n, int k, void *codes,
+                                             float *scales, void *stream);
 
 /* (12) y = x w^T (+ add): for every block of 128 k the products of the codes are
  * summed in fp32 and enter an fp32 sum times sx * sw (one fp32 product of the two

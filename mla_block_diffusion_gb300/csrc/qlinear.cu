@@ -226,6 +226,12 @@ dspark_status check_weight(const dspark_qweight_t *w) {
     if (!w->codes || !w->scales) return DSPARK_ERR_NULL;
     return ok16(w->codes) && ok4(w->scales) ? DSPARK_OK : DSPARK_ERR_ALIGN;
 }
+// A matrix that the quantiser writes: any number of rows.
+dspark_status check_matrix(const dspark_qweight_t &w) {
+    if (w.n < 1 || w.n > DSPARK_QLINEAR_MAX_DIM || !ok_dim(w.k)) return DSPARK_ERR_SHAPE;
+    if (!w.codes || !w.scales) return DSPARK_ERR_NULL;
+    return ok16(w.codes) && ok4(w.scales) ? DSPARK_OK : DSPARK_ERR_ALIGN;
+}
 dspark_status check_source(const void *x, int type, int64_t stride, int k) {
     if (type != DSPARK_ENTRY_BF16 && type != DSPARK_ENTRY_FP32) return DSPARK_ERR_UNSUPPORTED;
     if (stride < k || stride > kMaxStride) return DSPARK_ERR_SHAPE;
@@ -253,6 +259,14 @@ bool overlaps(const Range &a, const T &x) {  // either part of x
 
 Range source(const void *at, int type, int64_t stride, int rows, int k) {
     return {at, ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4)};
+}
+
+dspark_status quantise_matrix(const void *w, int type, int64_t stride, const dspark_qweight_t &out, cudaStream_t st) {
+    dspark_status s = check_matrix(out);
+    if (s == DSPARK_OK) s = check_source(w, type, stride, out.k);
+    if (s != DSPARK_OK) return s;
+    if (overlaps(source(w, type, stride, out.n, out.k), out) || overlap(codes_of(out), scales_of(out))) return DSPARK_ERR_SHAPE;
+    return done(type == DSPARK_ENTRY_BF16 ? launch_weight<__nv_bfloat16>(w, stride, out, st) : launch_weight<float>(w, stride, out, st));
 }
 
 // Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes. 64 rows, one against the
@@ -283,13 +297,13 @@ dspark_status dspark_qlinear_quantise(const void *x, int x_type, int64_t x_strid
 
 dspark_status dspark_qlinear_quantise_weight(const void *w, int w_type, int64_t w_stride, const dspark_qweight_t *out,
                                              void *stream) {
-    dspark_status s = check_weight(out);
-    if (s != DSPARK_OK) return s;
-    s = check_source(w, w_type, w_stride, out->k);
-    if (s != DSPARK_OK) return s;
-    if (overlaps(source(w, w_type, w_stride, out->n, out->k), *out) || overlap(codes_of(*out), scales_of(*out))) return DSPARK_ERR_SHAPE;
-    return done(w_type == DSPARK_ENTRY_BF16 ? launch_weight<__nv_bfloat16>(w, w_stride, *out, (cudaStream_t)stream)
-                                            : launch_weight<float>(w, w_stride, *out, (cudaStream_t)stream));
+    const dspark_status s = check_weight(out);
+    return s == DSPARK_OK ? quantise_matrix(w, w_type, w_stride, *out, (cudaStream_t)stream) : s;
+}
+
+dspark_status dspark_qlinear_quantise_matrix(const void *w, int w_type, int64_t w_stride, int n, int k, void *codes, float *scales,
+                                             void *stream) {
+    return quantise_matrix(w, w_type, w_stride, dspark_qweight_t{n, k, codes, scales}, (cudaStream_t)stream);
 }
 
 dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweight_t *w, const float *add, int64_t add_stride,

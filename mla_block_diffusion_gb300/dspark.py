@@ -25,7 +25,7 @@ EXPORTS = ("dspark_create", "dspark_destroy", "dspark_workspace_bytes", "dspark_
            "dspark_markov_rollout", "dspark_confidence", "dspark_verify", "dspark_check", "dspark_status_str",
            "dspark_fuse_ctx_noalloc", "dspark_kv_append", "dspark_qcache_plan", "dspark_qcache_append",
            "dspark_qcache_attend", "dspark_qcache_workspace_bytes", "dspark_qcache_check", "dspark_qlinear_quantise",
-           "dspark_qlinear_quantise_weight", "dspark_qlinear_matmul", "dspark_qlinear_gated")
+           "dspark_qlinear_quantise_weight", "dspark_qlinear_quantise_matrix", "dspark_qlinear_matmul", "dspark_qlinear_gated")
 
 
 class Geom(C.Structure):
@@ -124,6 +124,7 @@ def lib():
         L.dspark_qcache_check.argtypes = [vp, vp]
         L.dspark_qlinear_quantise.argtypes = [vp, i, C.c_int64, C.POINTER(QRowsStruct), vp]
         L.dspark_qlinear_quantise_weight.argtypes = [vp, i, C.c_int64, C.POINTER(QWeightStruct), vp]
+        L.dspark_qlinear_quantise_matrix.argtypes = [vp, i, C.c_int64, i, i, vp, vp, vp]
         L.dspark_qlinear_matmul.argtypes = [C.POINTER(QRowsStruct), C.POINTER(QWeightStruct), vp, C.c_int64, vp, i, C.c_int64, vp,
                                             sz, vp]
         L.dspark_qlinear_gated.argtypes = [C.POINTER(QRowsStruct), C.POINTER(QWeightStruct), C.POINTER(QWeightStruct),
@@ -486,13 +487,13 @@ def quantise_rows(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
 
 def quantise_weight(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
     """w [n, k] (bf16 or fp32, any row stride) into E4M3 codes [n, k] and scales fp32 [ceil(n / 128), ceil(k / 128)], one
-    power of two per block of 128 x 128; n and k are multiples of 16."""
+    power of two per block of 128 x 128; k is a multiple of 16, n any number (a product's: a multiple of 16)."""
     dev = torch._C._cuda_getDevice()
     a = _qweight(codes, scales, dev)
     kind, stride = _qsource("w", w, codes.shape, dev)
-    st = lib().dspark_qlinear_quantise_weight(w.data_ptr() or None, kind, stride, C.byref(a), _stream())
+    st = lib().dspark_qlinear_quantise_matrix(w.data_ptr() or None, kind, stride, a.n, a.k, a.codes, a.scales, _stream())
     if st:
-        raise DSparkError("dspark_qlinear_quantise_weight", st)
+        raise DSparkError("dspark_qlinear_quantise_matrix", st)
 
 
 def _qweight(codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QWeightStruct:
