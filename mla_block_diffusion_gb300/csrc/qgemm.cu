@@ -215,7 +215,11 @@ __global__ void __launch_bounds__(kQgThreads, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
+        // Registers are taken back behind the barrier, before which the summing warps have given theirs up: a warp that is done
+        // at once (one has nothing to do) could otherwise take again what they have not got yet, and nothing would end their wait.
         __syncwarp();
+        tc_fence_before();
+        named_bar_sync(6, kQgThreads);
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQgRegs));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQgRegsSum));
@@ -364,9 +368,9 @@ __global__ void __launch_bounds__(kQgThreads, 1)
         // all warps leave with their share of the launch again
         __syncwarp();
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQgRegs));
+        tc_fence_before();
+        named_bar_sync(6, kQgThreads);
     }
-    tc_fence_before();
-    __syncthreads();
     if (tid == 0) {
         // Every arrival that the products' commits, or the other CTA's warps, send to this CTA has come: one that is still on
         // its way when the CTA has left would land in memory that is no longer its own.

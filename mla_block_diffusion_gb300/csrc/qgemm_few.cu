@@ -174,7 +174,11 @@ __global__ void __launch_bounds__(kQfThreads, 1)
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
+        // Registers are taken back behind the barrier, before which the summing warps have given theirs up: a warp that is done
+        // at once (one has nothing to do) could otherwise take again what they have not got yet, and nothing would end their wait.
         __syncwarp();
+        tc_fence_before();
+        named_bar_sync(6, kQfThreads);
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQfRegs));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kQfRegsSum));
@@ -230,9 +234,9 @@ __global__ void __launch_bounds__(kQfThreads, 1)
         // all warps finish the tile together, each with its share of the launch again
         __syncwarp();
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kQfRegs));
+        tc_fence_before();
+        named_bar_sync(6, kQfThreads);
     }
-    tc_fence_before();
-    __syncthreads();
     // four outputs of a row: of this CTA's groups, added in order
     auto own = [&](int mat, int row, int c) {
         const float *at = (const float *)qf_smem + (mat * C::kTurns * NT + row) * 128 + c;

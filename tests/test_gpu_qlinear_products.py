@@ -1,0 +1,50 @@
+"""Products and gated products of quantised rows: CTAs that leave and come."""
+import numpy as np
+import pytest
+import torch
+
+import mla_block_diffusion_gb300 as M
+from tests.test_gpu_qlinear import dev, rows_of, weight_of
+
+pytestmark = pytest.mark.gpu
+
+
+def blocks(n):
+    return -(-n // 128)
+
+
+@pytest.mark.parametrize("kb", [1, 4, 5, 6, 11, 12, 13, 25])
+def test_kernels_that_follow_one_another(kb):
+    """Every kernel has its barriers in another place of shared memory, and the next one's CTAs come as soon as one has left:
+    rings that are not filled, just filled and filled again, results bit for bit those of calls that are waited for."""
+    rng = np.random.default_rng(kb)
+    k, n = 128 * kb - 16, 4112
+    gate, up = (M.QLinear(*(dev(a) for a in weight_of(rng, n, k))) for _ in range(2))
+    gated = M.QGated(gate, up)
+    calls, outs = [], []
+    for m in (1, 64, 17, 65, 32, 5):
+        x = [dev(a) for a in rows_of(rng, m, k)]
+        y = torch.zeros(m, n, device="cuda")
+        h = torch.zeros(m, n, dtype=torch.uint8, device="cuda"), torch.zeros(blocks(n), m, device="cuda")
+        calls += [lambda x=x, y=y: gate.matmul(*x, y), lambda x=x, h=h: gated.forward(*x, *h)]
+        outs += [y, *h]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    for t in outs:
+        t.zero_()
+    for _ in range(20):
+        for call in calls:
+            call()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    for t in outs:
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in calls[::-1]:
+            call()
+    for _ in range(20):
+        g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert gate.check() == 0
