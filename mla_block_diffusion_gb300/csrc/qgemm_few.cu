@@ -136,7 +136,8 @@ __global__ void __launch_bounds__(kQfThreads, 1)
             if (ql_elect()) {
                 const uint32_t lo = sdesc_lo(smem_u32(qf_smem));
                 constexpr uint32_t hi = sdesc_hi(1024, 2), id = idesc_e4m3_f32(128, NT);
-                for (int u = 0; u < KB; ++u) {
+                int u = 0;
+                for (; u < KB; ++u) {
                     const uint32_t s = u % C::kStages, slot = u % C::kSlots;
                     if (!mbar_wait_bounded(&ms.full[s], (u / C::kStages) & 1, abort)) break;
                     if (u >= C::kSlots && !mbar_wait_bounded(&ms.aempty[slot], ((u / C::kSlots) & 1) ^ 1, abort)) break;
@@ -148,11 +149,17 @@ __global__ void __launch_bounds__(kQfThreads, 1)
                         for (int k = 0; k < 4; ++k)
                             mma_e4m3(tmem + (slot * C::kMats + i) * NT, (uint64_t)hi << 32 | (w + i * 1024 + 2 * k), (uint64_t)hi << 32 | (x + 2 * k), id,
                                      k > 0);
-                    mma_commit(&ms.empty[s]);
+                    // Only of a stage that is filled again, for which the producer waits: an arrival that is still on its way
+                    // when the CTA has left would land in memory that is no longer its own.
+                    if (u + C::kStages < KB) mma_commit(&ms.empty[s]);
                     mma_commit(&ms.afull[slot]);
                 }
                 mma_commit(&ms.done);
                 ql_drain(&ms.done, 0);
+                if (u < KB) {  // given up: the others may no longer wait for what was sent
+                    for (int v = max(0, u - C::kStages); v < min(u, KB - C::kStages); ++v) ql_drain(&ms.empty[v % C::kStages], (v / C::kStages) & 1);
+                    for (int v = max(0, u - C::kSlots); v < u; ++v) ql_drain(&ms.afull[v % C::kSlots], (v / C::kSlots) & 1);
+                }
             }
             __syncwarp();
         } else if (warp == 2) {

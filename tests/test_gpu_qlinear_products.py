@@ -48,3 +48,35 @@ def test_kernels_that_follow_one_another(kb):
         g.replay()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert gate.check() == 0
+
+
+@pytest.mark.parametrize("m", [16, 32, 64])
+def test_rings_around_their_length(m):
+    """Few rows, up to 26 blocks of k: rings of 5 to 11 stages that are not filled, just filled, and filled again once and twice;
+    the kernels lie close behind one another, and nothing of one may arrive in the next."""
+    rng = np.random.default_rng(m)
+    n, calls, outs = 272, [], []
+    for kb in range(1, 27):
+        k = 128 * kb
+        gate, up = (M.QLinear(*(dev(a) for a in weight_of(rng, n, k))) for _ in range(2))
+        x = [dev(a) for a in rows_of(rng, m, k)]
+        y = torch.zeros(m, n, device="cuda")
+        h = torch.zeros(m, n, dtype=torch.uint8, device="cuda"), torch.zeros(blocks(n), m, device="cuda")
+        calls += [lambda a=gate, x=x, y=y: a.matmul(*x, y), lambda a=M.QGated(gate, up), x=x, h=h: a.forward(*x, *h)]
+        outs += [y, *h]
+    for call in calls:
+        call()
+        torch.cuda.synchronize()
+    want = [t.clone() for t in outs]
+    for t in outs:
+        t.zero_()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for call in calls:
+            call()
+        for call in calls[::-1]:
+            call()
+    for _ in range(30):
+        g.replay()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert gate.check() == 0
