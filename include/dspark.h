@@ -462,6 +462,8 @@ dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweigh
  * silu(g) = g / (1 + exp(-g)), quantised as rows (call 10) straight from the fp32
  * sums; the second half is dspark_qlinear_matmul. gate and up have one shape; h is
  * [rows, n] and overlaps no input. Values that are not finite become NaN codes.
+ * Beside what the fp32 sums are off by, a value is off by less than 2^-15 of itself
+ * (fast exponential and division) before its rounding to a code.
  * Device errors: DSPARK_ERR_TIMEOUT. */
 dspark_status dspark_qlinear_gated(const dspark_qrows_t *x, const dspark_qweight_t *gate, const dspark_qweight_t *up,
                                    const dspark_qrows_t *h, void *ws, size_t ws_bytes, void *stream);
