@@ -407,6 +407,10 @@ dspark_status dspark_qcache_check(void *ws, void *stream);
  * E4M3 NaN makes every output that it enters NaN. n and k are multiples of 16 up
  * to DSPARK_QLINEAR_MAX_DIM (dspark_qlinear_quantise_matrix: any n); the last block
  * of an edge may be shorter than 128.
+ * Results overlap no input and no other result of the call (one exception at call 12):
+ * no byte is in both. Columns of one buffer do not overlap where their rows are equally
+ * far apart in bytes; of strided matrices whose rows are not, the bytes between the
+ * rows count as well.
  * No handle is needed. The products' workspace is an error word (16-byte
  * aligned, zero-filled once, DSPARK_QLINEAR_WS_BYTES), read with
  * dspark_qcache_check(); concurrent calls may share one. The calls read no other

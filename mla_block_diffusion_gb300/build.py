@@ -11,7 +11,7 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdspark.so")
 SOURCES = ["api.cu", "layers.cu", "attn_tc.cu", "sampling.cu", "verify.cu", "noalloc.cu", "qcache.cu", "qattn.cu", "qattn_tc.cu",
            "qlinear.cu", "qgemm.cu", "qgemm_few.cu"]
-HEADERS = ["common.cuh", "gemm.cuh", "gemm_q.cuh", "gemm_f8.cuh", "internal.h", "sampling_spec.cuh", "exact_div.cuh", "e4m3.cuh", "per_device.h", "qcache.h", "qattn.cuh", "qlinear.h",
+HEADERS = ["common.cuh", "gemm.cuh", "gemm_q.cuh", "gemm_f8.cuh", "internal.h", "sampling_spec.cuh", "exact_div.cuh", "e4m3.cuh", "per_device.h", "qcache.h", "qattn.cuh", "qlinear.h", "overlap.h",
            os.path.join("..", "..", "include", "dspark.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

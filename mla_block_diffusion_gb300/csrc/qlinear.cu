@@ -3,6 +3,7 @@
 #include <math.h>
 #include <string.h>
 
+#include "overlap.h"
 #include "qlinear.h"
 
 using namespace ds;
@@ -239,26 +240,19 @@ dspark_status check_source(const void *x, int type, int64_t stride, int k) {
     return ok16(x) && stride % (type == DSPARK_ENTRY_BF16 ? 8 : 4) == 0 ? DSPARK_OK : DSPARK_ERR_ALIGN;
 }
 
-struct Range {
-    const void *at;
-    unsigned long long bytes;
-};
-bool overlap(const Range &a, const Range &b) {
-    const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
-    return x < y + b.bytes && y < x + a.bytes;
-}
-Range codes_of(const dspark_qrows_t &x) { return {x.codes, (unsigned long long)x.rows * x.k}; }
-Range codes_of(const dspark_qweight_t &w) { return {w.codes, (unsigned long long)w.n * w.k}; }
+Span codes_of(const dspark_qrows_t &x) { return {x.codes, (unsigned)x.k, (unsigned)x.k, (unsigned)x.rows}; }
+Span codes_of(const dspark_qweight_t &w) { return {w.codes, (unsigned)w.k, (unsigned)w.k, (unsigned)w.n}; }
 unsigned long long blocks(int d) { return (d + kQlBlock - 1) / kQlBlock; }
-Range scales_of(const dspark_qrows_t &x) { return {x.scales, ((blocks(x.k) - 1) * (unsigned long long)x.scale_stride + x.rows) * 4}; }
-Range scales_of(const dspark_qweight_t &w) { return {w.scales, blocks(w.n) * blocks(w.k) * 4}; }
+Span scales_of(const dspark_qrows_t &x) { return {x.scales, 4ull * x.rows, 4ull * x.scale_stride, blocks(x.k)}; }
+Span scales_of(const dspark_qweight_t &w) { return {w.scales, 4 * blocks(w.k), 4 * blocks(w.k), blocks(w.n)}; }
 template <typename T>
-bool overlaps(const Range &a, const T &x) {  // either part of x
+bool overlaps(const Span &a, const T &x) {  // either part of x
     return overlap(a, codes_of(x)) || overlap(a, scales_of(x));
 }
 
-Range source(const void *at, int type, int64_t stride, int rows, int k) {
-    return {at, ((unsigned long long)(rows - 1) * stride + k) * (type == DSPARK_ENTRY_BF16 ? 2 : 4)};
+Span source(const void *at, int type, int64_t stride, int rows, int k) {
+    const unsigned long long size = type == DSPARK_ENTRY_BF16 ? 2 : 4;
+    return {at, k * size, stride * size, (unsigned)rows};
 }
 
 dspark_status quantise_matrix(const void *w, int type, int64_t stride, const dspark_qweight_t &out, cudaStream_t st) {
@@ -319,7 +313,7 @@ dspark_status dspark_qlinear_matmul(const dspark_qrows_t *x, const dspark_qweigh
     if (x->rows == 0) return DSPARK_OK;
     if (!y) return DSPARK_ERR_NULL;
     if (!ok16(y) || !ok16(add) || y_stride % (y_type == DSPARK_ENTRY_BF16 ? 8 : 4) || (add && add_stride % 4)) return DSPARK_ERR_ALIGN;
-    const Range out = source(y, y_type, y_stride, x->rows, w->n);
+    const Span out = source(y, y_type, y_stride, x->rows, w->n);
     if (overlaps(out, *x) || overlaps(out, *w)) return DSPARK_ERR_SHAPE;
     // the residual may be y itself, element for element, and nothing else that overlaps it
     if (add && !((const void *)add == y && y_type == DSPARK_ENTRY_FP32 && add_stride == y_stride) &&
@@ -353,7 +347,7 @@ dspark_status dspark_qlinear_gated(const dspark_qrows_t *x, const dspark_qweight
     if (!ws || ws_bytes < DSPARK_QLINEAR_WS_BYTES) return DSPARK_ERR_WORKSPACE;
     if (!ok16(ws)) return DSPARK_ERR_ALIGN;
     if (x->rows == 0) return DSPARK_OK;
-    const Range hc = codes_of(*h), hs = scales_of(*h);
+    const Span hc = codes_of(*h), hs = scales_of(*h);
     if (overlap(hc, hs) || overlaps(hc, *x) || overlaps(hs, *x) || overlaps(hc, *gate) || overlaps(hs, *gate) || overlaps(hc, *up) ||
         overlaps(hs, *up))
         return DSPARK_ERR_SHAPE;

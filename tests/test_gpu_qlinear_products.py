@@ -80,3 +80,39 @@ def test_rings_around_their_length(m):
         g.replay()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
     assert gate.check() == 0
+
+
+@pytest.mark.parametrize("m", [1, 7, 64, 65, 300])
+@pytest.mark.parametrize("n,k", [(272, 528), (2112, 1552)])
+def test_columns_of_one_buffer(m, n, k):
+    """A result, the residual and a stranger's column side by side; the scales of the rows and of h in one buffer: bit for bit
+    what contiguous tensors give, and nothing else is written."""
+    rng = np.random.default_rng(m * 7 + n)
+    x, sx = (dev(a) for a in rows_of(rng, m, k))
+    gate, up = (M.QLinear(*(dev(a) for a in weight_of(rng, n, k))) for _ in range(2))
+    add = torch.randn(m, n, device="cuda") * 30
+    want = {t: torch.empty(m, n, dtype=t, device="cuda") for t in (torch.float32, torch.bfloat16)}
+    for y in want.values():
+        gate.matmul(x, sx, y, add=add)
+    hw = torch.empty(m, n, dtype=torch.uint8, device="cuda"), torch.empty(blocks(n), m, device="cuda")
+    M.QGated(gate, up).forward(x, sx, *hw)
+    for first in (0, n + 16):  # the result in front of the residual or behind it
+        for t, y0 in want.items():
+            buf = torch.full((m, 3 * n), 5.0, device="cuda")
+            other = n + 16 - first
+            buf[:, other:other + n] = add
+            size = 4 // t.itemsize
+            y = buf.view(t)[:, size * first:size * first + n]
+            before = buf.clone()
+            gate.matmul(x, sx, y, add=buf[:, other:other + n])
+            assert torch.equal(y, y0)
+            before.view(t)[:, size * first:size * first + n] = y0
+            assert torch.equal(buf, before)
+    scales = torch.full((max(blocks(k), blocks(n)), 2 * m + 3), 5.0, device="cuda")
+    scales[:blocks(k), :m] = sx
+    h = torch.empty_like(hw[0])
+    before = scales.clone()
+    M.QGated(gate, up).forward(x, scales[:blocks(k), :m], h, scales[:blocks(n), m + 1:2 * m + 1])
+    before[:blocks(n), m + 1:2 * m + 1] = hw[1]
+    assert torch.equal(h, hw[0]) and torch.equal(scales, before)
+    assert gate.check() == 0
