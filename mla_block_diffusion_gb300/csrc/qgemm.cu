@@ -414,7 +414,9 @@ static QlPlan plan(const QlParams &p) {
         return cudaFuncSetAttribute(qgemm_kernel<GATED, HALVES, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kQgSmem);
     });
     if (r.error != cudaSuccess) return r;
-    r.room = room(qgemm_kernel<GATED, HALVES, ADD>, 2, kQgThreads, kQgSmem);
+    r.error = room(qgemm_kernel<GATED, HALVES, ADD>, 2, kQgThreads, kQgSmem, &r.room);
+    if (r.error == cudaSuccess && r.room < 1) r.error = cudaErrorLaunchOutOfResources;  // no pair fits this device
+    if (r.error != cudaSuccess) return r;
     // us a block of k, from whole calls. Tiles of 256 against 128 outputs: 2112 x 7168, 256 rows 28.8 and 20.2, 4000 rows 54.9
     // and 65.7; 7168 x 14336, 512 rows 51.6 and 66.4; 12288 x 1536, 512 rows 20.3 and 18.2
     r.time = 4.f + (float)((r.tiles + r.room - 1) / r.room) * (1.f + p.KB * (HALVES == 2 ? 0.47f : 0.26f));
@@ -438,8 +440,9 @@ static cudaError_t launch(const QlParams &p, const dspark_qrows_t &x, const dspa
 QlPlan plan_qgemm(const QlParams &p, bool gated) {
     if (gated) return plan<true, 2, false>(p);
     const QlPlan wide = p.add ? plan<false, 2, true>(p) : plan<false, 2, false>(p);
+    if (wide.error != cudaSuccess) return wide;
     const QlPlan half = p.add ? plan<false, 1, true>(p) : plan<false, 1, false>(p);
-    return half.time < wide.time ? half : wide;
+    return half.error != cudaSuccess || half.time < wide.time ? half : wide;
 }
 cudaError_t launch_qgemm(const QlParams &p, bool gated, const dspark_qrows_t &x, const dspark_qweight_t &w0, const dspark_qweight_t &w1,
                          const QlPlan &plan, cudaStream_t st) {

@@ -331,8 +331,11 @@ static QlPlan plan(const QlParams &p) {
     // the clusters' sum costs more than it saves. us, whole and in clusters, 1 and 64 rows: 1024 outputs x 512 inputs 3.2 and
     // 4.9 against 3.8 and 6.2; x 1024 3.9 and 5.8 against (of two) 4.2 and 6.8; x 1536 4.7 and 6.6 against (of four) 3.9
     // and 6.5; 576 x 14336 25.0 and 29.5 against (of eight) 6.6 and 9.2.
-    for (int s = 2; s <= kQfMaxSplit && p.KB >= 12 && s <= p.KB / 3; ++s)
-        if (r.tiles <= room(qgemm_few_kernel<NT, GATED>, s, kQfThreads, C::kSmem)) r.split = s;
+    for (int s = 2, fit; s <= kQfMaxSplit && p.KB >= 12 && s <= p.KB / 3; ++s) {
+        r.error = room(qgemm_few_kernel<NT, GATED>, s, kQfThreads, C::kSmem, &fit);
+        if (r.error != cudaSuccess) return r;
+        if (r.tiles <= fit) r.split = s;
+    }
     return r;
 }
 

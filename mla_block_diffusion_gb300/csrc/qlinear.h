@@ -107,18 +107,20 @@ DS_DEVINL void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Clusters of `cluster` CTAs that fit on the current device at once; asked once per kernel, size and device.
+// Clusters of `cluster` CTAs that fit on the current device at once (0: it holds none); asked once per kernel, size and device,
+// and again where the question failed.
 template <typename Kernel>
 class ClusterRoom {
     static constexpr int kDevices = 64, kMost = 8;
-    std::atomic<int> known_[kDevices][kMost + 1] = {};
+    std::atomic<int> known_[kDevices][kMost + 1] = {};  // answer + 1
 
   public:
-    int operator()(Kernel kern, int cluster, int threads, int smem) {
-        int dev = 0, n = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    cudaError_t operator()(Kernel kern, int cluster, int threads, int smem, int *n) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
         const bool kept = dev >= 0 && dev < kDevices && cluster <= kMost;
-        if (kept && (n = known_[dev][cluster].load(std::memory_order_relaxed)) > 0) return n;
+        if (kept && (*n = known_[dev][cluster].load(std::memory_order_relaxed) - 1) >= 0) return cudaSuccess;
         carveout_max((const void *)kern);  // as every launch has it
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
@@ -130,12 +132,9 @@ class ClusterRoom {
         cfg.dynamicSmemBytes = smem;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
-            (void)cudaGetLastError();
-            n = 1;
-        }
-        if (kept) known_[dev][cluster].store(n, std::memory_order_relaxed);
-        return n;
+        e = cudaOccupancyMaxActiveClusters(n, kern, &cfg);
+        if (e == cudaSuccess && kept) known_[dev][cluster].store(*n + 1, std::memory_order_relaxed);
+        return e;
     }
 };
 
