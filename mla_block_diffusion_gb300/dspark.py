@@ -163,6 +163,16 @@ def _stream():
     return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
 
 
+def _workspace(size: int, device) -> torch.Tensor:
+    """A zero-filled workspace. It is waited for, as the first call may run on another stream than the one that fills it;
+    in a capture the fill belongs to the graph, which calls outside it have to follow."""
+    ws = torch.zeros(size, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream().synchronize()
+    return ws
+
+
 def _chk(fn: str, st: int):
     if st != 0:
         raise DSparkError(fn, st)
@@ -215,7 +225,7 @@ class DSpark:
         self.ws_bytes = L.dspark_workspace_bytes(h, max_bs, max_ctx)
         if self.ws_bytes == 0:
             raise DSparkError("dspark_workspace_bytes", 3)
-        self.ws = torch.zeros(self.ws_bytes, dtype=torch.uint8, device="cuda")
+        self.ws = _workspace(self.ws_bytes, "cuda")
 
     def close(self):
         if getattr(self, "h", None):
@@ -337,7 +347,7 @@ class QCache:
         if need == 0:
             raise DSparkError("dspark_qcache_workspace_bytes", 3)
         if workspace is None:
-            workspace = torch.zeros(need, dtype=torch.uint8, device=page_table.device)
+            workspace = _workspace(need, page_table.device)
         if workspace.dtype is not torch.uint8 or workspace.get_device() != self.dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{self.dev}, zero-filled before its first use")
         self.ws, self.ws_ptr, self.ws_bytes = workspace, C.c_void_p(workspace.data_ptr()), workspace.numel()
@@ -526,7 +536,7 @@ class QLinear:
         self.ref = C.byref(self.w)
         self._keep = (codes, scales)  # the struct holds raw device pointers
         if workspace is None:
-            workspace = torch.zeros(_QLINEAR_WS, dtype=torch.uint8, device=codes.device)
+            workspace = _workspace(_QLINEAR_WS, codes.device)
         if workspace.dtype is not torch.uint8 or workspace.get_device() != self.dev or not workspace.is_contiguous():
             raise ValueError(f"workspace: a contiguous uint8 tensor on cuda:{self.dev}, zero-filled before its first use")
         self.ws, self.ws_ptr, self.ws_bytes = workspace, C.c_void_p(workspace.data_ptr()), workspace.numel()
