@@ -200,12 +200,17 @@ constexpr int64_t kMaxStride = 1ll << 36;
 bool ok4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
 bool ok_dim(int d) { return d >= 16 && d <= DSPARK_QLINEAR_MAX_DIM && d % 16 == 0; }
 
+// SMs of the current device; 0: the runtime does not say.
 int current_sms() {
-    static int sms[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (!sms[dev] && cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return sms[dev];
+    constexpr int kDevices = 64;  // devices past these: asked on every call
+    static std::atomic<int> known[kDevices];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (kept) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 dspark_status done(cudaError_t e) {

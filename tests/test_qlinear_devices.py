@@ -133,3 +133,8 @@ def test_clusters_that_do_not_fit(lines):
     assert lines[9] == "many alone 5 grid 0 cluster 0"
     assert lines[10] == "few of three 0 grid 3 cluster 3"
     assert lines[11] == "few of three tiles 0 grid 3 cluster 1"
+
+
+def test_every_device_is_served(lines):
+    assert lines[12:19] == ["0 0 0 0"] * 7  # also those behind the 64 that answers are kept for
+    assert lines[19] == "launches 28"
