@@ -177,9 +177,11 @@ static cudaError_t launch_rows(const void *x, long long stride, const dspark_qro
     // Two blocks a half-warp for long calls of bf16, whose loads are half as long, else one. us, one against two, rows of
     // 7168: bf16, 7 rows 1.4 and 1.6, 512 3.1 and 2.9, 1024 5.0 and 4.0, 4000 18.6 and 15.2 (four 15.9); fp32, 1024 7.3
     // and 8.0, 4000 26.6 and 28.6.
-    if (sizeof(T) == 2 && (long long)rb * kb >= 20ll * sms)
-        return launch_pdl(quantise_rows_kernel<T, 2>, dim3(rb, (kb + 3) / 4), dim3(kQrThreads), 0, st, (const T *)x, stride,
-                          o.rows, o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
+    if constexpr (sizeof(T) == 2) {
+        if ((long long)rb * kb >= 20ll * sms)
+            return launch_pdl(quantise_rows_kernel<T, 2>, dim3(rb, (kb + 3) / 4), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
+                              o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
+    }
     return launch_pdl(quantise_rows_kernel<T, 1>, dim3(rb, (kb + 1) / 2), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
                       o.k, (uint8_t *)o.codes, o.scales, (long long)o.scale_stride);
 }

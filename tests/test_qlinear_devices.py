@@ -138,3 +138,10 @@ def test_clusters_that_do_not_fit(lines):
 def test_every_device_is_served(lines):
     assert lines[12:19] == ["0 0 0 0"] * 7  # also those behind the 64 that answers are kept for
     assert lines[19] == "launches 28"
+
+
+def test_every_kernel_of_the_library_is_launched():
+    """The quantiser of rows has one form for fp32, two for bf16."""
+    out = subprocess.run(["nm", "-C", B.build()], capture_output=True, text=True, check=True).stdout
+    forms = {line.split("quantise_rows_kernel<")[1].split(">")[0] for line in out.splitlines() if "quantise_rows_kernel<" in line}
+    assert forms == {"__nv_bfloat16, 1", "__nv_bfloat16, 2", "float, 1"}
