@@ -454,7 +454,8 @@ dspark_status dspark_qlinear_quantise_matrix(const void *w, int w_type, int64_t 
 
 /* (12) y = x w^T (+ add): for every block of 128 k the products of the codes are
  * summed in fp32 and enter an fp32 sum times sx * sw (one fp32 product of the two
- * scales, which has to be a normal number). y [rows, n], y_type DSPARK_ENTRY_BF16 or
+ * scales, which has to be zero or a normal number for the result to be exact to fp32:
+ * a subnormal one has fewer bits, an infinite one makes NaN of zero codes). y [rows, n], y_type DSPARK_ENTRY_BF16 or
  * _FP32; add, fp32 [rows, n] or null, is added before the one rounding and may be
  * y itself (fp32, the same stride); otherwise y overlaps no input. Strides count
  * elements (y: a multiple of 8 for bf16, 4 for fp32; add: of 4). Results do not
