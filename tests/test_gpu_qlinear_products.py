@@ -116,3 +116,61 @@ def test_columns_of_one_buffer(m, n, k):
     before[:blocks(n), m + 1:2 * m + 1] = hw[1]
     assert torch.equal(h, hw[0]) and torch.equal(scales, before)
     assert gate.check() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("m,k,n", [(1, 512, 1040), (7, 7168, 272), (64, 2112, 1024), (65, 1536, 4112), (700, 1040, 2064)])
+def test_feed_forward_chains(m, k, n, dtype):
+    """Quantise, gated product, down onto the residual, quantise again, each kernel beginning before the last has ended: the bits of
+    calls that are waited for, eager on two streams and replayed, for inputs that change between the passes."""
+    g = torch.Generator(device="cuda").manual_seed(m)
+
+    def linear(n, k):
+        codes, scales = torch.empty(n, k, dtype=torch.uint8, device="cuda"), torch.empty(blocks(n), blocks(k), device="cuda")
+        M.quantise_weight(torch.randn(n, k, device="cuda", generator=g) / k ** 0.5, codes, scales)
+        return M.QLinear(codes, scales)
+
+    class Chain:
+        def __init__(self):
+            self.x, self.y = torch.empty(m, k, dtype=dtype, device="cuda"), torch.empty(m, k, device="cuda")
+            self.q, self.h, self.z = ((torch.empty(m, w, dtype=torch.uint8, device="cuda"), torch.empty(blocks(w), m, device="cuda"))
+                                      for w in (k, n, k))
+
+        def run(self, source, wait=lambda: None):
+            self.x.copy_(source)
+            self.y.copy_(source)
+            for call in (lambda: M.quantise_rows(self.x, *self.q), lambda: gated.forward(*self.q, *self.h),
+                         lambda: down.matmul(*self.h, self.y, add=self.y), lambda: M.quantise_rows(self.y, *self.z)):
+                wait()
+                call()
+
+        def results(self):
+            return [t.clone() for t in (self.y, *self.z)]
+
+    gated, down = M.QGated(linear(n, k), linear(n, k)), linear(k, n)
+    sources = [torch.randn(m, k, device="cuda", generator=g).to(dtype) for _ in range(3)]
+    chain, want = Chain(), []
+    for s in sources:
+        chain.run(s, torch.cuda.synchronize)
+        torch.cuda.synchronize()
+        want.append(chain.results())
+    same = lambda a, b: all(torch.equal(p, q) for p, q in zip(a, b))  # noqa: E731
+    chains, streams = (Chain(), Chain()), (torch.cuda.Stream(), torch.cuda.Stream())
+    torch.cuda.synchronize()
+    got = []
+    for i in range(12):
+        for j in range(2):
+            with torch.cuda.stream(streams[j]):
+                chains[j].run(sources[(i + j) % 3])
+                got.append((chains[j].results(), (i + j) % 3))
+    torch.cuda.synchronize()
+    assert all(same(r, want[i]) for r, i in got)
+    source, graph = torch.empty_like(sources[0]), torch.cuda.CUDAGraph()
+    source.copy_(sources[0])
+    with torch.cuda.graph(graph):
+        chain.run(source)
+    for i in range(12):
+        source.copy_(sources[i % 3])
+        graph.replay()
+        assert same(chain.results(), want[i % 3])
+    assert gated.check() == 0 and down.check() == 0
