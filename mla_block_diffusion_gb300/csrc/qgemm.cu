@@ -12,9 +12,9 @@
 // FMAs. The accumulator's columns are the first CTA's 64 of the first half, its 64 of
 // the second, then the other CTA's, so that a warp's 128 columns have two factors.
 //
-// Bound: a block's products, followed by its sums (66 % of the tensor pipe, 62 % of the issue slots, gated product of 2048
-// rows), and power under a lasting load. Measured: 4000 x 8192 x 7168, bf16 result 181 us (2.6 PFLOP/s), fp32 with a
-// residual 223; gated 2900 x 7168 x 2 14336 440 us, for seconds on end 494 at 1.66 GHz. One CTA a tile of 128 x 256
+// Bound: a block's products, followed by its sums (63 % of the tensor pipe's time, 62 % of the issue slots, gated product of
+// 2048 rows), and power under a lasting load. Measured: 4000 x 8192 x 7168, bf16 result 175 us (2.7 PFLOP/s), fp32 with a
+// residual 223; gated 2900 x 7168 x 2 14336 426 us, for seconds on end 494 at 1.66 GHz. One CTA a tile of 128 x 256
 // took 319 us for the product with a residual.
 #include <math.h>
 

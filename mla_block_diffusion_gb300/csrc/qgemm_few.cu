@@ -2,7 +2,7 @@
 //
 // The same sums as in qgemm.cu with outputs on the accumulator's 128 lanes and the
 // rows (padded to NT = 16, 32 or 64) as its columns: the weights stream past the rows
-// once, one CTA an SM, through a ring of 200 KB. A tile is 128 outputs (gated: 128 of gate and
+// once, one CTA an SM, through a ring of 170 to 200 KB (128 to 176 KB of it weights). A tile is 128 outputs (gated: 128 of gate and
 // the same 128 of up, which have a scale in common). With fewer tiles than SMs, the up to eight
 // CTAs of a cluster share a tile's blocks of k, add their sums in rank order through
 // distributed shared memory, and each finishes some of the rows: nothing goes through
@@ -13,8 +13,8 @@
 // four groups of four warps take blocks in turn (gated: two groups for each matrix), each
 // with accumulators of its own in tensor memory and sums of its own in registers, which are
 // added in order at the end.
-// Measured (graphs, weights in turn): one row, 35840 x 7168 42.5 us (6.0 TB/s), gated 7168 x 2 14336 34.5 (6.0 TB/s),
-// 7168 x 2112 7.4; 64 rows 47.1, 38.3 and 10.0.
+// Measured (graphs, weights in turn): one row, 35840 x 7168 43.8 us (5.9 TB/s), gated 7168 x 2 14336 35.5 (5.8 TB/s),
+// 7168 x 2112 7.4; 64 rows 48.3, 39.9 and 10.0.
 #include <math.h>
 
 #include "per_device.h"
@@ -28,7 +28,7 @@ constexpr int kQfRegsIssue = 56, kQfRegsSum = 104, kQfRegs = 96;
 constexpr int kQfMaxStages = 12;
 constexpr int kQfMaxSplit = 8;                              // CTAs of a cluster
 constexpr int kQfWindow = 8, kQfWindows = 4;                // blocks of k whose scales arrive together, and such windows in shared memory
-constexpr int kQfRing = 200 * 1024;                         // stages
+constexpr int kQfRing = 200 * 1024;                         // stages: at most
 
 template <int NT, bool GATED>
 struct QfCfg {

@@ -17,7 +17,8 @@ namespace ds {
 // one rounding since 2^-e is a power of two. Bound: HBM (2 or 4 bytes read and
 // one written per element). A CTA takes 8 rows x 2 PER blocks, each half-warp PER
 // blocks that it requests together; the scales of 8 rows are one full sector of
-// their [block, row] matrix. Measured: 4000 x 7168 bf16 15.2 us in a graph, 16.9 through Python (5.1 TB/s), fp32 26.6.
+// their [block, row] matrix. Measured, inputs in turn: 4000 x 7168 bf16 17.4 us (5.0 TB/s, 63 % of the
+// issue slots), fp32 27.1 (5.3 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kQrThreads = 256, kQrRows = 8;
 
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kQrThreads, sizeof(T) == 2 ? 8 : 5) quantise_r
 }
 
 // The same over blocks of 128 x 128, one CTA each; the block waits in registers for its maximum.
-// Bound: HBM; 7168 x 14336 bf16 55.8 us, 5.5 TB/s.
+// Bound: HBM; 7168 x 14336 bf16 55.8 us (5.5 TB/s), fp32 107.9 (4.8 TB/s).
 constexpr int kQwThreads = 512;
 template <typename T>
 __global__ void __launch_bounds__(kQwThreads, sizeof(T) == 2 ? 3 : 2)
@@ -174,9 +175,9 @@ __global__ void __launch_bounds__(kQwThreads, sizeof(T) == 2 ? 3 : 2)
 template <typename T>
 static cudaError_t launch_rows(const void *x, long long stride, const dspark_qrows_t &o, int sms, cudaStream_t st) {
     const int kb = (o.k + kQlBlock - 1) / kQlBlock, rb = (o.rows + kQrRows - 1) / kQrRows;
-    // Two blocks a half-warp for long calls of bf16, whose loads are half as long, else one. us, one against two, rows of
-    // 7168: bf16, 7 rows 1.4 and 1.6, 512 3.1 and 2.9, 1024 5.0 and 4.0, 4000 18.6 and 15.2 (four 15.9); fp32, 1024 7.3
-    // and 8.0, 4000 26.6 and 28.6.
+    // Two blocks a half-warp for long calls of bf16, whose loads are half as long, else one. us, one against two, inputs in
+    // turn, rows of 7168: bf16, 7 rows 1.2 and 1.4, 256 2.7 and 3.4, 512 4.1 and 3.9, 1024 6.6 and 6.0, 4000 20.2 and 17.4;
+    // fp32, 1024 8.7 and 9.4, 4000 27.1 and 29.1.
     if constexpr (sizeof(T) == 2) {
         if ((long long)rb * kb >= 20ll * sms)
             return launch_pdl(quantise_rows_kernel<T, 2>, dim3(rb, (kb + 3) / 4), dim3(kQrThreads), 0, st, (const T *)x, stride, o.rows,
@@ -272,7 +273,9 @@ dspark_status quantise_matrix(const void *w, int type, int64_t stride, const dsp
 
 // Up to 64 rows the weights stream past the rows, above the rows are the tensor core's lanes. 64 rows, one against the
 // other, us: 12288 outputs x 576 inputs 5.4 and 9.3, 1808 x 720 6.1 and 7.1, 1024 x 512 4.9 and 6.3, 576 x 14336 9.2 and 33.1,
-// 14336 x 7168 21.2 and 30.2.
+// 14336 x 7168 21.2 and 30.2. What the rule does not know: with few outputs and long rows, where pairs of CTAs are idle,
+// calls of 64 rows each would be faster up to 192 rows (576 x 14336, us, as it is and in such calls: 65 rows 35.2 and
+// 16.1, 128 35.3 and 19.0, 192 34.9 and 27.9, 256 35.0 and 37.0).
 dspark_status product(const QlParams &p, bool gated, const dspark_qrows_t *x, const dspark_qweight_t *w0,
                       const dspark_qweight_t *w1, cudaStream_t st) {
     const QlPlan plan = p.M <= 64 ? plan_qgemm_few(p, gated) : plan_qgemm(p, gated);
