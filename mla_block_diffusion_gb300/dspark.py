@@ -499,14 +499,15 @@ def quantise_weight(w: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor):
     """w [n, k] (bf16 or fp32, any row stride) into E4M3 codes [n, k] and scales fp32 [ceil(n / 128), ceil(k / 128)], one
     power of two per block of 128 x 128; k is a multiple of 16, n any number (a product's: a multiple of 16)."""
     dev = torch._C._cuda_getDevice()
-    a = _qweight(codes, scales, dev)
+    a = _qblocks(codes, scales, dev)
     kind, stride = _qsource("w", w, codes.shape, dev)
-    st = lib().dspark_qlinear_quantise_matrix(w.data_ptr() or None, kind, stride, a.n, a.k, a.codes, a.scales, _stream())
+    st = lib().dspark_qlinear_quantise_matrix(w.data_ptr() or None, kind, stride, *a, _stream())
     if st:
         raise DSparkError("dspark_qlinear_quantise_matrix", st)
 
 
-def _qweight(codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QWeightStruct:
+def _qblocks(codes: torch.Tensor, scales: torch.Tensor, dev: int):
+    """Rows, inputs and addresses of a matrix with a scale for each block of 128 x 128."""
     if codes.dim() != 2 or codes.dtype not in _CODES or codes.get_device() != dev or not codes.is_contiguous():
         raise ValueError(f"codes: a contiguous uint8 or float8_e4m3fn tensor [n, k] on cuda:{dev}")
     n, k = codes.shape
@@ -514,7 +515,7 @@ def _qweight(codes: torch.Tensor, scales: torch.Tensor, dev: int) -> QWeightStru
     if (scales.dtype is not torch.float32 or scales.get_device() != dev or tuple(scales.shape) != want
             or not scales.is_contiguous()):
         raise ValueError(f"scales: a contiguous fp32 tensor {list(want)} on cuda:{dev}")
-    return QWeightStruct(n, k, codes.data_ptr() or None, scales.data_ptr() or None)
+    return n, k, codes.data_ptr() or None, scales.data_ptr() or None
 
 
 class QLinear:
@@ -530,7 +531,7 @@ class QLinear:
         self.dev = codes.get_device()
         if self.dev < 0:
             raise ValueError("codes: a CUDA tensor")
-        self.w = _qweight(codes, scales, self.dev)
+        self.w = QWeightStruct(*_qblocks(codes, scales, self.dev))
         if not 16 <= self.w.n <= 1 << 20 or not 16 <= self.w.k <= 1 << 20 or self.w.n % 16 or self.w.k % 16:
             raise ValueError("codes: n and k are multiples of 16 up to 2^20")
         self.ref = C.byref(self.w)
